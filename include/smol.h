@@ -377,6 +377,107 @@ int smol_append_kv(const smol_config *cfg, int B, const void *k_new, const void 
 int smol_sample(const void *logits, int B, int V, long long ld, float temperature, int top_k,
                 float top_p, int do_sample, const float *uniform, int32_t *next, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * A key/value cache in pages.  One pool of pages serves every sequence: a page
+ * holds page_size consecutive positions of one sequence, for every kv head of
+ * every layer, and a page table names the pages of each sequence in order.
+ * The pages and tables are the caller's; the library only reads the table.
+ *
+ *   position x of sequence b, layer l, kv head h lies at
+ *   pages[l][page_table[b][x / page_size]][h][x % page_size][0 .. head_dim)
+ *
+ *   kv_dtype SMOL_KV_BF16: bf16 values; the scales are NULL.
+ *   kv_dtype SMOL_KV_E4M3: 8-bit codes (e4m3, largest 448) with one fp32 scale
+ *            for each position and kv head, keys and values apart: the value
+ *            of a code is code * scale.
+ *   page_size  a power of two, 16 to 256.  head_dim 64 or 128.
+ *   max_pages  columns of the page table; max_pages * page_size <= 2^30.
+ * Entries of the table behind a sequence's last page are never used.  The same
+ * page may stand in several rows (a shared prefix) as long as no call writes it
+ * for one sequence while it is read for another. */
+enum { SMOL_KV_BF16 = 0, SMOL_KV_E4M3 = 1 };
+typedef struct smol_paged_cache {
+  void *k_pages, *v_pages;    /* device [n_layers, n_pages, n_kv_heads, page_size, head_dim] */
+  float *k_scale, *v_scale;   /* device [n_layers, n_pages, n_kv_heads, page_size] or NULL   */
+  const int32_t *page_table;  /* device [B, max_pages]                                        */
+  int kv_dtype, n_layers, n_pages, n_kv_heads, page_size, head_dim, max_pages;
+} smol_paged_cache;
+
+/* A chunk of rows for each of B sequences: row t of sequence b stands at
+ * position pos[b] + t of its cache.
+ *   T          the most rows that any sequence has (>= 1).
+ *   pos        device int32 [B].
+ *   row_start  device int32 [B + 1] or NULL.  Given: the sequences' rows lie one
+ *              behind the other in tensors of `rows` rows, sequence b's at
+ *              row_start[b] .. row_start[b + 1] - 1 (ascending; rows behind
+ *              row_start[B] are not touched).  NULL: tensors have a sequence
+ *              axis of B and a row axis of T.
+ *   n_new      device int32 [B] or NULL (with row_start NULL only): sequence b
+ *              has n_new[b] rows, 0 to T; NULL: all T.
+ * Values outside their range (a negative position or count, more than T rows, a
+ * position behind the table's last page, a page number outside [0, n_pages))
+ * touch no memory outside the buffers; the rows concerned are not written by
+ * smol_paged_append and smol_paged_read, and not defined (but recorded in the
+ * status word as SMOL_ERR_INPUT) by smol_paged_attention. */
+typedef struct smol_chunk {
+  int B, T;
+  const int32_t *pos, *row_start, *n_new;
+  long long rows;             /* with row_start: rows of the packed tensors */
+} smol_chunk;
+
+/* Rows of head_dim contiguous bf16 values at data + layer * l + seq * b +
+ * row * t + head * h (strides in elements, multiples of 8; with row_start the
+ * row index is row_start[b] + t and `seq` is not used; `layer` is not used by
+ * smol_paged_attention).  data 16-byte aligned. */
+typedef struct smol_rows {
+  void *data;
+  long long layer, seq, row, head;
+} smol_rows;
+
+/* ---------------------------------------------------------------------------
+ * smol_paged_append: writes a chunk's keys and values into the pages, for every
+ * layer of the cache (smol_append_kv's counterpart; the lengths are the
+ * caller's to advance, since drafted rows may yet be refused).
+ *   k_new, v_new   bf16 rows (as the forward calls return them, or packed).
+ * e4m3 pages: scale = max |x| / 448 over the row's head_dim values (fp32), codes
+ * are x / scale rounded to the nearest e4m3 (ties to even).  A row of zeros has
+ * scale 0; a row holding an infinity or NaN has scale NaN and reads back as NaN.
+ * bf16 pages: the values as they are.
+ * smol_paged_read: the reverse.  Row t of sequence b receives the values at
+ * position pos[b] + t, rounded to bf16 (exact for bf16 pages); rows at and
+ * behind a sequence's count are left as they were.  With pos = 0 and n_new =
+ * the lengths it lays sequences out as the dense caches of smol_decode_step.
+ * One kernel launch on `stream` each, no workspace.
+ * ------------------------------------------------------------------------- */
+int smol_paged_append(const smol_paged_cache *cache, const smol_chunk *chunk, const smol_rows *k_new,
+                      const smol_rows *v_new, void *stream);
+int smol_paged_read(const smol_paged_cache *cache, const smol_chunk *chunk, const smol_rows *k_out,
+                    const smol_rows *v_out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * smol_paged_attention: causal grouped-query attention of a chunk of new tokens
+ * over one layer of a paged cache that already holds them (append first).
+ *   out[b, t, h] = sum_j softmax_j(scale * q[b, t, h] . k[b, h / g, j]) v[b, h / g, j]
+ * over positions j <= p and, with window w > 0, j > p - w, where p = pos[b] + t
+ * and g = n_heads / n_kv_heads (1 to 8).  T = 1 is a decode step, T of a few a
+ * drafted continuation, large T a chunk of a prompt; sequences of all three may
+ * share a call.  A sequence with no rows costs and writes nothing.
+ *   layer    0 .. cache->n_layers - 1.
+ *   q, out   bf16 rows of n_heads heads; out must not overlap q or itself.
+ *   scale    of the scores; 0 means 1 / sqrt(head_dim).
+ *   ws       >= smol_paged_workspace_bytes(cache, n_heads, B, T) bytes, zeroed
+ *            once; calls that may run at the same time need one each.
+ * The values at the positions that a sequence's rows see have to be finite;
+ * what lies elsewhere in its pages (behind the last row, before every row's
+ * window) is never used, whatever it is.  Scores, sums and accumulators are
+ * fp32; the weights are rounded to bf16 for the product with the values.
+ * Repeated calls give the same bits.  B up to 4096.
+ * ------------------------------------------------------------------------- */
+size_t smol_paged_workspace_bytes(const smol_paged_cache *cache, int n_heads, int B, int T);
+int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_chunk *chunk, int n_heads,
+                         const smol_rows *q, const smol_rows *out, float scale, int window, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Reads (synchronising `stream`) and clears the workspace status word.
  * Returns SMOL_OK, SMOL_ERR_TIMEOUT (a bounded wait gave up), SMOL_ERR_RANGE
  * (a value beyond the f16 range), SMOL_ERR_INPUT (an input value out of

@@ -1,0 +1,98 @@
+// paged.cuh - declarations of the paged-cache kernels and the device-side reading
+// of their chunk and page table.
+#pragma once
+
+#include "common.cuh"
+#include "prims.cuh"
+
+namespace smol {
+
+// A layer's pages (or, for append and read, the first layer's and the strides
+// between layers in rows of head_dim values).
+struct PagedKv {
+  uint8_t *k, *v;              // [P, KV, page, hd] bf16 or e4m3
+  float *ks, *vs;              // [P, KV, page] (e4m3)
+  const int *table;            // [B, max_pages]
+  long long layer_rows;        // P * KV * page: rows of one layer
+  int P, KV, page_shift, max_pages, hd, e4m3;
+};
+
+struct PagedChunk {
+  int B, T;
+  const int *pos, *row_start, *n_new;
+  long long rows;
+};
+
+// Strided rows of heads, strides in elements (smol_rows).
+struct PagedRows {
+  uint8_t *data;
+  long long layer, seq, row, head;
+};
+
+// One sequence of a chunk as the kernels use it: clamped so that no index built
+// from it leaves the tables or the row tensors.
+struct PagedSeq {
+  int L;                       // position of its row 0
+  int n;                       // rows
+  long long row0;              // packed: index of its row 0 (0 otherwise)
+  bool bad;                    // a value was out of its range
+};
+
+__device__ __forceinline__ PagedSeq paged_seq(const PagedChunk &c, int b, int cap) {
+  PagedSeq s;
+  const int L = c.pos[b];
+  s.L = min(max(L, 0), cap);
+  s.bad = s.L != L;
+  long long n = c.T;
+  s.row0 = 0;
+  if (c.row_start) {
+    const long long a = c.row_start[b], e = c.row_start[b + 1];
+    s.row0 = min(max(a, 0ll), c.rows);
+    const long long end = min(max(e, s.row0), c.rows);
+    s.bad |= s.row0 != a || end != e;
+    n = end - s.row0;
+  } else if (c.n_new) {
+    n = c.n_new[b];
+  }
+  const long long most = min(c.T, cap - s.L);
+  s.n = static_cast<int>(min(max(n, 0ll), most));
+  s.bad |= s.n != n;
+  return s;
+}
+
+// The address offset (in elements) of row t, head h of sequence b.
+__device__ __forceinline__ long long paged_row_off(const PagedRows &r, const PagedChunk &c, const PagedSeq &s,
+                                                   int b, int t, int h) {
+  return (c.row_start ? 0 : b * r.seq) + (s.row0 + t) * r.row + h * r.head;
+}
+
+// Page of a position of sequence b (x < max_pages << page_shift); outside
+// [0, P): no such page.
+__device__ __forceinline__ int paged_page(const PagedKv &kv, int b, int x) {
+  return kv.table[static_cast<long long>(b) * kv.max_pages + (x >> kv.page_shift)];
+}
+
+// Row index (in units of head_dim values, within one layer) of position x of kv
+// head h on page `page`.
+__device__ __forceinline__ long long paged_slot(const PagedKv &kv, int page, int x, int h) {
+  return ((static_cast<long long>(page) * kv.KV + h) << kv.page_shift) + (x & ((1 << kv.page_shift) - 1));
+}
+
+cudaError_t launch_paged_append(const PagedKv &kv, int layers, const PagedChunk &c, const PagedRows &k,
+                                const PagedRows &v, cudaStream_t st);
+cudaError_t launch_paged_read(const PagedKv &kv, int layers, const PagedChunk &c, const PagedRows &k,
+                              const PagedRows &v, cudaStream_t st);
+
+struct PagedAttnParams {
+  PagedKv kv;
+  PagedChunk c;
+  PagedRows q, o;
+  int H, G;                    // query heads, query heads per kv head
+  float scale_log2;            // scale * log2(e)
+  int window;                  // > 0: position p sees j > p - window only
+  int *status;
+};
+size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T);
+cudaError_t launch_paged_attention(const PagedAttnParams &p, uint8_t *ws, int sms, cudaStream_t st, int *launches);
+
+}  // namespace smol

@@ -2,11 +2,13 @@
 // weight and workspace layouts, and the launch sequences of the block, model
 // and decode paths.  No entry point allocates, frees or synchronises (except
 // smol_workspace_status, which is documented as a synchronising query).
+#include <math.h>
 #include <stdio.h>
 #include <string.h>
 
 #include "common.cuh"
 #include "decode.cuh"
+#include "paged.cuh"
 #include "profile.cuh"
 
 using namespace smol;
@@ -736,6 +738,147 @@ SMOL_API int smol_sample(const void *logits, int B, int V, long long ld, float t
   LAUNCH_K(SMOL_K_SAMPLE, st, launch_sample(logits, ld, B, V, temperature, top_k, top_p, do_sample, uniform,
                                             reinterpret_cast<int *>(next), st));
   return SMOL_OK;
+}
+
+namespace {
+
+int check_paged(const smol_paged_cache *c) {
+  if (!c || !c->k_pages || !c->v_pages || !c->page_table) return SMOL_ERR_INVALID_ARG;
+  if (c->n_layers <= 0 || c->n_pages <= 0 || c->n_kv_heads <= 0 || c->max_pages <= 0) return SMOL_ERR_INVALID_ARG;
+  if (c->kv_dtype != SMOL_KV_BF16 && c->kv_dtype != SMOL_KV_E4M3) return SMOL_ERR_INVALID_ARG;
+  if (c->kv_dtype == SMOL_KV_E4M3 && (!c->k_scale || !c->v_scale)) return SMOL_ERR_INVALID_ARG;
+  if (c->head_dim != 64 && c->head_dim != 128) return SMOL_ERR_UNSUPPORTED_SHAPE;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return SMOL_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)c->max_pages * c->page_size > (1ll << 30) || c->n_kv_heads > 65535 || c->n_layers > 65535)
+    return SMOL_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
+    return SMOL_ERR_MISALIGNED;
+  return SMOL_OK;
+}
+
+int check_chunk(const smol_chunk *c) {
+  if (!c || !c->pos || c->B <= 0 || c->T <= 0 || (c->row_start && (c->n_new || c->rows < 0)))
+    return SMOL_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->pos) & 3u) || (reinterpret_cast<uintptr_t>(c->row_start) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->n_new) & 3u))
+    return SMOL_ERR_MISALIGNED;
+  // T rows of B sequences, or the packed rows, must be countable in an int
+  const long long rows = c->row_start ? c->rows : (long long)c->B * c->T;
+  return rows > 0x7fffffffLL ? SMOL_ERR_UNSUPPORTED_SHAPE : SMOL_OK;
+}
+
+// Rows of `heads` heads; `layers` > 1 when the layer stride is used.  Written
+// rows must not lie on one another.
+int check_rows(const smol_rows *r, const smol_chunk *c, int heads, int layers, int hd, bool written) {
+  if (!r || !r->data) return SMOL_ERR_INVALID_ARG;
+  if (!aligned16(r->data) || ((r->layer | r->seq | r->row | r->head) & 7)) return SMOL_ERR_MISALIGNED;
+  if (r->layer < 0 || r->seq < 0 || r->row < 0 || r->head < 0) return SMOL_ERR_INVALID_ARG;
+  if (written && ((heads > 1 && r->head < hd) || ((c->T > 1 || c->row_start) && r->row < hd) ||
+                  (layers > 1 && r->layer < hd) || (!c->row_start && c->B > 1 && r->seq < hd)))
+    return SMOL_ERR_INVALID_ARG;
+  return SMOL_OK;
+}
+
+PagedKv paged_kv(const smol_paged_cache *c, int layer) {
+  PagedKv p{};
+  p.P = c->n_pages;
+  p.KV = c->n_kv_heads;
+  p.page_shift = 31 - __builtin_clz((unsigned)c->page_size);
+  p.max_pages = c->max_pages;
+  p.hd = c->head_dim;
+  p.e4m3 = c->kv_dtype == SMOL_KV_E4M3;
+  p.layer_rows = (long long)c->n_pages * c->n_kv_heads * c->page_size;
+  const size_t row = (size_t)layer * p.layer_rows, bytes = (size_t)p.hd * (p.e4m3 ? 1 : 2);
+  p.k = static_cast<uint8_t *>(c->k_pages) + row * bytes;
+  p.v = static_cast<uint8_t *>(c->v_pages) + row * bytes;
+  p.ks = p.e4m3 ? c->k_scale + row : nullptr;
+  p.vs = p.e4m3 ? c->v_scale + row : nullptr;
+  p.table = c->page_table;
+  return p;
+}
+
+PagedChunk paged_chunk(const smol_chunk *c) { return PagedChunk{c->B, c->T, c->pos, c->row_start, c->n_new, c->rows}; }
+
+PagedRows paged_rows(const smol_rows *r) {
+  return PagedRows{static_cast<uint8_t *>(r->data), r->layer, r->seq, r->row, r->head};
+}
+
+int paged_copy(bool append, const smol_paged_cache *cache, const smol_chunk *chunk, const smol_rows *k,
+               const smol_rows *v, void *stream) {
+  g_launches = 0;
+  int rc = check_paged(cache);
+  if (!rc) rc = check_chunk(chunk);
+  if (!rc) rc = check_rows(k, chunk, cache->n_kv_heads, cache->n_layers, cache->head_dim, !append);
+  if (!rc) rc = check_rows(v, chunk, cache->n_kv_heads, cache->n_layers, cache->head_dim, !append);
+  if (rc) return rc;
+  int sms;
+  if ((rc = device_sms(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (chunk->row_start && chunk->rows == 0) return SMOL_OK;
+  LAUNCH((append ? launch_paged_append : launch_paged_read)(paged_kv(cache, 0), cache->n_layers, paged_chunk(chunk),
+                                                            paged_rows(k), paged_rows(v), st));
+  return SMOL_OK;
+}
+
+}  // namespace
+
+SMOL_API int smol_paged_append(const smol_paged_cache *cache, const smol_chunk *chunk, const smol_rows *k_new,
+                               const smol_rows *v_new, void *stream) {
+  return paged_copy(true, cache, chunk, k_new, v_new, stream);
+}
+
+SMOL_API int smol_paged_read(const smol_paged_cache *cache, const smol_chunk *chunk, const smol_rows *k_out,
+                             const smol_rows *v_out, void *stream) {
+  return paged_copy(false, cache, chunk, k_out, v_out, stream);
+}
+
+namespace {
+constexpr int kPagedMaxSeqs = 4096;   // sequences of one attention call (its schedule is held on chip)
+
+bool paged_heads_ok(const smol_paged_cache *c, int n_heads) {
+  return n_heads > 0 && n_heads % c->n_kv_heads == 0 && n_heads / c->n_kv_heads <= 8;
+}
+}  // namespace
+
+SMOL_API size_t smol_paged_workspace_bytes(const smol_paged_cache *cache, int n_heads, int B, int T) {
+  if (check_paged(cache) != SMOL_OK || B <= 0 || B > kPagedMaxSeqs || T <= 0 || !paged_heads_ok(cache, n_heads)) return 0;
+  return paged_attention_ws_bytes(cache->head_dim, n_heads, cache->n_kv_heads, B, T);
+}
+
+SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_chunk *chunk, int n_heads,
+                                  const smol_rows *q, const smol_rows *out, float scale, int window, void *ws,
+                                  size_t ws_bytes, void *stream) {
+  g_launches = 0;
+  int rc = check_paged(cache);
+  if (!rc) rc = check_chunk(chunk);
+  if (rc) return rc;
+  if (layer < 0 || layer >= cache->n_layers || n_heads <= 0 || window < 0 || !(scale >= 0.f) || !isfinite(scale) || !ws)
+    return SMOL_ERR_INVALID_ARG;
+  if (!paged_heads_ok(cache, n_heads) || chunk->B > kPagedMaxSeqs) return SMOL_ERR_UNSUPPORTED_SHAPE;
+  if (!(rc = check_rows(q, chunk, n_heads, 1, cache->head_dim, false)))
+    rc = check_rows(out, chunk, n_heads, 1, cache->head_dim, true);
+  if (rc) return rc;
+  if (!aligned16(ws)) return SMOL_ERR_MISALIGNED;
+  if (ws_bytes < paged_attention_ws_bytes(cache->head_dim, n_heads, cache->n_kv_heads, chunk->B, chunk->T))
+    return SMOL_ERR_WORKSPACE;
+  int sms;
+  if ((rc = device_sms(&sms))) return rc;
+  if (chunk->row_start && chunk->rows == 0) return SMOL_OK;
+  PagedAttnParams p{};
+  p.kv = paged_kv(cache, layer);
+  p.c = paged_chunk(chunk);
+  p.q = paged_rows(q);
+  p.o = paged_rows(out);
+  p.H = n_heads;
+  p.G = n_heads / cache->n_kv_heads;
+  p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)cache->head_dim));
+  p.window = window;
+  p.status = static_cast<int *>(ws);
+  int n = 0;
+  const cudaError_t e = launch_paged_attention(p, static_cast<uint8_t *>(ws), sms, static_cast<cudaStream_t>(stream), &n);
+  g_launches = n;
+  return e == cudaSuccess ? SMOL_OK : cuda_fail(e);
 }
 
 // The host status of a device status word: the first code any kernel wrote

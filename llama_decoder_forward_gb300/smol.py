@@ -29,6 +29,7 @@ ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE, ERR_TIMEOUT = -5, -6, -7, -8
 ERR_RANGE, ERR_INPUT = -9, -10
 OP_BLOCK, OP_MODEL, OP_DECODE = 1, 2, 3
 ACT_BF16, ACT_F32 = 0, 1
+KV_BF16, KV_E4M3 = 0, 1
 
 
 class Config(ctypes.Structure):
@@ -49,7 +50,23 @@ class ModelWeights(ctypes.Structure):
     _fields_ = [("layers", POINTER(BlockWeights)), ("embed", c_void_p), ("final_norm", c_void_p)]
 
 
+class _PagedCacheStruct(ctypes.Structure):
+    _fields_ = ([(k, c_void_p) for k in ("k_pages", "v_pages", "k_scale", "v_scale", "page_table")]
+                + [(k, c_int) for k in ("kv_dtype", "n_layers", "n_pages", "n_kv_heads", "page_size", "head_dim",
+                                        "max_pages")])
+
+
+class _ChunkStruct(ctypes.Structure):
+    _fields_ = [("B", c_int), ("T", c_int), ("pos", c_void_p), ("row_start", c_void_p), ("n_new", c_void_p),
+                ("rows", ctypes.c_longlong)]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", c_void_p)] + [(k, ctypes.c_longlong) for k in ("layer", "seq", "row", "head")]
+
+
 _CFG = POINTER(Config)
+_PC, _CK, _RW = POINTER(_PagedCacheStruct), POINTER(_ChunkStruct), POINTER(_Rows)
 _SIGS = {
     "smol_packed_bytes": (c_size_t, [_CFG, c_int, c_int]),
     "smol_prepare_weights": (c_int, [_CFG, POINTER(ModelWeights), c_int, c_void_p, c_size_t, c_void_p]),
@@ -81,6 +98,11 @@ _SIGS = {
                                         c_int, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "smol_sample": (c_int, [c_void_p, c_int, c_int, ctypes.c_longlong, c_float, c_int, c_float, c_int,
                             c_void_p, c_void_p, c_void_p]),
+    "smol_paged_append": (c_int, [_PC, _CK, _RW, _RW, c_void_p]),
+    "smol_paged_read": (c_int, [_PC, _CK, _RW, _RW, c_void_p]),
+    "smol_paged_workspace_bytes": (c_size_t, [_PC, c_int, c_int, c_int]),
+    "smol_paged_attention": (c_int, [_PC, c_int, _CK, c_int, _RW, _RW, c_float, c_int, c_void_p, c_size_t,
+                                     c_void_p]),
     "smol_profile_begin": (c_int, [ctypes.c_uint, c_int]),
     "smol_profile_end": (c_int, [POINTER(c_int), POINTER(c_float), c_int]),
 }
@@ -364,6 +386,146 @@ def sample(logits: torch.Tensor, next_ids: torch.Tensor, uniform: Optional[torch
     _check(_lib.smol_sample(_p(logits), B, V, logits.stride(0), float(temperature), int(top_k),
                             float(top_p), int(bool(do_sample)), _p(uniform), _p(next_ids),
                             _stream(stream)), "smol_sample")
+
+
+class PagedCache:
+    """Descriptor of a key/value cache in pages (the tensors stay the caller's).
+
+    k_pages, v_pages  [n_layers, n_pages, n_kv_heads, page_size, head_dim], bf16 or float8_e4m3fn
+    page_table        int32 [B, max_pages]
+    k_scale, v_scale  fp32 [n_layers, n_pages, n_kv_heads, page_size] with float8_e4m3fn pages
+    """
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, k_scale=None,
+                 v_scale=None):
+        dtype = k_pages.dtype
+        if dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+            raise ValueError("pages must be bfloat16 or float8_e4m3fn")
+        _dev(k_pages, dtype, "k_pages")
+        _dev(v_pages, dtype, "v_pages")
+        _dev(page_table, torch.int32, "page_table")
+        if k_pages.dim() != 5 or v_pages.shape != k_pages.shape or page_table.dim() != 2:
+            raise ValueError("pages must be [n_layers, n_pages, n_kv_heads, page_size, head_dim], page_table [B, max_pages]")
+        self.e4m3 = dtype == torch.float8_e4m3fn
+        if self.e4m3:
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or t.shape != k_pages.shape[:-1]:
+                    raise ValueError(f"{name} must be [n_layers, n_pages, n_kv_heads, page_size] with float8_e4m3fn pages")
+                _dev(t, torch.float32, name)
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("bfloat16 pages have no scales")
+        self.tensors = (k_pages, v_pages, page_table, k_scale, v_scale)   # kept alive with the descriptor
+        self.device = k_pages.device
+        if any(t is not None and t.device != self.device for t in self.tensors):
+            raise ValueError("pages, scales and page_table must be on one device")
+        self.n_layers, self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = k_pages.shape
+        self.n_seqs, self.max_pages = page_table.shape
+        self.struct = _PagedCacheStruct(k_pages.data_ptr(), v_pages.data_ptr(),
+                                        k_scale.data_ptr() if self.e4m3 else None,
+                                        v_scale.data_ptr() if self.e4m3 else None, page_table.data_ptr(),
+                                        KV_E4M3 if self.e4m3 else KV_BF16, self.n_layers, self.n_pages,
+                                        self.n_kv_heads, self.page_size, self.head_dim, self.max_pages)
+        self.ref = ctypes.byref(self.struct)
+
+
+class Chunk:
+    """Descriptor of a chunk of rows: row t of sequence b stands at position pos[b] + t.
+
+    B, T       sequences, and the most rows that any has
+    pos        int32 [B]
+    row_start  int32 [B + 1]: the row tensors are packed, [rows, heads, head_dim], sequence b's rows at
+               row_start[b] .. row_start[b + 1] - 1; None: they are [B, T, heads, head_dim]
+    n_new      int32 [B] or None: rows of each sequence, without row_start (None: T)
+    """
+
+    def __init__(self, B: int, T: int, pos: torch.Tensor, row_start: Optional[torch.Tensor] = None,
+                 n_new: Optional[torch.Tensor] = None):
+        for name, t, n in (("pos", pos, B), ("row_start", row_start, B + 1), ("n_new", n_new, B)):
+            if t is not None:
+                _dev(t, torch.int32, name)
+                if t.shape != (n,) or t.device != pos.device:
+                    raise ValueError(f"{name} must be [{n}], on the device of pos")
+        if row_start is not None and n_new is not None:
+            raise ValueError("row_start and n_new exclude each other")
+        self.tensors = (pos, row_start, n_new)
+        self.B, self.T, self.packed, self.device = B, T, row_start is not None, pos.device
+        self._fields = (B, T, pos.data_ptr(), None if row_start is None else row_start.data_ptr(),
+                        None if n_new is None else n_new.data_ptr())
+        self._ref = ctypes.byref(_ChunkStruct(*self._fields, 0))
+
+    def ref(self, rows: int):
+        """The C descriptor; of a packed chunk a new one, for tensors of `rows` rows."""
+        return ctypes.byref(_ChunkStruct(*self._fields, rows)) if self.packed else self._ref
+
+
+def _rows(t: torch.Tensor, name: str, cache: PagedCache, chunk: Chunk, heads: int, layers: bool) -> _Rows:
+    """bf16 rows [(layers,) B, T, heads, head_dim], or [(layers,) rows, heads, head_dim] of a packed chunk."""
+    shape, strides = t.shape, t.stride()
+    lead = 1 if layers else 0
+    if t.dtype != torch.bfloat16 or t.device != cache.device or strides[-1] != 1:
+        raise ValueError(f"{name} must be bfloat16 on the cache's device, its last axis contiguous")
+    if layers and shape[0] != cache.n_layers:
+        raise ValueError(f"{name} must have a first axis of {cache.n_layers} layers")
+    if shape[lead + (1 if chunk.packed else 2):] != (heads, cache.head_dim) or (
+            not chunk.packed and shape[lead:lead + 2] != (chunk.B, chunk.T)):
+        raise ValueError(f"{name}: {tuple(shape)} does not fit the chunk ({heads} heads of {cache.head_dim}, "
+                         f"{'packed rows' if chunk.packed else (chunk.B, chunk.T)})")
+    # the strides of axes of one entry say nothing (torch may give them any value)
+    st = [s if n > 1 else cache.head_dim for s, n in zip(strides[lead:-1], shape[lead:-1])]
+    seq = 0 if chunk.packed else st[0]
+    return _Rows(t.data_ptr(), strides[0] if layers and shape[0] > 1 else (cache.head_dim if layers else 0), seq, st[-2],
+                 st[-1])
+
+
+def _same_place(cache: PagedCache, chunk: Chunk) -> None:
+    if chunk.device != cache.device or cache.device.index != torch.cuda.current_device():
+        raise ValueError("the cache, the chunk and the current device must be the same")
+    if chunk.B > cache.n_seqs:
+        raise ValueError(f"{chunk.B} sequences, and {cache.n_seqs} rows of the page table")
+
+
+def _paged_copy(fn, where, cache, chunk, k, v, names, stream):
+    _same_place(cache, chunk)
+    kr = _rows(k, names[0], cache, chunk, cache.n_kv_heads, True)
+    vr = _rows(v, names[1], cache, chunk, cache.n_kv_heads, True)
+    if k.shape != v.shape:
+        raise ValueError(f"{names[0]} and {names[1]} must have the same rows")
+    _check(fn(cache.ref, chunk.ref(k.shape[1]), ctypes.byref(kr), ctypes.byref(vr), _stream(stream)), where)
+
+
+def paged_append(cache: PagedCache, chunk: Chunk, k_new: torch.Tensor, v_new: torch.Tensor, stream=None) -> None:
+    """Writes a chunk's keys and values, [n_layers, B, T, n_kv_heads, head_dim] (any strides but the last) or
+    [n_layers, rows, n_kv_heads, head_dim] packed, into the pages; e4m3 pages quantise them."""
+    _paged_copy(_lib.smol_paged_append, "smol_paged_append", cache, chunk, k_new, v_new, ("k_new", "v_new"), stream)
+
+
+def paged_read(cache: PagedCache, chunk: Chunk, k_out: torch.Tensor, v_out: torch.Tensor, stream=None) -> None:
+    """The reverse of paged_append: the values at the chunk's positions into bf16 rows of the same layouts.
+    `cache.transpose(2, 3)` of a dense [n_layers, B, n_kv_heads, S, head_dim] cache is such a layout."""
+    _paged_copy(_lib.smol_paged_read, "smol_paged_read", cache, chunk, k_out, v_out, ("k_out", "v_out"), stream)
+
+
+def alloc_paged_workspace(cache: PagedCache, n_heads: int, B: int, T: int) -> torch.Tensor:
+    n = _lib.smol_paged_workspace_bytes(cache.ref, n_heads, B, T)
+    if n == 0:
+        raise SmolError(ERR_UNSUPPORTED_SHAPE, "smol_paged_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def paged_attention(cache: PagedCache, layer: int, chunk: Chunk, q: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                    scale: float = 0.0, window: int = 0, stream=None) -> None:
+    """Causal grouped-query attention of a chunk of new tokens, already appended, over one layer of the cache.
+    q, out: [B, T, n_heads, head_dim] or [rows, n_heads, head_dim] packed, bf16; scale 0: 1 / sqrt(head_dim)."""
+    _same_place(cache, chunk)
+    heads = q.shape[-2]
+    qr = _rows(q, "q", cache, chunk, heads, False)
+    orr = _rows(out, "out", cache, chunk, heads, False)
+    if q.shape != out.shape:
+        raise ValueError("q and out must have the same rows")
+    if ws.device != cache.device:
+        raise ValueError("ws must be on the cache's device")
+    _check(_lib.smol_paged_attention(cache.ref, layer, chunk.ref(q.shape[0]), heads, ctypes.byref(qr), ctypes.byref(orr), scale,
+                                     window, ws.data_ptr(), ws.numel(), _stream(stream)), "smol_paged_attention")
 
 
 def set_wait_limit_ns(ns: int) -> None:
