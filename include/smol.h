@@ -478,6 +478,47 @@ int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_ch
                          const smol_rows *q, const smol_rows *out, float scale, int window, void *ws,
                          size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * smol_verify_drafts: which of a sequence's drafted tokens stay, and its next
+ * token, from the target's logits and the caller's random numbers.
+ *   With p_i the target's distribution in row i (the softmax of logits /
+ *   temperature over what top_k and top_p leave, as in smol_sample) and q_i the
+ *   drafter's: draft i = 0, 1, ... stays while u_i * q_i(draft_i) < p_i(draft_i).
+ *   At the first that does not, the next token is drawn from max(p_i - q_i, 0)
+ *   (from p_i where nothing is left of that); where all n stay, from p_n.  A draw
+ *   is the first index, in vocabulary order, at which the running sum exceeds u
+ *   times the whole.  So accepted drafts and next token are distributed as the
+ *   target's own tokens.  Greedy (do_sample == 0 or temperature <= 0): draft i
+ *   stays while it is the first index of row i's maximum, and that index of the
+ *   last row looked at is the next token.
+ *   logits      device bf16, row i of sequence b (i = 0 .. T: the distribution of
+ *               the token at draft i's place, the last one behind all drafts) at
+ *               (b * (T + 1) + i) * ld; rows of V values, -infinity for a token
+ *               that cannot be.  A row whose largest value is NaN or infinite
+ *               keeps no draft and gives next = -1 (SMOL_ERR_INPUT).
+ *   drafts      device int32 [B, T]; one outside [0, V) does not stay
+ *               (SMOL_ERR_INPUT).
+ *   n_draft     device int32 [B] or NULL: sequence b has n = n_draft[b] drafts, 0
+ *               to T (clamped, SMOL_ERR_INPUT), and its last row is row n; NULL: T.
+ *   draft_probs device fp32 or NULL, q_i of sequence b at (b * T + i) * ld_probs;
+ *               NULL: a drafter that chooses its token for certain (q = 1).
+ *   uniform     device fp32 [B, T + 1] in [0, 1): column i for draft i, the last
+ *               one for the next token (may be NULL when greedy).
+ *   n_accepted  device int32 [B] output.       next  device int32 [B] output.
+ *   p_draft     device fp32 [B, T] output or NULL: p_i(draft_i), 0 behind a
+ *               sequence's drafts.
+ *   ws          >= smol_verify_workspace_bytes(B, T) bytes, zeroed once.
+ * Probabilities are held to about 2^-43 of the row's largest and summed exactly
+ * (a token below 2^-45 of the largest counts as impossible), so the choice is
+ * the definition's except where u lies within 1e-11 of a border.
+ * V <= 2^19.  Two kernel launches on `stream`.
+ * ------------------------------------------------------------------------- */
+size_t smol_verify_workspace_bytes(int B, int T);
+int smol_verify_drafts(const void *logits, long long ld, const int32_t *drafts, const int32_t *n_draft,
+                       const float *draft_probs, long long ld_probs, int B, int T, int V, float temperature,
+                       int top_k, float top_p, int do_sample, const float *uniform, int32_t *n_accepted,
+                       int32_t *next, float *p_draft, void *ws, size_t ws_bytes, void *stream);
+
 /* Reads (synchronising `stream`) and clears the workspace status word.
  * Returns SMOL_OK, SMOL_ERR_TIMEOUT (a bounded wait gave up), SMOL_ERR_RANGE
  * (a value beyond the f16 range), SMOL_ERR_INPUT (an input value out of

@@ -6,10 +6,13 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 #include "decode.cuh"
 #include "paged.cuh"
 #include "profile.cuh"
+#include "verify.cuh"
 
 using namespace smol;
 
@@ -877,6 +880,56 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
   p.status = static_cast<int *>(ws);
   int n = 0;
   const cudaError_t e = launch_paged_attention(p, static_cast<uint8_t *>(ws), sms, static_cast<cudaStream_t>(stream), &n);
+  g_launches = n;
+  return e == cudaSuccess ? SMOL_OK : cuda_fail(e);
+}
+
+SMOL_API size_t smol_verify_workspace_bytes(int B, int T) {
+  if (B <= 0 || T <= 0 || ((long long)T + 1) * B > (1 << 24)) return 0;
+  return 1024 + sizeof(VerifyRow) * (size_t)B * ((size_t)T + 1);
+}
+
+SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t *drafts, const int32_t *n_draft,
+                                const float *draft_probs, long long ld_probs, int B, int T, int V,
+                                float temperature, int top_k, float top_p, int do_sample, const float *uniform,
+                                int32_t *n_accepted, int32_t *next, float *p_draft, void *ws, size_t ws_bytes,
+                                void *stream) {
+  g_launches = 0;
+  const bool greedy = !do_sample || !(temperature > 0.f);
+  if (!logits || !drafts || !n_accepted || !next || !ws || (!greedy && !uniform)) return SMOL_ERR_INVALID_ARG;
+  if (B < 1 || T < 1 || V < 1 || ld < V || (draft_probs && ld_probs < V) || temperature != temperature ||
+      top_p != top_p || (!greedy && !isfinite(temperature)))
+    return SMOL_ERR_INVALID_ARG;
+  if (V > (1 << 19) || smol_verify_workspace_bytes(B, T) == 0) return SMOL_ERR_UNSUPPORTED_SHAPE;
+  uintptr_t words = 0;
+  for (const void *q : {(const void *)drafts, (const void *)n_draft, (const void *)draft_probs, (const void *)uniform,
+                        (const void *)n_accepted, (const void *)next, (const void *)p_draft})
+    words |= reinterpret_cast<uintptr_t>(q);
+  if ((words & 3u) || (reinterpret_cast<uintptr_t>(logits) & 1u) || !aligned16(ws)) return SMOL_ERR_MISALIGNED;
+  if (ws_bytes < smol_verify_workspace_bytes(B, T)) return SMOL_ERR_WORKSPACE;
+  int sms;
+  const int rc = device_sms(&sms);
+  if (rc) return rc;
+  VerifyParams p{};
+  p.logits = static_cast<const uint16_t *>(logits);
+  p.ld = ld;
+  p.drafts = drafts;
+  p.n_draft = n_draft;
+  p.probs = greedy ? nullptr : draft_probs;
+  p.ldq = ld_probs;
+  p.B = B; p.T = T; p.V = V;
+  p.temperature = temperature;
+  p.top_p = top_p > 0.f ? top_p : 0.f;   // as in smol_sample: the first token in descending order
+  p.top_k = top_k;
+  p.greedy = greedy;
+  p.uniform = uniform;
+  p.n_accepted = n_accepted;
+  p.next = next;
+  p.p_draft = p_draft;
+  p.status = static_cast<int *>(ws);
+  p.rows = reinterpret_cast<VerifyRow *>(static_cast<uint8_t *>(ws) + 1024);
+  int n = 0;
+  const cudaError_t e = launch_verify(p, static_cast<cudaStream_t>(stream), &n);
   g_launches = n;
   return e == cudaSuccess ? SMOL_OK : cuda_fail(e);
 }

@@ -1,0 +1,618 @@
+// verify.cu - verification of drafted tokens against the target's probabilities.
+//
+// p_i is the target's distribution after the tokens before draft i: the softmax
+// of logits / temperature over what top-k and top-p leave (the rules of
+// sample.cu), q_i the drafter's.  Draft x_i stays iff u_i q_i(x_i) < p_i(x_i); at
+// the first that does not, the next token is drawn from max(p_i - q_i, 0), and
+// from the row behind the drafts where all stay: then the tokens are distributed
+// as the target's own.  The draw is the first index in vocabulary order at which
+// the running sum exceeds u times the whole.
+//
+// Exactness.  A row of 50,000 or more running sums has a border within 1e-7 of u
+// once in a hundred draws, so fp32 sums would pick another token than the
+// definition.  Here a token's mass is e = 2^((l - l_max) log2(e) / temperature) as
+// an integer in units of 2^-44, from an exponential good to about 2^-43 (mass_of),
+// and every sum is a 64-bit integer: exact, and the same in any order.  The
+// borders are then off by less than 1e-11 of the whole.
+//
+// Two launches.
+//   rows    one CTA of 1024 threads for each target row.  The row is read once,
+//           into registers (up to 65,536 tokens; what is longer is read again
+//           from L2).  bf16 logits take few distinct values, so the row becomes
+//           a histogram over the values (32,768 counters: the values >= 0, then
+//           those < 0) and the exponential is taken once for each value that
+//           occurs: a tenth of the row and less.  The sum, the k-th largest
+//           value and the top-p cut are prefix sums over the histogram.
+//   choice  one cluster of eight CTAs for each sequence: the acceptances, then
+//           the draw over one row, an eighth of the vocabulary for each CTA.
+#include <math.h>
+
+#include "common.cuh"
+#include "prims.cuh"
+#include "profile.cuh"
+#include "verify.cuh"
+
+namespace smol {
+namespace {
+
+typedef unsigned long long u64;
+
+constexpr int kRowThreads = 1024;
+constexpr int kKeep = 8;             // chunks of 8 tokens a thread keeps in registers
+constexpr int kBins = 32768;         // values of one sign
+constexpr int kBinRows = kBins / 32;
+constexpr int kChoiceThreads = 512;
+constexpr int kChoiceCtas = 8;
+constexpr float kMinLog2 = -45.f;    // 2^x below half a unit of 2^-44 counts as 0
+
+// ---------------------------------------------------------------- masses
+// 2^(j / 256), j = -128 .. 128, in units of 2^-62: from 2^-0.5 by products with
+// 2^(1/256), each rounded at 2^-63 (off by 2^-55 at most).
+struct Pow2Table {
+  u64 v[257];
+  constexpr Pow2Table() : v() {
+    unsigned __int128 x = 0x5a827999fcef3242ull;               // 2^-0.5 in units of 2^-63
+    for (int j = 0; j < 257; ++j) {
+      v[j] = static_cast<u64>((x + 1) >> 1);
+      // 2^(1/256) - 1 in units of 2^-63
+      x += (x * 0x0058d7d2d5e5f6b1ull + (static_cast<unsigned __int128>(1) << 62)) >> 63;
+    }
+  }
+};
+__device__ constexpr Pow2Table kPow2{};
+
+// Exponentials of one row: y = (l - l_max) * c with c = log2(e) / temperature.
+struct MassCtx {
+  float lmax, c_hi, c_lo;
+  const u64 *table;                  // kPow2 in shared memory
+};
+
+__device__ __forceinline__ MassCtx mass_ctx(float lmax, float temperature, const u64 *table) {
+  const double c = 1.4426950408889634 / static_cast<double>(temperature);
+  MassCtx m;
+  m.lmax = lmax;
+  m.c_hi = static_cast<float>(c);
+  m.c_lo = static_cast<float>(c - static_cast<double>(m.c_hi));
+  m.table = table;
+  return m;
+}
+
+// round(2^44 * 2^y): the difference and the product are carried as sums of two
+// floats (Dekker's and Knuth's exact sums and products), y is split into a whole
+// number, 256ths from the table and a remainder r, |r| <= 2^-9, whose 2^r - 1 is
+// a short series (Tang's table-driven exponential): the leading term in two
+// floats, the others below 2^-18 in one.
+__device__ __forceinline__ u64 mass_of(const MassCtx &m, float l) {
+  const float dh = __fsub_rn(l, m.lmax);
+  const float yh = __fmul_rn(dh, m.c_hi);
+  if (!(yh >= kMinLog2)) return dh == 0.f ? 1ull << 44 : 0;           // also -inf and NaN
+  const float bb = __fsub_rn(dh, l);
+  const float dl = __fsub_rn(__fsub_rn(l, __fsub_rn(dh, bb)), __fadd_rn(m.lmax, bb));
+  const float yl = __fadd_rn(__fmaf_rn(dh, m.c_hi, -yh), __fmaf_rn(dh, m.c_lo, __fmul_rn(dl, m.c_hi)));
+  const float n = rintf(yh);
+  const float f = __fsub_rn(yh, n);
+  const float j = rintf(f * 256.f);
+  const float f2 = __fmaf_rn(j, -0.00390625f, f);
+  const float rh = __fadd_rn(f2, yl);
+  const float rb = __fsub_rn(rh, f2);
+  const float rl = __fadd_rn(__fsub_rn(f2, __fsub_rn(rh, rb)), __fsub_rn(yl, rb));
+  // ln 2 as a sum of two floats
+  constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654299957768e-9f;
+  const float ph = __fmul_rn(rh, kLn2Hi);
+  const float pl = __fadd_rn(__fmaf_rn(rh, kLn2Hi, -ph), __fmaf_rn(rh, kLn2Lo, __fmul_rn(rl, kLn2Hi)));
+  // ln2^2 / 2, ln2^3 / 6, ln2^4 / 24
+  const float s = __fmaf_rn(__fmaf_rn(rh, 0.009618129107628f, 0.055504108664822f), rh, 0.240226506959101f);
+  const float rest = __fmaf_rn(__fmul_rn(rh, rh), s, pl);
+  // 2^r - 1 in units of 2^-62 (below 2^54 in magnitude)
+  const long long w = __float2ll_rn(ph * 4611686018427387904.f) + __float2ll_rn(rest * 4611686018427387904.f);
+  const u64 t = m.table[static_cast<int>(j) + 128];
+  const u64 e = t + (static_cast<u64>(__mul64hi(static_cast<long long>(t), w)) << 2);
+  const int shift = 18 - static_cast<int>(n);                         // 18 .. 63
+  return (e + (1ull << (shift - 1))) >> shift;
+}
+
+// floor(q * z) for z < 2^63 (a q that is negative or NaN counts as 0, one of 2 or
+// more as just under 2).
+__device__ __forceinline__ u64 scaled_floor(float q, u64 z) {
+  if (!(q > 0.f)) return 0;
+  const uint32_t bits = min(__float_as_uint(q), 0x3fffffffu);
+  const int ex = static_cast<int>(bits >> 23);
+  const u64 man = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
+  const int s = 150 - max(ex, 1);                                     // q = man * 2^-s, s >= 23
+  const u64 lo = man * z, hi = __umul64hi(man, z);
+  if (s >= 64) return s >= 128 ? 0 : hi >> (s - 64);
+  return (hi << (64 - s)) | (lo >> s);
+}
+
+// ---------------------------------------------------------------- rows in chunks
+// A row of V bf16 as chunks of eight tokens whose 16 bytes are aligned: chunk c
+// holds the tokens base + 8 c .. + 7, base in (-8, 0].  Tokens outside the row
+// read as -infinity (mass 0, below every other value).
+struct Row {
+  const uint16_t *p;
+  int V, base, chunks;
+};
+
+__device__ __forceinline__ Row make_row(const uint16_t *p, int V) {
+  Row r;
+  r.p = p;
+  r.V = V;
+  const int past = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) >> 1);   // tokens past a 16-byte border
+  r.base = -past;
+  r.chunks = (V + past + 7) >> 3;
+  return r;
+}
+
+__device__ __forceinline__ uint4 load_chunk(const Row &r, int c) {
+  const int i = r.base + 8 * c;
+  if (i >= 0 && i + 8 <= r.V) return *reinterpret_cast<const uint4 *>(r.p + i);
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int a = i + 2 * e;
+    const uint32_t lo = a >= 0 && a < r.V ? r.p[a] : 0xff80u, hi = a + 1 >= 0 && a + 1 < r.V ? r.p[a + 1] : 0xff80u;
+    w[e] = lo | (hi << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint32_t chunk_bits(const uint4 &c, int e) {
+  const uint32_t w = (e >> 1) == 0 ? c.x : (e >> 1) == 1 ? c.y : (e >> 1) == 2 ? c.z : c.w;
+  return (w >> ((e & 1) * 16)) & 0xffffu;
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {
+  const uint32_t bits = (key & 0x8000u) ? key & 0x7fffu : ~key & 0xffffu;
+  return __uint_as_float(bits << 16);
+}
+
+// ---------------------------------------------------------------- block sums
+template <int THREADS>
+__device__ __forceinline__ u64 block_scan(u64 v, u64 *sh, u64 *total) {   // exclusive
+  constexpr int W = THREADS / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  u64 inc = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) sh[warp] = inc;
+  __syncthreads();
+  if (warp == 0) {
+    const u64 w = lane < W ? sh[lane] : 0;
+    u64 wi = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 t = __shfl_up_sync(0xffffffffu, wi, o);
+      if (lane >= o) wi += t;
+    }
+    if (lane < W) sh[lane] = wi - w;
+    if (lane == 31) sh[32] = wi;
+  }
+  __syncthreads();
+  const u64 before = sh[warp];
+  *total = sh[32];
+  __syncthreads();
+  return before + inc - v;
+}
+
+__device__ __forceinline__ u64 warp_max(u64 v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ---------------------------------------------------------------- rows
+struct RowSmem {
+  unsigned hist[kBins];
+  unsigned row_count[2 * kBinRows];  // tokens, and masses, of 32 neighbouring values, the largest first
+  u64 row_mass[2 * kBinRows];
+  u64 table[257];
+  u64 red[33];
+  unsigned bins[32];
+  u64 before_mass, z, t_cut;
+  unsigned before_count;
+  int found, bin, x_cut;
+};
+
+__global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const VerifyParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  RowSmem &S = *reinterpret_cast<RowSmem *>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / (p.T + 1), i = blockIdx.x - b * (p.T + 1);
+  griddep_launch_dependents();
+  int n = p.T;
+  if (p.n_draft) {
+    const int v = p.n_draft[b];
+    n = min(max(v, 0), p.T);
+    if (n != v && i == 0 && tid == 0) set_status(p.status, kDevBadInput);
+  }
+  const long long at = static_cast<long long>(b) * p.T + i;
+  if (i >= n && i < p.T && p.p_draft && tid == 0) p.p_draft[at] = 0.f;   // no draft in this row
+  if (i > n) return;
+  const Row row = make_row(p.logits + static_cast<long long>(blockIdx.x) * p.ld, p.V);
+
+  uint4 buf[kKeep];
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int c = tid + k * kRowThreads;
+    buf[k] = c < row.chunks ? load_chunk(row, c) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+  }
+  auto for_chunks = [&](auto &&fn) {
+#pragma unroll
+    for (int k = 0; k < kKeep; ++k)
+      if (tid + k * kRowThreads < row.chunks) fn(tid + k * kRowThreads, buf[k]);
+    for (int c = tid + kKeep * kRowThreads; c < row.chunks; c += kRowThreads) fn(c, load_chunk(row, c));
+  };
+
+  // ---- the largest value and its first index
+  u64 best = 0;
+  for_chunks([&](int c, const uint4 &w) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int x = row.base + 8 * c + e;
+      if (x >= 0 && x < p.V) best = max(best, argmax_pack(bf16_order_key(static_cast<uint16_t>(chunk_bits(w, e))), x));
+    }
+  });
+  best = warp_max(best);
+  if (lane == 0) S.red[warp] = best;
+  for (int k = tid; k < 257; k += kRowThreads) S.table[k] = kPow2.v[k];
+  __syncthreads();
+  best = warp_max(S.red[lane]);
+  __syncthreads();
+  const uint32_t kmax = static_cast<uint32_t>(best >> 32);
+  const float lmax = key_value(kmax);
+  const bool fine = lmax > -INFINITY && lmax < INFINITY;              // NaN and infinities: no distribution
+  VerifyRow out{};
+  out.argmax = fine ? argmax_index(best) : -1;
+  out.lmax = lmax;
+  const int x = i < n ? p.drafts[at] : -1;
+  const bool x_ok = x >= 0 && x < p.V;
+  if (tid == 0 && (!fine || (i < n && !x_ok))) set_status(p.status, kDevBadInput);
+  if (p.greedy || !fine) {
+    out.z = fine ? 1 : 0;
+    out.mx = fine && x_ok && x == out.argmax ? 1 : 0;
+    if (tid == 0) {
+      p.rows[blockIdx.x] = out;
+      if (i < n && p.p_draft) p.p_draft[at] = out.mx ? 1.f : 0.f;
+    }
+    return;
+  }
+  const MassCtx mc = mass_ctx(lmax, p.temperature, S.table);
+  // a value below this has mass 0 (45 ln 2 = 31.2); it is not counted
+  const float lmin = lmax - 32.f * p.temperature;
+  const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f;
+
+  // ---- histograms: value rank d within its sign, the largest first
+  int resident = 0;
+  for (int half = 0; half < 2; ++half) {
+    const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
+    unsigned *rc = S.row_count + half * kBinRows;
+    u64 *rm = S.row_mass + half * kBinRows;
+    if ((half == 0 && kmax < 0x8000u) || (half == 1 && lmin > 0.f)) {   // no value of this sign counts
+      for (int r = tid; r < kBinRows; r += kRowThreads) {
+        rc[r] = 0;
+        rm[r] = 0;
+      }
+      continue;
+    }
+    resident = half;
+    __syncthreads();                              // the last half's counters have been read
+    for (int k = tid; k < kBins / 4; k += kRowThreads) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for_chunks([&](int, const uint4 &w) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t bits = chunk_bits(w, e);
+        const uint32_t d = top - bf16_order_key(static_cast<uint16_t>(bits));
+        if (d < static_cast<uint32_t>(kBins) && __uint_as_float(bits << 16) >= lmin) atomicAdd(&S.hist[d], 1u);
+      }
+    });
+    __syncthreads();
+    for (int r = warp; r < kBinRows; r += kRowThreads / 32) {
+      const unsigned c = S.hist[r * 32 + lane];
+      unsigned cs = c;
+      u64 ms = 0;
+      if (__any_sync(0xffffffffu, c != 0)) {
+        if (c) ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          cs += __shfl_xor_sync(0xffffffffu, cs, o);
+          ms += __shfl_xor_sync(0xffffffffu, ms, o);
+        }
+      }
+      if (lane == 0) {
+        rc[r] = cs;
+        rm[r] = ms;
+      }
+    }
+  }
+  __syncthreads();
+  // prefix sums over the 2048 rows of values, two for each thread
+  u64 total_c, total_m;
+  const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
+  const u64 m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
+  const u64 pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
+  const u64 pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
+
+  // the counters of one row of 32 values, into S.bins
+  auto fetch_bins = [&](int r) {
+    const bool here = r / kBinRows == resident;
+    if (tid < 32) S.bins[tid] = here ? S.hist[(r % kBinRows) * 32 + tid] : 0u;
+    __syncthreads();
+    if (here) return;
+    const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
+    for_chunks([&](int, const uint4 &w) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t bits = chunk_bits(w, e);
+        const uint32_t d = top - bf16_order_key(static_cast<uint16_t>(bits));
+        if (d < 32u && __uint_as_float(bits << 16) >= lmin) atomicAdd(&S.bins[d], 1u);
+      }
+    });
+    __syncthreads();
+  };
+  auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
+
+  // ---- top-k: the k-th largest value; where fewer than k have a mass, all stay
+  uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
+  int xcut = p.V;
+  u64 z = total_m;
+  const u64 k_th = static_cast<u64>(max(p.top_k, 0));
+  if (use_k && total_c >= k_th) {
+    if (pc < k_th && k_th <= pc + c0 + c1) {
+      const bool second = k_th > pc + c0;
+      S.found = 2 * tid + second;
+      S.before_count = static_cast<unsigned>(pc + (second ? c0 : 0));
+      S.before_mass = pm + (second ? m0 : 0);
+    }
+    __syncthreads();
+    const int r = S.found;
+    fetch_bins(r);
+    if (warp == 0) {
+      const unsigned c = S.bins[lane];
+      unsigned ci = c;
+      const u64 m = c ? mass_of(mc, key_value(key_of(r, lane))) * c : 0;
+      u64 mi = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned tc = __shfl_up_sync(0xffffffffu, ci, o);
+        const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
+        if (lane >= o) {
+          ci += tc;
+          mi += tm;
+        }
+      }
+      const int bin = __ffs(__ballot_sync(0xffffffffu, S.before_count + ci >= k_th)) - 1;
+      if (lane == bin) {
+        S.bin = bin;
+        S.z = S.before_mass + mi;
+      }
+    }
+    __syncthreads();
+    vcut = key_of(r, S.bin);
+    z = S.z;
+    __syncthreads();
+  }
+  // ---- top-p: the value at which the running mass first exceeds top_p of the whole
+  if (use_p) {
+    const double goal = static_cast<double>(p.top_p) * static_cast<double>(z);
+    auto over = [&](u64 v) { return static_cast<double>(v) > goal; };
+    if (tid == 0) S.found = -1;
+    __syncthreads();
+    if (!over(pm) && over(pm + m0 + m1)) {
+      const bool second = !over(pm + m0);
+      S.found = 2 * tid + second;
+      S.before_mass = pm + (second ? m0 : 0);
+    }
+    __syncthreads();
+    const int r = S.found;                        // found: z > goal
+    if (r >= 0) {
+      fetch_bins(r);
+      if (warp == 0) {
+        const unsigned c = S.bins[lane];
+        const u64 one = c ? mass_of(mc, key_value(key_of(r, lane))) : 0, m = one * c;
+        u64 mi = m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
+          if (lane >= o) mi += tm;
+        }
+        const int bin = __ffs(__ballot_sync(0xffffffffu, over(S.before_mass + mi))) - 1;
+        if (lane == bin) {
+          // equal values have equal masses: the first t + 1 of them in index order stay
+          const u64 above = S.before_mass + mi - m;
+          const double t = floor((goal - static_cast<double>(above)) / static_cast<double>(one));
+          const u64 tc = t <= 0.0 ? 0 : t >= static_cast<double>(c) ? c - 1 : static_cast<u64>(t);
+          S.bin = bin;
+          S.t_cut = tc + 1 < c ? tc : ~0ull;      // ~0: all of them
+          S.z = above + (tc + 1) * one;
+        }
+      }
+      __syncthreads();
+      const uint32_t v = key_of(r, S.bin);
+      const u64 tc = S.t_cut;
+      z = S.z;
+      vcut = v;
+      if (tc != ~0ull) {
+        // the index of the (t + 1)-th token of this value: counts in vocabulary
+        // order, a round of 1024 chunks at a time
+        if (tid == 0) S.x_cut = p.V;
+        u64 seen = 0;
+        for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
+          const int c = c_first + tid;
+          uint4 w = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
+          if (c < row.chunks) w = load_chunk(row, c);
+          unsigned mine = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mine += bf16_order_key(static_cast<uint16_t>(chunk_bits(w, e))) == v;
+          u64 all;
+          u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
+          if (rank <= tc && tc < rank + mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (bf16_order_key(static_cast<uint16_t>(chunk_bits(w, e))) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
+          }
+          seen += all;
+          if (seen > tc) break;                   // the same for every thread
+        }
+        __syncthreads();
+        xcut = S.x_cut;
+      }
+    }
+  }
+  if (tid == 0) {
+    out.z = z;
+    out.vcut = vcut;
+    out.xcut = xcut;
+    if (x_ok) {
+      const uint32_t key = bf16_order_key(row.p[x]);
+      if (key > vcut || (key == vcut && x <= xcut)) out.mx = mass_of(mc, key_value(key));
+    }
+    p.rows[blockIdx.x] = out;
+    if (i < n && p.p_draft) p.p_draft[at] = static_cast<float>(static_cast<double>(out.mx) / static_cast<double>(z));
+  }
+}
+
+// ---------------------------------------------------------------- choice
+__device__ __forceinline__ u64 ld_cluster_u64(const u64 *local, uint32_t rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
+  return v;
+}
+
+__global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThreads)
+    verify_choice_kernel(const VerifyParams p) {
+  __shared__ u64 red[33], table[257], my_total;
+  __shared__ int s_refused;
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / kChoiceCtas;
+  const uint32_t rank = cluster_ctarank();
+  for (int k = tid; k < 257; k += kChoiceThreads) table[k] = kPow2.v[k];
+  const int n = p.n_draft ? min(max(p.n_draft[b], 0), p.T) : p.T;
+  if (tid == 0) s_refused = n;
+  __syncthreads();
+  griddep_wait();
+  const VerifyRow *rows = p.rows + static_cast<long long>(b) * (p.T + 1);
+  // ---- the first draft that does not stay: u q < p as u q z < mass
+  for (int i = tid; i < n; i += kChoiceThreads) {
+    const VerifyRow r = rows[i];
+    const long long at = static_cast<long long>(b) * p.T + i;
+    bool stays = r.mx != 0;
+    if (!p.greedy && stays) {
+      const int x = p.drafts[at];                 // in the vocabulary: it has a mass
+      const double q = p.probs ? static_cast<double>(p.probs[at * p.ldq + x]) : 1.0;
+      const double u = p.uniform[static_cast<long long>(b) * (p.T + 1) + i];
+      stays = u * q * static_cast<double>(r.z) < static_cast<double>(r.mx);
+    }
+    if (!stays) atomicMin(&s_refused, i);
+  }
+  __syncthreads();
+  const int kept = s_refused;
+  const VerifyRow r = rows[kept];
+  if (rank == 0 && tid == 0) p.n_accepted[b] = kept;
+  if (p.greedy || r.z == 0) {                     // the same for the whole cluster
+    if (rank == 0 && tid == 0) p.next[b] = r.argmax;
+    return;
+  }
+  // ---- the draw
+  const Row row = make_row(p.logits + (static_cast<long long>(b) * (p.T + 1) + kept) * p.ld, p.V);
+  const MassCtx mc = mass_ctx(r.lmax, p.temperature, table);
+  const long long at = static_cast<long long>(b) * p.T + kept;
+  const bool refused = kept < n;
+  const float *q = refused && p.probs ? p.probs + at * p.ldq : nullptr;
+  const int gone = refused && !p.probs ? p.drafts[at] : -1;           // q is 1 there: nothing is left of p
+  const int per = (row.chunks + kChoiceCtas - 1) / kChoiceCtas;
+  const int first = min(row.chunks, static_cast<int>(rank) * per), last = min(row.chunks, first + per);
+  bool rest = refused;                            // weights max(p - q, 0), else p
+  auto weights = [&](int c, u64 (&w)[8]) -> u64 {
+    const uint4 bits = load_chunk(row, c);
+    u64 sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t u = chunk_bits(bits, e);
+      const int x = row.base + 8 * c + e;
+      const uint32_t key = bf16_order_key(static_cast<uint16_t>(u));
+      u64 m = 0;
+      if ((key > r.vcut || (key == r.vcut && x <= r.xcut)) && x >= 0 && x < p.V) {
+        m = mass_of(mc, __uint_as_float(u << 16));
+        if (rest && m) {
+          const u64 have = q ? scaled_floor(q[x], r.z) : x == gone ? m : 0;
+          m = m > have ? m - have : 0;
+        }
+      }
+      w[e] = m;
+      sum += m;
+    }
+    return sum;
+  };
+  u64 w[8], before = 0, whole = 0;
+  while (true) {
+    u64 mine = 0, all;
+    for (int c = first + tid; c < last; c += kChoiceThreads) mine += weights(c, w);
+    block_scan<kChoiceThreads>(mine, red, &all);
+    if (tid == 0) my_total = all;
+    cluster_sync_all();
+    before = 0;
+    whole = 0;
+#pragma unroll
+    for (int k = 0; k < kChoiceCtas; ++k) {
+      const u64 t = ld_cluster_u64(&my_total, k);
+      if (k < static_cast<int>(rank)) before += t;
+      whole += t;
+    }
+    cluster_sync_all();                           // my_total has been read, and no CTA leaves before
+    if (whole != 0 || !rest) break;
+    rest = false;                                 // nothing is left of p - q: draw from p
+  }
+  // the first token whose running sum exceeds u * whole, i.e. floor(u * whole)
+  const u64 goal = min(scaled_floor(p.uniform[static_cast<long long>(b) * (p.T + 1) + p.T], whole), whole - 1);
+  u64 running = before;
+  if (goal < before) return;                      // in an earlier eighth
+  for (int c0 = first; c0 < last; c0 += kChoiceThreads) {
+    const int c = c0 + tid;
+    u64 all, sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = 0;
+    if (c < last) sum = weights(c, w);
+    u64 s = running + block_scan<kChoiceThreads>(sum, red, &all);
+    if (s <= goal && goal < s + sum) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (s <= goal && goal < s + w[e]) p.next[b] = row.base + 8 * c + e;
+        s += w[e];
+      }
+    }
+    running += all;
+    if (goal < running) return;                   // the same for every thread
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st, int *launches) {
+  cudaError_t e = ensure_smem_attr<verify_rows_kernel>(sizeof(RowSmem));
+  if (e != cudaSuccess) return e;
+  prof_before(SMOL_K_SAMPLE, st);
+  verify_rows_kernel<<<static_cast<unsigned>(p.B) * (p.T + 1), kRowThreads, sizeof(RowSmem), st>>>(p);
+  prof_after(SMOL_K_SAMPLE, st);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  *launches = 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * kChoiceCtas);
+  cfg.blockDim = dim3(kChoiceThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  prof_before(SMOL_K_SAMPLE, st);
+  e = cudaLaunchKernelEx(&cfg, verify_choice_kernel, p);
+  prof_after(SMOL_K_SAMPLE, st);
+  if (e == cudaSuccess) *launches = 2;
+  return e;
+}
+
+}  // namespace smol

@@ -103,6 +103,10 @@ _SIGS = {
     "smol_paged_workspace_bytes": (c_size_t, [_PC, c_int, c_int, c_int]),
     "smol_paged_attention": (c_int, [_PC, c_int, _CK, c_int, _RW, _RW, c_float, c_int, c_void_p, c_size_t,
                                      c_void_p]),
+    "smol_verify_workspace_bytes": (c_size_t, [c_int, c_int]),
+    "smol_verify_drafts": (c_int, [c_void_p, ctypes.c_longlong, c_void_p, c_void_p, c_void_p, ctypes.c_longlong,
+                                   c_int, c_int, c_int, c_float, c_int, c_float, c_int, c_void_p, c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "smol_profile_begin": (c_int, [ctypes.c_uint, c_int]),
     "smol_profile_end": (c_int, [POINTER(c_int), POINTER(c_float), c_int]),
 }
@@ -526,6 +530,53 @@ def paged_attention(cache: PagedCache, layer: int, chunk: Chunk, q: torch.Tensor
         raise ValueError("ws must be on the cache's device")
     _check(_lib.smol_paged_attention(cache.ref, layer, chunk.ref(q.shape[0]), heads, ctypes.byref(qr), ctypes.byref(orr), scale,
                                      window, ws.data_ptr(), ws.numel(), _stream(stream)), "smol_paged_attention")
+
+
+def alloc_verify_workspace(B: int, T: int, device="cuda") -> torch.Tensor:
+    n = _lib.smol_verify_workspace_bytes(B, T)
+    if n == 0:
+        raise SmolError(ERR_UNSUPPORTED_SHAPE, "smol_verify_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _table(t: torch.Tensor, name: str, dtype, shape) -> int:
+    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _row_pitch(t: torch.Tensor, name: str, dtype, B: int, rows: int, V: int) -> int:
+    """Elements from row to row of a [B, rows, V] tensor whose B * rows rows are evenly spaced."""
+    if not (t.is_cuda and t.dtype == dtype and t.shape == (B, rows, V)):
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor of shape {(B, rows, V)}")
+    s0, s1, s2 = t.stride()
+    pitch = s1 if rows > 1 else s0 if B > 1 else V
+    if (s2 != 1 and V > 1) or pitch < V or (B > 1 and s0 != rows * pitch):
+        raise ValueError(f"{name}: rows must be contiguous and evenly spaced")
+    return pitch
+
+
+def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, n_accepted: torch.Tensor, next_ids: torch.Tensor,
+                  ws: torch.Tensor, uniform: Optional[torch.Tensor] = None, draft_probs: Optional[torch.Tensor] = None,
+                  n_draft: Optional[torch.Tensor] = None, p_draft: Optional[torch.Tensor] = None,
+                  temperature: float = 1.0, top_k: int = 0, top_p: float = 1.0, do_sample: bool = True,
+                  stream=None) -> None:
+    """How many of each sequence's drafts [B, T] (int32) stay, and its next token, from the target's logits
+    [B, T + 1, V] (bf16), the drafter's probabilities [B, T, V] (fp32; None: it chooses for certain) and
+    uniform [B, T + 1] (fp32): column i decides draft i, the last one draws the next token."""
+    B, T = drafts.shape
+    V = logits.shape[-1]
+    ld = _row_pitch(logits, "logits", torch.bfloat16, B, T + 1, V)
+    ldq = 0 if draft_probs is None else _row_pitch(draft_probs, "draft_probs", torch.float32, B, T, V)
+    i32, f32 = torch.int32, torch.float32
+    _check(_lib.smol_verify_drafts(
+        logits.data_ptr(), ld, _table(drafts, "drafts", i32, (B, T)),
+        None if n_draft is None else _table(n_draft, "n_draft", i32, (B,)),
+        None if draft_probs is None else draft_probs.data_ptr(), ldq, B, T, V, temperature, top_k, top_p,
+        int(bool(do_sample)), None if uniform is None else _table(uniform, "uniform", f32, (B, T + 1)),
+        _table(n_accepted, "n_accepted", i32, (B,)), _table(next_ids, "next_ids", i32, (B,)),
+        None if p_draft is None else _table(p_draft, "p_draft", f32, (B, T)), ws.data_ptr(), ws.numel(),
+        _stream(stream)), "smol_verify_drafts")
 
 
 def set_wait_limit_ns(ns: int) -> None:
