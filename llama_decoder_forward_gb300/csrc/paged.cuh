@@ -90,9 +90,13 @@ struct PagedAttnParams {
   int H, G;                    // query heads, query heads per kv head
   float scale_log2;            // scale * log2(e)
   int window;                  // > 0: position p sees j > p - window only
+  int q_f16;                   // q and out are f16 (the library's own blocks), else bf16
+  int tt, bk_shift;            // query tokens of a unit, log2 of the keys of a tile (paged_sched.cuh)
+  int ctas;                    // CTAs that share the work
+  uint8_t *ws;
   int *status;
 };
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T);
-cudaError_t launch_paged_attention(const PagedAttnParams &p, uint8_t *ws, int sms, cudaStream_t st, int *launches);
+cudaError_t launch_paged_attention(const PagedAttnParams &p, int sms, cudaStream_t st, int *launches);
 
 }  // namespace smol

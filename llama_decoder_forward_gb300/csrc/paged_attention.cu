@@ -1,94 +1,156 @@
 // paged_attention.cu - causal grouped-query attention of a chunk of new tokens
-// over a paged cache.
+// over a paged cache: the kernel for few rows, the combination of partial
+// results, and the choice of kernel.
 //
 // out[t, h] = sum_j softmax_j(scale q[t, h] . k[j]) v[j] over the positions
-// j <= p, j > p - window, p = L + t.  One warp takes one query row and head and
-// walks over its keys with a running maximum and sum; lane i holds the values
-// at i * hd / 32 .. of q, k, v and the accumulator.
-#include <cuda_fp8.h>
+// j <= p, j > p - window, p = L + t.
 #include <math.h>
 
-#include "paged.cuh"
+#include "paged_decode.cuh"
+#include "profile.cuh"
 
 namespace smol {
 namespace {
 
-template <int HD, bool FP8>
-__device__ __forceinline__ void load_row(const uint8_t *base, long long slot, int lane, float scale,
-                                         float (&f)[HD / 32]) {
-  constexpr int E = HD / 32;
+constexpr int kCombThreads = 256;
+
+// Units cut by a border between CTAs: CTA c's combines the unit that CTA c began
+// and did not finish, from its place 1 and the place 0 of the CTAs behind it up
+// to the one in which the unit ends, in that order (the same bits every time).
+// One warp for each row; blockIdx.y splits the rows.
+template <int HD>
+__global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const PagedAttnParams p, int rows) {
+  __shared__ int list[kPagedMaxCtas], n_warp[8], first_end;
+  __shared__ float weight[8][kPagedMaxCtas];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+  griddep_wait();
+  const PagedMeta *metas = paged_meta(p.ws);
+  const PagedMeta mine = metas[c];
+  if (!mine.out) return;
+  if (tid == 0) first_end = p.ctas;
+  __syncthreads();
+  const int other = c + tid;                      // tid 0: this CTA's own place 1
+  PagedMeta mo{};
+  if (tid > 0 && other < p.ctas) mo = metas[other];
+  if (mo.in && mo.ends) atomicMin(&first_end, other);
+  __syncthreads();
+  const bool in = tid == 0 || (mo.in && other <= first_end);
+  const unsigned vote = __ballot_sync(0xffffffffu, in);
+  if (lane == 0) n_warp[warp] = __popc(vote);
+  __syncthreads();
+  int at = __popc(vote & ((1u << lane) - 1)), n = 0;
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) at += n_warp[w];
+    n += n_warp[w];
+  }
+  if (in) list[at] = other;
+  __syncthreads();
+  const PagedSeq s = paged_seq(p.c, mine.b, paged_cap(p));
+  int t0, nt, lo, hi, j0, j1;
+  paged_unit_tiles(p, s, mine.qt, t0, nt, lo, hi, j0, j1);
+  const int live = nt * p.G;
+  for (int r = blockIdx.y * 8 + warp; r < live; r += gridDim.y * 8) {
+    float mx = -INFINITY, sum = 0.f;
+    for (int i = lane; i < n; i += 32)
+      mx = fmaxf(mx, paged_part(p.ws, list[i], i == 0, rows, HD)[rows * HD + 2 * r]);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const long long i = slot * HD + lane * E + e;
-    if constexpr (FP8)
-      f[e] = __half2float(__half(__nv_cvt_fp8_to_halfraw(base[i], __NV_E4M3))) * scale;
-    else
-      f[e] = __bfloat162float(reinterpret_cast<const bf16 *>(base)[i]);
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int i = lane; i < n; i += 32) {
+      const float2 ml = *reinterpret_cast<const float2 *>(paged_part(p.ws, list[i], i == 0, rows, HD) + rows * HD + 2 * r);
+      const float a = mx == -INFINITY ? 0.f : pd_ex2(ml.x - mx);
+      weight[warp][i] = a;
+      sum += a * ml.y;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    float acc[HD / 32];
+#pragma unroll
+    for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float *row = paged_part(p.ws, list[i], i == 0, rows, HD) + r * HD + lane * (HD / 32);
+      const float a = weight[warp][i];
+      if constexpr (HD == 64) {
+        const float2 v = *reinterpret_cast<const float2 *>(row);
+        acc[0] += a * v.x;
+        acc[1] += a * v.y;
+      } else {
+        const float4 v = *reinterpret_cast<const float4 *>(row);
+        acc[0] += a * v.x;
+        acc[1] += a * v.y;
+        acc[2] += a * v.z;
+        acc[3] += a * v.w;
+      }
+    }
+    uint32_t *out = reinterpret_cast<uint32_t *>(
+        p.o.data + (paged_unit_row(p.o, p, s, mine.b, t0, mine.kvh, r) + lane * (HD / 32)) * 2);
+#pragma unroll
+    for (int e = 0; e < HD / 64; ++e)
+      out[e] = p.q_f16 ? pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    __syncwarp();                                 // the weights are rewritten
   }
 }
 
-template <int HD, bool FP8>
-__global__ void __launch_bounds__(128) paged_rows_kernel(const PagedAttnParams p) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int b = static_cast<int>(item / (static_cast<long long>(p.c.T) * p.H));
-  if (b >= p.c.B) return;
-  const int rest = static_cast<int>(item - static_cast<long long>(b) * p.c.T * p.H);
-  const int t = rest / p.H, h = rest % p.H, kvh = h / p.G;
-  const PagedSeq s = paged_seq(p.c, b, p.kv.max_pages << p.kv.page_shift);
-  if (s.bad && lane == 0) set_status(p.status, kDevBadInput);
-  if (t >= s.n) return;
-  const bf16 *q = reinterpret_cast<const bf16 *>(p.q.data) + paged_row_off(p.q, p.c, s, b, t, h) + lane * E;
-  float qf[E], acc[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qf[e] = __bfloat162float(q[e]);
-    acc[e] = 0.f;
-  }
-  const int at = s.L + t, lo = p.window > 0 ? max(0, at - p.window + 1) : 0;
-  for (int j = lo; j <= at; ++j) {
-    const int page = paged_page(p.kv, b, j);
-    if (page < 0 || page >= p.kv.P) {
-      if (lane == 0) set_status(p.status, kDevBadInput);
-      continue;
-    }
-    const long long slot = paged_slot(p.kv, page, j, kvh);
-    float kf[E], vf[E];
-    load_row<HD, FP8>(p.kv.k, slot, lane, FP8 ? p.kv.ks[slot] : 1.f, kf);
-    load_row<HD, FP8>(p.kv.v, slot, lane, FP8 ? p.kv.vs[slot] : 1.f, vf);
-    float d = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) d += qf[e] * kf[e];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-    d *= p.scale_log2;
-    const float mn = fmaxf(m, d), a = exp2f(m - mn), w = exp2f(d - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = acc[e] * a + w * vf[e];
-  }
-  bf16 *o = reinterpret_cast<bf16 *>(p.o.data) + paged_row_off(p.o, p.c, s, b, t, h) + lane * E;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = __float2bfloat16_rn(acc[e] / l);
+template <int HD, bool FP8, int RT>
+cudaError_t launch_few(const PagedAttnParams &p, cudaStream_t st) {
+  using C = PdCfg<HD, FP8, RT>;
+  const cudaError_t e = ensure_smem_attr<paged_few_rows_kernel<HD, FP8, RT>>(C::SMEM);
+  if (e != cudaSuccess) return e;
+  PagedAttnParams q = p;
+  q.bk_shift = C::BK_SHIFT;
+  paged_few_rows_kernel<HD, FP8, RT><<<p.ctas, C::THREADS, C::SMEM, st>>>(q);
+  return cudaGetLastError();
+}
+
+template <int HD>
+cudaError_t launch_combine(const PagedAttnParams &p, int rows, cudaStream_t st) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.ctas, static_cast<unsigned>(cdiv(rows, 32)));
+  cfg.blockDim = dim3(kCombThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_combine_kernel<HD>, p, rows);
 }
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) { return 1024; }
+// Rows of a unit: the tile of the kernel that takes the call.
+static int unit_rows(int G, int T) { return T * G <= 16 ? 16 : 32; }
 
-cudaError_t launch_paged_attention(const PagedAttnParams &p, uint8_t *ws, int sms, cudaStream_t st, int *launches) {
-  const unsigned blocks = static_cast<unsigned>(cdiv(static_cast<long long>(p.c.B) * p.c.T * p.H, 4));
-  if (p.kv.hd == 64) {
-    if (p.kv.e4m3) paged_rows_kernel<64, true><<<blocks, 128, 0, st>>>(p);
-    else paged_rows_kernel<64, false><<<blocks, 128, 0, st>>>(p);
+size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {
+  return kPagedPartOff + (size_t)kPagedMaxCtas * 2 * unit_rows(H / KV, T) * (hd + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStream_t st, int *launches) {
+  PagedAttnParams p = p0;
+  p.ctas = min(sms, kPagedMaxCtas);
+  const int rows = unit_rows(p.G, p.c.T);
+  p.tt = rows / p.G;
+  const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64, one = rows == 16;
+  p.bk_shift = h64 || f8 ? 8 : 7;
+  cudaError_t e;
+  prof_before(SMOL_K_DEC_ATTN, st);
+  if (h64) {
+    if (f8) e = one ? launch_few<64, true, 1>(p, st) : launch_few<64, true, 2>(p, st);
+    else e = one ? launch_few<64, false, 1>(p, st) : launch_few<64, false, 2>(p, st);
   } else {
-    if (p.kv.e4m3) paged_rows_kernel<128, true><<<blocks, 128, 0, st>>>(p);
-    else paged_rows_kernel<128, false><<<blocks, 128, 0, st>>>(p);
+    if (f8) e = one ? launch_few<128, true, 1>(p, st) : launch_few<128, true, 2>(p, st);
+    else e = one ? launch_few<128, false, 1>(p, st) : launch_few<128, false, 2>(p, st);
   }
+  prof_after(SMOL_K_DEC_ATTN, st);
+  if (e != cudaSuccess) return e;
   *launches = 1;
-  return cudaGetLastError();
+  prof_before(SMOL_K_OTHER, st);
+  e = h64 ? launch_combine<64>(p, rows, st) : launch_combine<128>(p, rows, st);
+  prof_after(SMOL_K_OTHER, st);
+  if (e == cudaSuccess) *launches = 2;
+  return e;
 }
 
 }  // namespace smol

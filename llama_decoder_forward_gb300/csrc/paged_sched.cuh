@@ -1,0 +1,179 @@
+// paged_sched.cuh - how the paged attention kernels share a call's work among
+// their CTAs, and where a CTA leaves what it has of a unit it does not finish.
+//
+// A unit is one sequence, one kv head and a tile of `tt` query tokens (with all
+// g heads of each: tt * g rows that read the same keys).  Its work is a number of
+// tiles of `1 << bk_shift` keys, from the first that its first row's window shows
+// to the one of its last row.  The units of a call in the order (sequence, query
+// tile, kv head) form one line of tiles, cut into equal pieces, one for each CTA:
+// long caches, short ones, single tokens and chunks balance without a plan made
+// on the host.  A unit cut by a border is finished by the combining kernel from
+// the CTAs' partial results (unnormalised sums, row maxima and row sums).
+#pragma once
+
+#include "paged.cuh"
+
+namespace smol {
+
+// One unit of the line and the tile a worker stands at.
+struct PagedIter {
+  int b, qt, kvh, j;           // sequence, query tile, kv head, key tile
+  int j0, j1;                  // the unit's key tiles
+  int t0, nt;                  // its first token, and how many
+  int lo, hi;                  // the positions that some row of it sees: [lo, hi)
+  PagedSeq s;
+  long long left;              // tiles of this worker still to do, this one included
+};
+
+__device__ __forceinline__ int paged_cap(const PagedAttnParams &p) { return p.kv.max_pages << p.kv.page_shift; }
+
+__device__ __forceinline__ void paged_unit_tiles(const PagedAttnParams &p, const PagedSeq &s, int qt, int &t0, int &nt,
+                                                 int &lo, int &hi, int &j0, int &j1) {
+  t0 = qt * p.tt;
+  nt = min(p.tt, s.n - t0);
+  hi = s.L + t0 + nt;
+  lo = p.window > 0 ? max(0, s.L + t0 - p.window + 1) : 0;
+  j0 = lo >> p.bk_shift;
+  j1 = (hi + (1 << p.bk_shift) - 1) >> p.bk_shift;
+}
+
+__device__ __forceinline__ void paged_set_unit(const PagedAttnParams &p, PagedIter &it) {
+  paged_unit_tiles(p, it.s, it.qt, it.t0, it.nt, it.lo, it.hi, it.j0, it.j1);
+}
+
+// To the next tile; past the unit's last one, to the next unit's first.
+__device__ __forceinline__ void paged_next(const PagedAttnParams &p, PagedIter &it) {
+  if (--it.left <= 0) return;
+  if (++it.j < it.j1) return;
+  if (++it.kvh == p.kv.KV) {
+    it.kvh = 0;
+    if (++it.qt * p.tt >= it.s.n) {
+      it.qt = 0;
+      do {
+        ++it.b;                                   // there is a further unit: left > 0
+        it.s = paged_seq(p.c, it.b, paged_cap(p));
+      } while (it.s.n == 0 && it.b + 1 < p.c.B);
+    }
+  }
+  paged_set_unit(p, it);
+  it.j = it.j0;
+}
+
+// Tiles of one sequence.
+__device__ __forceinline__ long long paged_seq_tiles(const PagedAttnParams &p, const PagedSeq &s) {
+  long long sum = 0;
+  for (int qt = 0; qt * p.tt < s.n; ++qt) {
+    int t0, nt, lo, hi, j0, j1;
+    paged_unit_tiles(p, s, qt, t0, nt, lo, hi, j0, j1);
+    sum += j1 - j0;
+  }
+  return sum * p.kv.KV;
+}
+
+struct PagedSchedSmem {
+  long long warp_sum[32];
+  PagedIter start;
+};
+
+// Worker `w` of `workers`: its first tile and how many it has (left == 0: none).
+// Called by all THREADS threads of the CTA.
+template <int THREADS>
+__device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int w, int workers, PagedSchedSmem &sm) {
+  constexpr int W = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cap = paged_cap(p);
+  // the whole line
+  long long mine = 0, first = 0;
+  for (int b = tid; b < p.c.B; b += THREADS) {
+    const PagedSeq s = paged_seq(p.c, b, cap);
+    if (s.bad && w == 0) set_status(p.status, kDevBadInput);
+    const long long n = paged_seq_tiles(p, s);
+    if (b == tid) first = n;
+    mine += n;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sm.warp_sum[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) total += sm.warp_sum[i];
+  __syncthreads();
+  const long long from = total * w / workers, to = total * (w + 1) / workers;
+  PagedIter it{};
+  if (from == to) return it;                      // the same for the whole CTA
+  // the sequence that holds tile `from`, THREADS sequences at a time
+  long long before = 0;
+  for (int base = 0; base < p.c.B; base += THREADS) {
+    const int b = base + tid;
+    long long n = first;
+    PagedSeq s{};
+    if (b < p.c.B) {
+      s = paged_seq(p.c, b, cap);
+      if (base) n = paged_seq_tiles(p, s);
+    } else {
+      n = 0;
+    }
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    if (lane == 31) sm.warp_sum[warp] = inc;
+    __syncthreads();
+    long long pre = before + inc - n, round = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if (i < warp) pre += sm.warp_sum[i];
+      round += sm.warp_sum[i];
+    }
+    if (pre <= from && from < pre + n) {
+      it.b = b;
+      it.s = s;
+      it.left = to - from;
+      long long off = from - pre;
+      for (it.qt = 0;; ++it.qt) {
+        paged_set_unit(p, it);
+        const long long unit = it.j1 - it.j0, all = unit * p.kv.KV;
+        if (off < all) {
+          it.kvh = static_cast<int>(off / unit);
+          it.j = it.j0 + static_cast<int>(off - it.kvh * unit);
+          break;
+        }
+        off -= all;
+      }
+      sm.start = it;
+    }
+    before += round;
+    __syncthreads();
+    if (from < before) break;                     // the same for the whole CTA
+  }
+  return sm.start;
+}
+
+// ---------------------------------------------------------------- partial results
+// Each CTA has two places: 0 for a unit begun by an earlier CTA, 1 for one that
+// it begins and does not finish.
+struct PagedMeta {
+  int in, ends;                // place 0 is used; that unit ends in this CTA
+  int out;                     // place 1 is used
+  int b, qt, kvh;              // place 1's unit
+};
+constexpr int kPagedMaxCtas = 160;
+constexpr size_t kPagedMetaOff = 1024, kPagedPartOff = kPagedMetaOff + kPagedMaxCtas * sizeof(PagedMeta) + 256;
+
+// Place of CTA c: rows of HD sums, then (maximum, sum) of each row.
+__device__ __forceinline__ float *paged_part(uint8_t *ws, int c, int place, int rows, int hd) {
+  return reinterpret_cast<float *>(ws + kPagedPartOff) + (static_cast<long long>(c) * 2 + place) * rows * (hd + 2);
+}
+__device__ __forceinline__ PagedMeta *paged_meta(uint8_t *ws) { return reinterpret_cast<PagedMeta *>(ws + kPagedMetaOff); }
+
+// Element offset of row r (token r / g, head r % g) of a unit in q or out.
+__device__ __forceinline__ long long paged_unit_row(const PagedRows &x, const PagedAttnParams &p, const PagedSeq &s, int b,
+                                                    int t0, int kvh, int r) {
+  const int t = r / p.G;
+  return paged_row_off(x, p.c, s, b, t0 + t, kvh * p.G + (r - t * p.G));
+}
+
+}  // namespace smol

@@ -877,9 +877,10 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
   p.G = n_heads / cache->n_kv_heads;
   p.scale_log2 = 1.4426950408889634f * (scale > 0.f ? scale : 1.f / sqrtf((float)cache->head_dim));
   p.window = window;
+  p.ws = static_cast<uint8_t *>(ws);
   p.status = static_cast<int *>(ws);
   int n = 0;
-  const cudaError_t e = launch_paged_attention(p, static_cast<uint8_t *>(ws), sms, static_cast<cudaStream_t>(stream), &n);
+  const cudaError_t e = launch_paged_attention(p, sms, static_cast<cudaStream_t>(stream), &n);
   g_launches = n;
   return e == cudaSuccess ? SMOL_OK : cuda_fail(e);
 }
