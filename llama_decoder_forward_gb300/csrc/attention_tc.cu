@@ -105,48 +105,6 @@ enum : int {
   kAtTimeoutDrain = 0x204,
 };
 
-// 2^x with the hardware approximation (flushes subnormal results to zero;
-// 2^(-inf) = 0).
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// (a0, a1) * b + c on the packed two-lane fp32 pipe path (one instruction).
-__device__ __forceinline__ float2 ffma2(float a0, float a1, float b, float c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\t"
-      "mov.b64 rb, {%4, %4};\n\t"
-      "mov.b64 rc, {%5, %5};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
-      "mov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a0), "f"(a1), "f"(b), "f"(c));
-  return d;
-}
-
-// (a0 + b0, a1 + b1) on the packed two-lane fp32 path (one instruction).
-__device__ __forceinline__ float2 fadd2(float a0, float a1, float b0, float b1) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\t"
-      "mov.b64 rb, {%4, %5};\n\t"
-      "add.rn.f32x2 rd, ra, rb;\n\t"
-      "mov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
-  return d;
-}
-
-// max(a, b, c) in one instruction (three-input max of sm_100 and later).
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 __device__ __forceinline__ void at_status(int *status, int code) {
   if (status) atomicCAS(status, 0, code);
 }

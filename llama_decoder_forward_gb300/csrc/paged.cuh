@@ -93,10 +93,12 @@ struct PagedAttnParams {
   int q_f16;                   // q and out are f16 (the library's own blocks), else bf16
   int tt, bk_shift;            // query tokens of a unit, log2 of the keys of a tile (paged_sched.cuh)
   int ctas;                    // CTAs that share the work
+  unsigned long long wait_ns;  // limit of the bounded waits
   uint8_t *ws;
   int *status;
 };
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T);
+cudaError_t launch_paged_tiles(const PagedAttnParams &p, cudaStream_t st);   // units of 256 rows, on tcgen05
 cudaError_t launch_paged_attention(const PagedAttnParams &p, int sms, cudaStream_t st, int *launches);
 
 }  // namespace smol

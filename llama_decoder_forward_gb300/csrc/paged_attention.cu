@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const Paged
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     for (int i = lane; i < n; i += 32) {
       const float2 ml = *reinterpret_cast<const float2 *>(paged_part(p.ws, list[i], i == 0, rows, HD) + rows * HD + 2 * r);
-      const float a = mx == -INFINITY ? 0.f : pd_ex2(ml.x - mx);
+      const float a = mx == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
       weight[warp][i] = a;
       sum += a * ml.y;
     }
@@ -121,7 +121,10 @@ cudaError_t launch_combine(const PagedAttnParams &p, int rows, cudaStream_t st) 
 }  // namespace
 
 // Rows of a unit: the tile of the kernel that takes the call.
-static int unit_rows(int G, int T) { return T * G <= 16 ? 16 : 32; }
+static int unit_rows(int G, int T) {
+  const long long r = (long long)T * G;
+  return r <= 16 ? 16 : r <= 32 ? 32 : 256;
+}
 
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {
   return kPagedPartOff + (size_t)kPagedMaxCtas * 2 * unit_rows(H / KV, T) * (hd + 2) * sizeof(float);
@@ -133,10 +136,12 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   const int rows = unit_rows(p.G, p.c.T);
   p.tt = rows / p.G;
   const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64, one = rows == 16;
-  p.bk_shift = h64 || f8 ? 8 : 7;
+  p.bk_shift = rows == 256 || !(h64 || f8) ? 7 : 8;
   cudaError_t e;
   prof_before(SMOL_K_DEC_ATTN, st);
-  if (h64) {
+  if (rows == 256) {
+    e = launch_paged_tiles(p, st);
+  } else if (h64) {
     if (f8) e = one ? launch_few<64, true, 1>(p, st) : launch_few<64, true, 2>(p, st);
     else e = one ? launch_few<64, false, 1>(p, st) : launch_few<64, false, 2>(p, st);
   } else {

@@ -26,12 +26,6 @@
 namespace smol {
 namespace {
 
-__device__ __forceinline__ float pd_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ void pd_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -284,7 +278,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float mn = fmaxf(m[rt][i], mx[i]);
-            const float a = mn == -INFINITY ? 1.f : pd_ex2(m[rt][i] - mn);
+            const float a = mn == -INFINITY ? 1.f : ex2_approx(m[rt][i] - mn);
             m[rt][i] = mn;
             l[rt][i] *= a;
 #pragma unroll
@@ -299,7 +293,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
         for (int n = 0; n < NT8; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float w = pd_ex2(s[rt][n][e] - mu[e >> 1]);
+            const float w = ex2_approx(s[rt][n][e] - mu[e >> 1]);
             l[rt][e >> 1] += w;
             s[rt][n][e] = w;
           }
@@ -393,7 +387,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
             for (int i = 0; i < 2; ++i) {
               const float m2 = sr[(ND8 * 4 + i) * 32], l2 = sr[(ND8 * 4 + 2 + i) * 32];
               const float mn = fmaxf(m[rt][i], m2);
-              const float a = mn == -INFINITY ? 1.f : pd_ex2(m[rt][i] - mn), a2 = mn == -INFINITY ? 1.f : pd_ex2(m2 - mn);
+              const float a = mn == -INFINITY ? 1.f : ex2_approx(m[rt][i] - mn), a2 = mn == -INFINITY ? 1.f : ex2_approx(m2 - mn);
               m[rt][i] = mn;
               l[rt][i] = l[rt][i] * a + l2 * a2;
 #pragma unroll

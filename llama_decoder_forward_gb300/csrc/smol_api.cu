@@ -879,6 +879,8 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
   p.window = window;
   p.ws = static_cast<uint8_t *>(ws);
   p.status = static_cast<int *>(ws);
+  p.wait_ns = g_attn_wait_ns.load(std::memory_order_relaxed);
+  if (p.wait_ns == 0) p.wait_ns = kWaitTimeoutNs;
   int n = 0;
   const cudaError_t e = launch_paged_attention(p, sms, static_cast<cudaStream_t>(stream), &n);
   g_launches = n;
