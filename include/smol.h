@@ -511,7 +511,7 @@ int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_ch
  * Probabilities are held to about 2^-43 of the row's largest and summed exactly
  * (a token below 2^-45 of the largest counts as impossible), so the choice is
  * the definition's except where u lies within 1e-11 of a border.
- * V <= 2^19.  Two kernel launches on `stream`.
+ * V <= 2^19, T <= 512.  Two kernel launches on `stream`.
  * ------------------------------------------------------------------------- */
 size_t smol_verify_workspace_bytes(int B, int T);
 int smol_verify_drafts(const void *logits, long long ld, const int32_t *drafts, const int32_t *n_draft,

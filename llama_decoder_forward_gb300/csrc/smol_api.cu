@@ -888,7 +888,7 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
 }
 
 SMOL_API size_t smol_verify_workspace_bytes(int B, int T) {
-  if (B <= 0 || T <= 0 || ((long long)T + 1) * B > (1 << 24)) return 0;
+  if (B <= 0 || T <= 0 || T > 512 || ((long long)T + 1) * B > (1 << 24)) return 0;
   return 1024 + sizeof(VerifyRow) * (size_t)B * ((size_t)T + 1);
 }
 
@@ -922,6 +922,11 @@ SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t 
   p.ldq = ld_probs;
   p.B = B; p.T = T; p.V = V;
   p.temperature = temperature;
+  if (!greedy) {
+    const double c = 1.4426950408889634 / (double)temperature;
+    p.c_hi = (float)c;
+    p.c_lo = isfinite(p.c_hi) ? (float)(c - (double)p.c_hi) : 0.f;
+  }
   p.top_p = top_p > 0.f ? top_p : 0.f;   // as in smol_sample: the first token in descending order
   p.top_k = top_k;
   p.greedy = greedy;

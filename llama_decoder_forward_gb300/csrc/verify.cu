@@ -11,18 +11,20 @@
 // Exactness.  A row of 50,000 or more running sums has a border within 1e-7 of u
 // once in a hundred draws, so fp32 sums would pick another token than the
 // definition.  Here a token's mass is e = 2^((l - l_max) log2(e) / temperature) as
-// an integer in units of 2^-44, from an exponential good to about 2^-43 (mass_of),
+// an integer in units of 2^-44, from an exponential good to some 2^-44 (mass_of),
 // and every sum is a 64-bit integer: exact, and the same in any order.  The
 // borders are then off by less than 1e-11 of the whole.
 //
 // Two launches.
-//   rows    one CTA of 1024 threads for each target row.  The row is read once,
-//           into registers (up to 65,536 tokens; what is longer is read again
-//           from L2).  bf16 logits take few distinct values, so the row becomes
-//           a histogram over the values (32,768 counters: the values >= 0, then
-//           those < 0) and the exponential is taken once for each value that
-//           occurs: a tenth of the row and less.  The sum, the k-th largest
-//           value and the top-p cut are prefix sums over the histogram.
+//   rows    one CTA of 1024 threads for each target row, which it reads one to
+//           three times (from L2 after the first; in registers it would take half
+//           of them, and the spills cost more).  bf16 logits take few distinct
+//           values, so the row becomes a histogram over the values (32,768
+//           counters: the values >= 0, or those < 0) and the exponential is taken
+//           once for each value that occurs: a tenth of the row and less.  The
+//           sum, the k-th largest value and the top-p cut are prefix sums over
+//           the histogram.  Where the k largest are all >= 0, the rest is not
+//           looked at.
 //   choice  one cluster of eight CTAs for each sequence: the acceptances, then
 //           the draw over one row, an eighth of the vocabulary for each CTA.
 #include <math.h>
@@ -38,22 +40,26 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kRowThreads = 1024;
-constexpr int kKeep = 8;             // chunks of 8 tokens a thread keeps in registers
+constexpr int kBatch = 6;            // 16-byte loads in flight in each thread
 constexpr int kBins = 32768;         // values of one sign
 constexpr int kBinRows = kBins / 32;
-constexpr int kChoiceThreads = 512;
+constexpr int kChoiceThreads = 512;  // the most drafts of a sequence, too
 constexpr int kChoiceCtas = 8;
 constexpr float kMinLog2 = -45.f;    // 2^x below half a unit of 2^-44 counts as 0
 
 // ---------------------------------------------------------------- masses
-// 2^(j / 256), j = -128 .. 128, in units of 2^-62: from 2^-0.5 by products with
-// 2^(1/256), each rounded at 2^-63 (off by 2^-55 at most).
+// 2^(j / 256), j = -128 .. 128, each as a sum of two floats: from 2^-0.5 by
+// products with 2^(1/256), each rounded at 2^-63 (off by 2^-55 at most).
 struct Pow2Table {
-  u64 v[257];
+  float2 v[257];
   constexpr Pow2Table() : v() {
     unsigned __int128 x = 0x5a827999fcef3242ull;               // 2^-0.5 in units of 2^-63
     for (int j = 0; j < 257; ++j) {
-      v[j] = static_cast<u64>((x + 1) >> 1);
+      const u64 t = static_cast<u64>((x + 1) >> 1);            // units of 2^-62
+      const float hi = static_cast<float>(static_cast<double>(t));
+      const long long rest = static_cast<long long>(t - static_cast<u64>(static_cast<double>(hi)));
+      v[j].x = static_cast<float>(static_cast<double>(hi) / 4611686018427387904.0);
+      v[j].y = static_cast<float>(static_cast<double>(rest) / 4611686018427387904.0);
       // 2^(1/256) - 1 in units of 2^-63
       x += (x * 0x0058d7d2d5e5f6b1ull + (static_cast<unsigned __int128>(1) << 62)) >> 63;
     }
@@ -64,51 +70,54 @@ __device__ constexpr Pow2Table kPow2{};
 // Exponentials of one row: y = (l - l_max) * c with c = log2(e) / temperature.
 struct MassCtx {
   float lmax, c_hi, c_lo;
-  const u64 *table;                  // kPow2 in shared memory
+  const float2 *table;               // kPow2 in shared memory
 };
-
-__device__ __forceinline__ MassCtx mass_ctx(float lmax, float temperature, const u64 *table) {
-  const double c = 1.4426950408889634 / static_cast<double>(temperature);
-  MassCtx m;
-  m.lmax = lmax;
-  m.c_hi = static_cast<float>(c);
-  m.c_lo = static_cast<float>(c - static_cast<double>(m.c_hi));
-  m.table = table;
-  return m;
-}
 
 // round(2^44 * 2^y): the difference and the product are carried as sums of two
 // floats (Dekker's and Knuth's exact sums and products), y is split into a whole
 // number, 256ths from the table and a remainder r, |r| <= 2^-9, whose 2^r - 1 is
 // a short series (Tang's table-driven exponential): the leading term in two
-// floats, the others below 2^-18 in one.
+// floats, the others below 2^-18 in one.  Off by half a unit and, rarely, up to
+// three (against extended precision, 1.2 million values).  Whole numbers come from
+// adding 1.5 * 2^23: the conversion instructions share a slow pipe.
 __device__ __forceinline__ u64 mass_of(const MassCtx &m, float l) {
+  constexpr float kMagic = 12582912.f;
+  constexpr int kMagicBits = 0x4b400000;
   const float dh = __fsub_rn(l, m.lmax);
-  const float yh = __fmul_rn(dh, m.c_hi);
-  if (!(yh >= kMinLog2)) return dh == 0.f ? 1ull << 44 : 0;           // also -inf and NaN
+  float yh = __fmul_rn(dh, m.c_hi);
+  // not -inf, not NaN; and no value above l_max, which bins without tokens name: the
+  // table's index is 0 .. 256 for y <= 0 only
+  const bool counts = yh >= kMinLog2 && yh <= 0.f;
+  yh = counts ? yh : 0.f;
   const float bb = __fsub_rn(dh, l);
   const float dl = __fsub_rn(__fsub_rn(l, __fsub_rn(dh, bb)), __fadd_rn(m.lmax, bb));
   const float yl = __fadd_rn(__fmaf_rn(dh, m.c_hi, -yh), __fmaf_rn(dh, m.c_lo, __fmul_rn(dl, m.c_hi)));
-  const float n = rintf(yh);
+  const float ns = __fadd_rn(yh, kMagic), n = __fsub_rn(ns, kMagic);
   const float f = __fsub_rn(yh, n);
-  const float j = rintf(f * 256.f);
+  const float js = __fmaf_rn(f, 256.f, kMagic), j = __fsub_rn(js, kMagic);
   const float f2 = __fmaf_rn(j, -0.00390625f, f);
   const float rh = __fadd_rn(f2, yl);
-  const float rb = __fsub_rn(rh, f2);
-  const float rl = __fadd_rn(__fsub_rn(f2, __fsub_rn(rh, rb)), __fsub_rn(yl, rb));
-  // ln 2 as a sum of two floats
+  const float rl = __fsub_rn(yl, __fsub_rn(rh, f2));
+  // ln 2 as a sum of two floats; ln2^2 / 2, ln2^3 / 6, ln2^4 / 24
   constexpr float kLn2Hi = 0.693147182464599609375f, kLn2Lo = -1.904654299957768e-9f;
   const float ph = __fmul_rn(rh, kLn2Hi);
   const float pl = __fadd_rn(__fmaf_rn(rh, kLn2Hi, -ph), __fmaf_rn(rh, kLn2Lo, __fmul_rn(rl, kLn2Hi)));
-  // ln2^2 / 2, ln2^3 / 6, ln2^4 / 24
   const float s = __fmaf_rn(__fmaf_rn(rh, 0.009618129107628f, 0.055504108664822f), rh, 0.240226506959101f);
   const float rest = __fmaf_rn(__fmul_rn(rh, rh), s, pl);
-  // 2^r - 1 in units of 2^-62 (below 2^54 in magnitude)
-  const long long w = __float2ll_rn(ph * 4611686018427387904.f) + __float2ll_rn(rest * 4611686018427387904.f);
-  const u64 t = m.table[static_cast<int>(j) + 128];
-  const u64 e = t + (static_cast<u64>(__mul64hi(static_cast<long long>(t), w)) << 2);
-  const int shift = 18 - static_cast<int>(n);                         // 18 .. 63
-  return (e + (1ull << (shift - 1))) >> shift;
+  const float h = __fadd_rn(ph, rest), lo = __fsub_rn(rest, __fsub_rn(h, ph));   // 2^r - 1
+  const float2 t = m.table[__float_as_int(js) - kMagicBits + 128];
+  // t (1 + h + lo)
+  const float p = __fmul_rn(t.x, h), pe = __fmaf_rn(t.x, h, -p);
+  const float eh = __fadd_rn(t.x, p);
+  const float el = __fadd_rn(__fsub_rn(p, __fsub_rn(eh, t.x)), __fadd_rn(__fmaf_rn(t.x, lo, pe), __fmaf_rn(t.y, h, t.y)));
+  // in units of 2^-44: whole multiples of 2^23 (at most 2^21.5 of them), and the rest
+  const float scale = __int_as_float((127 + 44 + __float_as_int(ns) - kMagicBits) << 23);
+  const float v = __fmul_rn(eh, scale);
+  const float his = __fmaf_rn(v, 1.1920928955078125e-7f, kMagic);
+  const float rem = __fmaf_rn(__fsub_rn(his, kMagic), -8388608.f, v);
+  const float los = __fadd_rn(__fmaf_rn(el, scale, rem), kMagic);
+  const long long mass = static_cast<long long>(__float_as_int(his) - kMagicBits) * 8388608ll + (__float_as_int(los) - kMagicBits);
+  return counts ? static_cast<u64>(mass) : dh == 0.f ? 1ull << 44 : 0ull;   // l_max itself where c is infinite
 }
 
 // floor(q * z) for z < 2^63 (a q that is negative or NaN counts as 0, one of 2 or
@@ -156,14 +165,36 @@ __device__ __forceinline__ uint4 load_chunk(const Row &r, int c) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ uint32_t chunk_bits(const uint4 &c, int e) {
+// Element e of a chunk of eight 16-bit values.
+__device__ __forceinline__ uint32_t chunk_half(const uint4 &c, int e) {
   const uint32_t w = (e >> 1) == 0 ? c.x : (e >> 1) == 1 ? c.y : (e >> 1) == 2 ? c.z : c.w;
-  return (w >> ((e & 1) * 16)) & 0xffffu;
+  return (e & 1) ? w >> 16 : w & 0xffffu;
+}
+
+// bf16_order_key of two values: all bits of a negative one flipped, the sign of
+// another; adding +0 has turned -0 into +0.
+__device__ __forceinline__ uint32_t order_key2(uint32_t w) {
+  const __nv_bfloat162 v = __hadd2(*reinterpret_cast<const __nv_bfloat162 *>(&w), __nv_bfloat162(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0)));
+  w = *reinterpret_cast<const uint32_t *>(&v);
+  uint32_t sign;                                  // 0xffff where negative (the bytes' sign replicated)
+  asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(sign) : "r"(w));
+  return w ^ (sign | 0x80008000u);
+}
+
+__device__ __forceinline__ uint4 chunk_keys(const uint4 &c) {
+  return make_uint4(order_key2(c.x), order_key2(c.y), order_key2(c.z), order_key2(c.w));
 }
 
 __device__ __forceinline__ float key_value(uint32_t key) {
   const uint32_t bits = (key & 0x8000u) ? key & 0x7fffu : ~key & 0xffffu;
   return __uint_as_float(bits << 16);
+}
+
+// Adds 1 to the counter of key k (at `base` + 4 k) if k >= from, without a branch.
+__device__ __forceinline__ void count_from(uint32_t base, uint32_t k, uint32_t from) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(base + 4 * k),
+               "r"(k), "r"(from)
+               : "memory");
 }
 
 // ---------------------------------------------------------------- block sums
@@ -208,7 +239,7 @@ struct RowSmem {
   unsigned hist[kBins];
   unsigned row_count[2 * kBinRows];  // tokens, and masses, of 32 neighbouring values, the largest first
   u64 row_mass[2 * kBinRows];
-  u64 table[257];
+  float2 table[257];
   u64 red[33];
   unsigned bins[32];
   u64 before_mass, z, t_cut;
@@ -233,31 +264,60 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   if (i > n) return;
   const Row row = make_row(p.logits + static_cast<long long>(blockIdx.x) * p.ld, p.V);
 
-  uint4 buf[kKeep];
+  // fn(chunk, its eight order keys in pairs), over this thread's chunks, a batch of
+  // loads at a time; `between` runs with the first batch under way
+  auto for_chunks = [&](auto &&fn, auto &&between) {
+    bool start = true;
+    for (int c0 = tid; start || c0 < row.chunks; c0 += kBatch * kRowThreads) {
+      uint4 w[kBatch];
 #pragma unroll
-  for (int k = 0; k < kKeep; ++k) {
-    const int c = tid + k * kRowThreads;
-    buf[k] = c < row.chunks ? load_chunk(row, c) : make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-  }
-  auto for_chunks = [&](auto &&fn) {
+      for (int k = 0; k < kBatch; ++k)
+        if (c0 + k * kRowThreads < row.chunks) w[k] = load_chunk(row, c0 + k * kRowThreads);
+      if (start) between();
+      start = false;
 #pragma unroll
-    for (int k = 0; k < kKeep; ++k)
-      if (tid + k * kRowThreads < row.chunks) fn(tid + k * kRowThreads, buf[k]);
-    for (int c = tid + kKeep * kRowThreads; c < row.chunks; c += kRowThreads) fn(c, load_chunk(row, c));
+      for (int k = 0; k < kBatch; ++k)
+        if (c0 + k * kRowThreads < row.chunks) fn(c0 + k * kRowThreads, chunk_keys(w[k]));
+    }
+  };
+  auto nothing = [] {};
+  // adds the values of one sign with keys >= from to the histogram; in the pass over
+  // the negative ones the keys' top bit is flipped, so that they are the upper half
+  auto count = [&](int half, uint32_t from) {
+    const uint32_t flip = half ? 0x80008000u : 0u, base = smem_u32(S.hist) - 4 * kBins;
+    uint32_t top2 = 0;                            // two maxima side by side
+    for_chunks([&](int, const uint4 &k) {
+      top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(k.x, k.y)), __vmaxu2(k.z, k.w));
+      const uint4 q = make_uint4(k.x ^ flip, k.y ^ flip, k.z ^ flip, k.w ^ flip);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) count_from(base, chunk_half(q, e), from);
+    }, [&] {
+      for (int k = tid; k < kBins / 4; k += kRowThreads) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    });
+    return max(top2 & 0xffffu, top2 >> 16);
   };
 
-  // ---- the largest value and its first index
+  // ---- the largest value, with the histogram of the values >= 0 on the way
   u64 best = 0;
-  for_chunks([&](int c, const uint4 &w) {
+  if (p.greedy) {
+    for_chunks([&](int c, const uint4 &k) {       // chunks ascend: the first of equal values stays
+      const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w)), t = max(t2 & 0xffffu, t2 >> 16);
+      if (t > static_cast<uint32_t>(best >> 32)) {
+        int x = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int x = row.base + 8 * c + e;
-      if (x >= 0 && x < p.V) best = max(best, argmax_pack(bf16_order_key(static_cast<uint16_t>(chunk_bits(w, e))), x));
-    }
-  });
+        for (int e = 7; e >= 0; --e)
+          if (chunk_half(k, e) == t) x = row.base + 8 * c + e;
+        best = argmax_pack(t, x);
+      }
+    }, nothing);
+  } else {
+    best = argmax_pack(count(0, 0x8000u), 0);
+  }
   best = warp_max(best);
   if (lane == 0) S.red[warp] = best;
   for (int k = tid; k < 257; k += kRowThreads) S.table[k] = kPow2.v[k];
+  if (tid == 0) S.x_cut = p.V;
   __syncthreads();
   best = warp_max(S.red[lane]);
   __syncthreads();
@@ -265,7 +325,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   const float lmax = key_value(kmax);
   const bool fine = lmax > -INFINITY && lmax < INFINITY;              // NaN and infinities: no distribution
   VerifyRow out{};
-  out.argmax = fine ? argmax_index(best) : -1;
+  out.argmax = fine && p.greedy ? argmax_index(best) : -1;
   out.lmax = lmax;
   const int x = i < n ? p.drafts[at] : -1;
   const bool x_ok = x >= 0 && x < p.V;
@@ -279,54 +339,59 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     }
     return;
   }
-  const MassCtx mc = mass_ctx(lmax, p.temperature, S.table);
-  // a value below this has mass 0 (45 ln 2 = 31.2); it is not counted
-  const float lmin = lmax - 32.f * p.temperature;
+  const MassCtx mc = MassCtx{lmax, p.c_hi, p.c_lo, S.table};
+  // a value below l_max - 32 temperature has mass 0 (45 ln 2 = 31.2); it is not counted
+  const uint32_t kmin = bf16_order_key(static_cast<uint16_t>(__float_as_uint(lmax - 32.f * p.temperature) >> 16));
+  const uint32_t kcount = kmin > 0 ? kmin - 1 : 0;   // the smallest key counted (one to spare for the truncation)
   const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f;
 
-  // ---- histograms: value rank d within its sign, the largest first
-  int resident = 0;
-  for (int half = 0; half < 2; ++half) {
+  // ---- counts and masses of rows of 32 neighbouring values, the largest first
+  auto sum_rows = [&](int half, uint32_t from) {
     const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
-    unsigned *rc = S.row_count + half * kBinRows;
-    u64 *rm = S.row_mass + half * kBinRows;
-    if ((half == 0 && kmax < 0x8000u) || (half == 1 && lmin > 0.f)) {   // no value of this sign counts
-      for (int r = tid; r < kBinRows; r += kRowThreads) {
-        rc[r] = 0;
-        rm[r] = 0;
-      }
-      continue;
-    }
-    resident = half;
-    __syncthreads();                              // the last half's counters have been read
-    for (int k = tid; k < kBins / 4; k += kRowThreads) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    for_chunks([&](int, const uint4 &w) {
+    const int r_end = static_cast<int>((0x10000u - from + 31) >> 5);
+    for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
+      unsigned c[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t bits = chunk_bits(w, e);
-        const uint32_t d = top - bf16_order_key(static_cast<uint16_t>(bits));
-        if (d < static_cast<uint32_t>(kBins) && __uint_as_float(bits << 16) >= lmin) atomicAdd(&S.hist[d], 1u);
-      }
-    });
-    __syncthreads();
-    for (int r = warp; r < kBinRows; r += kRowThreads / 32) {
-      const unsigned c = S.hist[r * 32 + lane];
-      unsigned cs = c;
-      u64 ms = 0;
-      if (__any_sync(0xffffffffu, c != 0)) {
-        if (c) ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c;
+      for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
 #pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          cs += __shfl_xor_sync(0xffffffffu, cs, o);
-          ms += __shfl_xor_sync(0xffffffffu, ms, o);
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k * (kRowThreads / 32);
+        unsigned cs = 0;
+        u64 ms = 0;
+        if (r < r_end && __any_sync(0xffffffffu, c[k] != 0)) {
+          ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c[k];
+          cs = __reduce_add_sync(0xffffffffu, c[k]);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
+        }
+        if (lane == 0) {
+          S.row_count[half * kBinRows + r] = cs;
+          S.row_mass[half * kBinRows + r] = ms;
         }
       }
-      if (lane == 0) {
-        rc[r] = cs;
-        rm[r] = ms;
-      }
     }
+    __syncthreads();
+  };
+  int resident = 0;
+  sum_rows(0, 0x8000u);
+  // the negative values: not where none of them counts, nor where the k largest are all >= 0
+  bool negative = kcount <= 0x7fffu;
+  if (use_k && negative) {
+    unsigned c = __reduce_add_sync(0xffffffffu, S.row_count[tid]);
+    if (lane == 0) S.red[warp] = c;
+    __syncthreads();
+    c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(S.red[lane]));
+    negative = c < static_cast<unsigned>(p.top_k);
+    __syncthreads();
+  }
+  if (negative) {
+    resident = 1;
+    count(1, kcount + 0x8000u);
+    __syncthreads();
+    sum_rows(1, kcount + 0x8000u);
+  } else {
+    S.row_count[kBinRows + tid] = 0;
+    S.row_mass[kBinRows + tid] = 0;
   }
   __syncthreads();
   // prefix sums over the 2048 rows of values, two for each thread
@@ -339,18 +404,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   // the counters of one row of 32 values, into S.bins
   auto fetch_bins = [&](int r) {
     const bool here = r / kBinRows == resident;
-    if (tid < 32) S.bins[tid] = here ? S.hist[(r % kBinRows) * 32 + tid] : 0u;
+    if (tid < 32) S.bins[tid] = here ? S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)] : 0u;
     __syncthreads();
     if (here) return;
     const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
-    for_chunks([&](int, const uint4 &w) {
+    for_chunks([&](int, const uint4 &k) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t bits = chunk_bits(w, e);
-        const uint32_t d = top - bf16_order_key(static_cast<uint16_t>(bits));
-        if (d < 32u && __uint_as_float(bits << 16) >= lmin) atomicAdd(&S.bins[d], 1u);
+        const uint32_t d = top - chunk_half(k, e);
+        if (d < 32u) atomicAdd(&S.bins[d], 1u);
       }
-    });
+    }, nothing);
     __syncthreads();
   };
   auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
@@ -397,10 +461,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   }
   // ---- top-p: the value at which the running mass first exceeds top_p of the whole
   if (use_p) {
-    const double goal = static_cast<double>(p.top_p) * static_cast<double>(z);
-    auto over = [&](u64 v) { return static_cast<double>(v) > goal; };
-    if (tid == 0) S.found = -1;
+    if (tid == 0) {
+      S.found = -1;
+      S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
+    }
     __syncthreads();
+    const u64 goal = S.t_cut;                     // a whole sum exceeds top_p z iff it exceeds its floor
+    auto over = [&](u64 v) { return v > goal; };
     if (!over(pm) && over(pm + m0 + m1)) {
       const bool second = !over(pm + m0);
       S.found = 2 * tid + second;
@@ -423,8 +490,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
         if (lane == bin) {
           // equal values have equal masses: the first t + 1 of them in index order stay
           const u64 above = S.before_mass + mi - m;
-          const double t = floor((goal - static_cast<double>(above)) / static_cast<double>(one));
-          const u64 tc = t <= 0.0 ? 0 : t >= static_cast<double>(c) ? c - 1 : static_cast<u64>(t);
+          const u64 tc = min((goal - above) / one, static_cast<u64>(c - 1));
           S.bin = bin;
           S.t_cut = tc + 1 < c ? tc : ~0ull;      // ~0: all of them
           S.z = above + (tc + 1) * one;
@@ -438,21 +504,20 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       if (tc != ~0ull) {
         // the index of the (t + 1)-th token of this value: counts in vocabulary
         // order, a round of 1024 chunks at a time
-        if (tid == 0) S.x_cut = p.V;
         u64 seen = 0;
         for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
           const int c = c_first + tid;
-          uint4 w = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-          if (c < row.chunks) w = load_chunk(row, c);
+          uint4 k = make_uint4(0, 0, 0, 0);       // key 0 is a NaN, never the cut
+          if (c < row.chunks) k = chunk_keys(load_chunk(row, c));
           unsigned mine = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mine += bf16_order_key(static_cast<uint16_t>(chunk_bits(w, e))) == v;
+          for (int e = 0; e < 8; ++e) mine += chunk_half(k, e) == v;
           u64 all;
           u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
           if (rank <= tc && tc < rank + mine) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              if (bf16_order_key(static_cast<uint16_t>(chunk_bits(w, e))) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
+              if (chunk_half(k, e) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
           }
           seen += all;
           if (seen > tc) break;                   // the same for every thread
@@ -484,7 +549,8 @@ __device__ __forceinline__ u64 ld_cluster_u64(const u64 *local, uint32_t rank) {
 
 __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThreads)
     verify_choice_kernel(const VerifyParams p) {
-  __shared__ u64 red[33], table[257], my_total;
+  __shared__ u64 red[33], my_total;
+  __shared__ float2 table[257];
   __shared__ int s_refused;
   const int tid = threadIdx.x;
   const int b = blockIdx.x / kChoiceCtas;
@@ -493,20 +559,20 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   const int n = p.n_draft ? min(max(p.n_draft[b], 0), p.T) : p.T;
   if (tid == 0) s_refused = n;
   __syncthreads();
+  // u q of draft tid (T is at most the threads), before the rows are there
+  double uq = 0.0;
+  if (tid < n && !p.greedy) {
+    const long long at = static_cast<long long>(b) * p.T + tid;
+    const int x = p.drafts[at];
+    const float q = !p.probs ? 1.f : x >= 0 && x < p.V ? p.probs[at * p.ldq + x] : 0.f;
+    uq = static_cast<double>(p.uniform[static_cast<long long>(b) * (p.T + 1) + tid]) * static_cast<double>(q);
+  }
   griddep_wait();
   const VerifyRow *rows = p.rows + static_cast<long long>(b) * (p.T + 1);
   // ---- the first draft that does not stay: u q < p as u q z < mass
-  for (int i = tid; i < n; i += kChoiceThreads) {
-    const VerifyRow r = rows[i];
-    const long long at = static_cast<long long>(b) * p.T + i;
-    bool stays = r.mx != 0;
-    if (!p.greedy && stays) {
-      const int x = p.drafts[at];                 // in the vocabulary: it has a mass
-      const double q = p.probs ? static_cast<double>(p.probs[at * p.ldq + x]) : 1.0;
-      const double u = p.uniform[static_cast<long long>(b) * (p.T + 1) + i];
-      stays = u * q * static_cast<double>(r.z) < static_cast<double>(r.mx);
-    }
-    if (!stays) atomicMin(&s_refused, i);
+  if (tid < n) {
+    const VerifyRow r = rows[tid];
+    if (r.mx == 0 || !(p.greedy || uq * static_cast<double>(r.z) < static_cast<double>(r.mx))) atomicMin(&s_refused, tid);
   }
   __syncthreads();
   const int kept = s_refused;
@@ -518,43 +584,68 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   }
   // ---- the draw
   const Row row = make_row(p.logits + (static_cast<long long>(b) * (p.T + 1) + kept) * p.ld, p.V);
-  const MassCtx mc = mass_ctx(r.lmax, p.temperature, table);
+  const MassCtx mc = MassCtx{r.lmax, p.c_hi, p.c_lo, table};
   const long long at = static_cast<long long>(b) * p.T + kept;
   const bool refused = kept < n;
   const float *q = refused && p.probs ? p.probs + at * p.ldq : nullptr;
   const int gone = refused && !p.probs ? p.drafts[at] : -1;           // q is 1 there: nothing is left of p
-  const int per = (row.chunks + kChoiceCtas - 1) / kChoiceCtas;
-  const int first = min(row.chunks, static_cast<int>(rank) * per), last = min(row.chunks, first + per);
+  // this thread's chunks, in vocabulary order across the cluster
+  const int per = (row.chunks + kChoiceCtas * kChoiceThreads - 1) / (kChoiceCtas * kChoiceThreads);
+  const int first = min(row.chunks, (static_cast<int>(rank) * kChoiceThreads + tid) * per), last = min(row.chunks, first + per);
   bool rest = refused;                            // weights max(p - q, 0), else p
+  // max(m - q z, 0), the product as a sum of two floats (z = zh + zl to 2^-48, so it
+  // is off by less than a unit where it matters, next to a mass of at most 2^44)
+  const float zh = __ull2float_rn(r.z);
+  const float zl = __ll2float_rn(static_cast<long long>(r.z - __float2ull_rn(zh)));
+  auto less = [&](u64 m, float qx) -> u64 {
+    constexpr float kMagic = 12582912.f;
+    const float ph = __fmul_rn(qx, zh), pl = __fmaf_rn(qx, zl, __fmaf_rn(qx, zh, -ph));
+    if (!(ph > 0.f)) return m;                    // also a NaN
+    if (ph >= 17592186044416.f) return 0;         // 2^44: no mass is larger
+    const float his = __fmaf_rn(ph, 1.1920928955078125e-7f, kMagic);
+    const float los = __fadd_rn(__fadd_rn(__fmaf_rn(__fsub_rn(his, kMagic), -8388608.f, ph), pl), kMagic);
+    const long long have = static_cast<long long>(__float_as_int(his) - 0x4b400000) * 8388608ll + (__float_as_int(los) - 0x4b400000);
+    const long long left = static_cast<long long>(m) - have;
+    return left > 0 ? static_cast<u64>(left) : 0;
+  };
+  const uint32_t vcut2 = r.vcut | (r.vcut << 16);
   auto weights = [&](int c, u64 (&w)[8]) -> u64 {
-    const uint4 bits = load_chunk(row, c);
+    const uint4 keys = chunk_keys(load_chunk(row, c));
+    const uint32_t t2 = __vmaxu2(__vmaxu2(keys.x, keys.y), __vmaxu2(keys.z, keys.w));
     u64 sum = 0;
+    if (__vmaxu2(t2, vcut2) == vcut2 && (t2 & 0xffffu) != r.vcut && (t2 >> 16) != r.vcut) {
+      // none of the eight stays
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 0;
+      return 0;
+    }
+    const int x0 = row.base + 8 * c;
+    float qv[8];
+    if (rest && q) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) qv[e] = x0 + e >= 0 && x0 + e < p.V ? q[x0 + e] : 0.f;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t u = chunk_bits(bits, e);
-      const int x = row.base + 8 * c + e;
-      const uint32_t key = bf16_order_key(static_cast<uint16_t>(u));
-      u64 m = 0;
-      if ((key > r.vcut || (key == r.vcut && x <= r.xcut)) && x >= 0 && x < p.V) {
-        m = mass_of(mc, __uint_as_float(u << 16));
-        if (rest && m) {
-          const u64 have = q ? scaled_floor(q[x], r.z) : x == gone ? m : 0;
-          m = m > have ? m - have : 0;
-        }
-      }
+      const int x = x0 + e;
+      const uint32_t key = chunk_half(keys, e);
+      u64 m = mass_of(mc, key_value(key));        // 0 outside the row: -infinity
+      if (key < r.vcut || (key == r.vcut && x > r.xcut)) m = 0;
+      if (rest) m = q ? less(m, qv[e]) : x == gone ? 0 : m;
       w[e] = m;
       sum += m;
     }
     return sum;
   };
-  u64 w[8], before = 0, whole = 0;
+  u64 w[8], mine, before, whole;                  // this thread's mass, that of all before it, and the whole
   while (true) {
-    u64 mine = 0, all;
-    for (int c = first + tid; c < last; c += kChoiceThreads) mine += weights(c, w);
-    block_scan<kChoiceThreads>(mine, red, &all);
+    u64 all;
+    mine = 0;
+#pragma unroll 2
+    for (int c = first; c < last; ++c) mine += weights(c, w);
+    before = block_scan<kChoiceThreads>(mine, red, &all);
     if (tid == 0) my_total = all;
     cluster_sync_all();
-    before = 0;
     whole = 0;
 #pragma unroll
     for (int k = 0; k < kChoiceCtas; ++k) {
@@ -568,24 +659,14 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   }
   // the first token whose running sum exceeds u * whole, i.e. floor(u * whole)
   const u64 goal = min(scaled_floor(p.uniform[static_cast<long long>(b) * (p.T + 1) + p.T], whole), whole - 1);
-  u64 running = before;
-  if (goal < before) return;                      // in an earlier eighth
-  for (int c0 = first; c0 < last; c0 += kChoiceThreads) {
-    const int c = c0 + tid;
-    u64 all, sum = 0;
+  if (goal < before || goal >= before + mine) return;
+  for (int c = first; c < last; ++c) {
+    weights(c, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 0;
-    if (c < last) sum = weights(c, w);
-    u64 s = running + block_scan<kChoiceThreads>(sum, red, &all);
-    if (s <= goal && goal < s + sum) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (s <= goal && goal < s + w[e]) p.next[b] = row.base + 8 * c + e;
-        s += w[e];
-      }
+    for (int e = 0; e < 8; ++e) {
+      if (before <= goal && goal < before + w[e]) p.next[b] = row.base + 8 * c + e;
+      before += w[e];
     }
-    running += all;
-    if (goal < running) return;                   // the same for every thread
   }
 }
 

@@ -24,6 +24,7 @@ struct VerifyParams {
   long long ldq;
   int B, T, V;
   float temperature, top_p;
+  float c_hi, c_lo;            // log2(e) / temperature as a sum of two floats
   int top_k, greedy;
   const float *uniform;        // [B, T + 1]
   int *n_accepted, *next;      // [B]

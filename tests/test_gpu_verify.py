@@ -130,6 +130,19 @@ def test_flat_and_tied_rows(S):
             check(S, logits, drafts, u, None, **kw)
 
 
+def test_zeros_of_both_signs_are_equal(S):
+    B, T, V = 12, 2, 3000
+    g = torch.Generator("cuda").manual_seed(21)
+    _, drafts, u, probs = case(B, T, V, seed=7)
+    logits = torch.randint(-1, 2, (B, T + 1, V), generator=g, device="cuda").float()
+    logits = torch.where(torch.rand(logits.shape, generator=g, device="cuda") < 0.5, -logits.abs().neg(), logits * 0.0)
+    logits = (logits * torch.where(torch.rand(logits.shape, generator=g, device="cuda") < 0.5, -1.0, 1.0)).to(torch.bfloat16)
+    assert bool((torch.signbit(logits) & (logits == 0)).any()) and bool((~torch.signbit(logits) & (logits == 0)).any())
+    for kw in (dict(), dict(top_k=1500), dict(top_p=0.66666), dict(top_p=0.5001, top_k=2000)):
+        check(S, logits, drafts, u, probs, **kw)
+    check(S, torch.where(logits > 0, -logits, logits), drafts, u, None, do_sample=False)   # the zeros are the maximum
+
+
 def test_masked_and_extreme_logits(S):
     B, T, V = 6, 3, 3000
     logits, drafts, u, probs = case(B, T, V, seed=2)

@@ -25,7 +25,7 @@ def test_refusals(S):
     for kw in (dict(logits=None), dict(drafts=None), dict(n_accepted=None), dict(next=None), dict(ws=None), dict(uniform=None),
                dict(B=0), dict(T=0), dict(V=0), dict(ld=99), dict(ldq=99), dict(temperature=nan), dict(top_p=nan), dict(temperature=inf)):
         assert call(S, **kw) == -1, kw
-    for kw in (dict(V=(1 << 19) + 1, ld=1 << 20, ldq=1 << 20), dict(B=1 << 24, T=1)):
+    for kw in (dict(V=(1 << 19) + 1, ld=1 << 20, ldq=1 << 20), dict(B=1 << 24, T=1), dict(T=513)):
         assert call(S, **kw) == -2, kw
     for kw in (dict(logits=P + 1), dict(drafts=P + 2), dict(n_draft=P + 1), dict(probs=P + 2), dict(uniform=P + 1), dict(next=P + 3),
                dict(n_accepted=P + 1), dict(p_draft=P + 2), dict(ws=P + 8)):
