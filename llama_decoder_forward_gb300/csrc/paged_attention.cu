@@ -123,7 +123,7 @@ cudaError_t launch_combine(const PagedAttnParams &p, int rows, cudaStream_t st) 
 // Rows of a unit: the tile of the kernel that takes the call.
 static int unit_rows(int G, int T) {
   const long long r = (long long)T * G;
-  return r <= 16 ? 16 : r <= 32 ? 32 : 256;
+  return r <= 16 ? 16 : 256;
 }
 
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {

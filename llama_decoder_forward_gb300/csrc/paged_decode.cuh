@@ -53,11 +53,6 @@ __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__device__ __forceinline__ void cp_async4(void *smem, const void *gmem, bool valid) {
-  const int sz = valid ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem)), "l"(gmem), "r"(sz) : "memory");
-}
-
 // A pair of q's values (bf16, or f16 rounded to bf16).
 __device__ __forceinline__ uint32_t pd_q2(const uint8_t *q, long long off, int f16_q) {
   const uint32_t u = *reinterpret_cast<const uint32_t *>(q + off * 2);

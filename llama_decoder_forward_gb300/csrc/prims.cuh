@@ -260,6 +260,11 @@ __device__ __forceinline__ void cp_async16(void *smem, const void *gmem, bool va
                "r"(sz)
                : "memory");
 }
+// The same for 4 bytes.
+__device__ __forceinline__ void cp_async4(void *smem, const void *gmem, bool valid) {
+  const int sz = valid ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem)), "l"(gmem), "r"(sz) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -560,6 +565,19 @@ __device__ __forceinline__ float2 fadd2(float a0, float a1, float b0, float b1) 
       "mov.b64 ra, {%2, %3};\n\t"
       "mov.b64 rb, {%4, %5};\n\t"
       "add.rn.f32x2 rd, ra, rb;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+  return d;
+}
+
+// (a0 * b0, a1 * b1) on the packed two-lane fp32 path (one instruction).
+__device__ __forceinline__ float2 fmul2(float a0, float a1, float b0, float b1) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %5};\n\t"
+      "mul.rn.f32x2 rd, ra, rb;\n\t"
       "mov.b64 {%0, %1}, rd;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
