@@ -113,7 +113,11 @@ bool make_tmap_f16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t c
 // swizzle or none.
 bool make_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                   uint64_t row_pitch_elems, uint32_t box_cols, uint32_t box_rows, bool swizzle128);
-// The same through a small per-process cache keyed by (device, arguments):
+// Map of `rank` (2 to 5) dimensions of bf16 (2 bytes) or bytes, the innermost contiguous; swizzle of
+// 128, 64 or 0 bytes.
+bool make_tmap_nd(CUtensorMap *map, const void *base, int elem_bytes, int rank, const uint64_t *dims,
+                  const uint64_t *stride_bytes, const uint32_t *box, int swizzle_bytes);
+// make_tmap_f16 and make_tmap_2d through a small per-process cache keyed by (device, arguments):
 // encoding is a host call of a few microseconds, and the same buffers recur on
 // every forward.
 bool get_tmap_f16(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,

@@ -997,6 +997,25 @@ static EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
+bool make_tmap_nd(CUtensorMap *map, const void *base, int elem_bytes, int rank, const uint64_t *dims,
+                  const uint64_t *stride_bytes, const uint32_t *box, int swizzle_bytes) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc || rank < 2 || rank > 5) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = stride_bytes[i];
+  }
+  return enc(map, elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+             const_cast<void *>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_2d(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                   uint64_t row_pitch_elems, uint32_t box_cols, uint32_t box_rows, bool swizzle128) {
   EncodeTiledFn enc = get_encode_fn();

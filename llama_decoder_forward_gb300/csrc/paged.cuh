@@ -90,7 +90,7 @@ struct PagedAttnParams {
   int H, G;                    // query heads, query heads per kv head
   float scale_log2;            // scale * log2(e)
   int window;                  // > 0: position p sees j > p - window only
-  int q_f16;                   // q and out are f16 (the library's own blocks), else bf16
+  int o_f16;                   // out is f16 (the library's own blocks), else bf16
   int tt, bk_shift;            // query tokens of a unit, log2 of the keys of a tile (paged_sched.cuh)
   int ctas;                    // CTAs that share the work
   unsigned long long wait_ns;  // limit of the bounded waits

@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const Paged
         p.o.data + (paged_unit_row(p.o, p, s, mine.b, t0, mine.kvh, r) + lane * (HD / 32)) * 2);
 #pragma unroll
     for (int e = 0; e < HD / 64; ++e)
-      out[e] = p.q_f16 ? pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      out[e] = p.o_f16 ? pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
     __syncwarp();                                 // the weights are rewritten
   }
 }
@@ -123,7 +123,7 @@ cudaError_t launch_combine(const PagedAttnParams &p, int rows, cudaStream_t st) 
 // Rows of a unit: the tile of the kernel that takes the call.
 static int unit_rows(int G, int T) {
   const long long r = (long long)T * G;
-  return r <= 16 ? 16 : 256;
+  return r <= 16 ? 16 : r <= 128 ? 128 : 256;
 }
 
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {
@@ -136,10 +136,10 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   const int rows = unit_rows(p.G, p.c.T);
   p.tt = rows / p.G;
   const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64, one = rows == 16;
-  p.bk_shift = rows == 256 || !(h64 || f8) ? 7 : 8;
+  p.bk_shift = rows >= 128 || !(h64 || f8) ? 7 : 8;
   cudaError_t e;
   prof_before(SMOL_K_DEC_ATTN, st);
-  if (rows == 256) {
+  if (rows >= 128) {
     e = launch_paged_tiles(p, st);
   } else if (h64) {
     if (f8) e = one ? launch_few<64, true, 1>(p, st) : launch_few<64, true, 2>(p, st);

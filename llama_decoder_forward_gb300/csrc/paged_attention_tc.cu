@@ -14,18 +14,23 @@
 // warpgroup that holds S may rescale O.  It does so only when a row's maximum grows
 // by more than 2^8 (P then stays below 256, exact in the fp32 sums).
 //
-// K and V come from pages of 16 tokens and more, so four loader warps copy 16
-// rows at a time (one page number each) with 16-byte asynchronous copies into the
-// swizzled operand layout.  Rows outside the sight of the unit, or on a page that
-// is not there, are filled with zeros: whatever lies in unused slots, P = 0 meets
-// V = 0.  e4m3 codes are copied ahead and become bf16 exactly on the way to the
-// operand tiles; the keys' scales multiply the scores, the values' scales P.
+// K and V of bf16 pages, and Q, come by TMA straight into the swizzled operand
+// layout: a box for each page of a key tile (up to 128 of its rows), the tokens and
+// heads of the unit for Q.  A page number outside the pool is a coordinate outside
+// the tensor: zeros.  Where a tile reaches past what the unit's rows see, a second
+// warp sets V's rows there to zero before the tensor core reads them: whatever lies
+// in unused slots, P = 0 meets V = 0.  (Copies by the loader's threads, 16 bytes
+// each, took 4,600 cycles for a tile of 64 KB: more than its 32 MMAs.)
+// e4m3 codes are copied ahead by bulk copies, as they lie, and four warps turn them
+// into bf16 on the way to the operand tiles, exactly; the keys' scales multiply the
+// scores, the values' scales P.
 //
-// The loaders alone walk the schedule and leave a note of each tile beside its K:
-// the walk's registers would have been spilled in the other roles (the issuing
-// thread then took 140 cycles for each MMA).  Registers: 512 threads start with 128
-// each; the softmax warpgroups take 184 or more (their 128 scores stay in
-// registers), the loaders and the issuer give up theirs.
+// One warp alone walks the schedule for the MMA issuer and the softmax, and leaves a
+// note of each tile beside its K: the walk's registers would have been spilled in
+// those roles.  Registers: 512 threads start with 128 each; the softmax warpgroups
+// take 184 or more (their 128 scores stay in registers), the others give up theirs.
+// NQ: query tiles of a unit; a call whose units have at most 128 rows leaves the
+// second tile's shared memory to more stages.
 #include <math.h>
 
 #include "paged_sched.cuh"
@@ -35,33 +40,32 @@ namespace {
 
 constexpr int kTileK = 128;
 
-// What the other roles need to know of a key tile, written by the loaders with K.
+// What the other roles need to know of a key tile, written by the loader with K.
 struct PtInfo {
   int flags;                   // kPt*
   int x0;                      // its first position
   int first_at, rows;          // position of the unit's first row; query rows of the unit
   long long o_base;            // element offset of the unit's first row in out
-  int b, qt, kvh, pad;
+  int b, qt, kvh;
+  int valid;                   // first and behind the last of its keys that some row sees (16 bits each)
 };
-enum : int { kPtNew = 1, kPtTwo = 2, kPtUnitLast = 4, kPtEnds = 8, kPtLast = 16, kPtInUnit = 32 };
+enum : int { kPtNew = 1, kPtTwo = 2, kPtUnitLast = 4, kPtEnds = 8, kPtLast = 16, kPtInUnit = 32, kPtEdge = 64 };
 
-template <int HD, bool FP8>
+template <int HD, bool FP8, int NQ>
 struct PtCfg {
   static constexpr int THREADS = 512;
   static constexpr int NSUB = HD / 64;                       // 64-column sub-tiles
-  static constexpr int TILE_BYTES = 128 * HD * 2;            // a Q, K or V tile, bf16
-  static constexpr int NST = HD == 64 ? (FP8 ? 3 : 4) : 2;   // K and V stages
-  static constexpr int SD = HD == 64 ? 3 : 1;                // tiles of codes under way (e4m3)
-  static constexpr int NCH = HD / 16;                        // 16-byte pieces of codes of a tensor's tile for each loader thread
-  static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = 2 * TILE_BYTES;
+  static constexpr int TILE_BYTES = 128 * HD * 2;            // a K or V tile, bf16
+  static constexpr int NST = HD == 64 ? 4 : (NQ == 1 && !FP8) ? 3 : 2;   // K and V stages
+  static constexpr int SD = HD == 64 ? 3 : NQ == 1 ? 2 : 1;  // tiles of codes under way (e4m3)
+  static constexpr int OFF_Q = 0;                            // [NSUB][NQ * 128 rows][64]
+  static constexpr int OFF_K = NQ * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + NST * TILE_BYTES;
-  static constexpr int OFF_CODES = OFF_V + NST * TILE_BYTES; // [SD][K, V][NCH][128 threads] 16 bytes
-  static constexpr int OFF_CSC = OFF_CODES + (FP8 ? SD * 2 * NCH * 2048 : 0);  // [SD][K, V][128] their scales, if SD > 1
-  static constexpr int OFF_SC = OFF_CSC + (FP8 && SD > 1 ? SD * 1024 : 0);     // [NST][2][128] scales of keys and values
+  static constexpr int OFF_CODES = OFF_V + NST * TILE_BYTES; // [SD][K, V][128 keys][HD]
+  static constexpr int OFF_SC = OFF_CODES + (FP8 ? SD * 2 * 128 * HD : 0);     // [NST][2][128] scales of keys and values
   static constexpr int OFF_INFO = OFF_SC + (FP8 ? NST * 2 * 128 * 4 : 0);
   static constexpr int OFF_BAR = OFF_INFO + NST * sizeof(PtInfo);
-  static constexpr int NBAR = 2 + 4 * NST + 2 + 2 + 2 + 1;
+  static constexpr int NBAR = 2 + 5 * NST + 4 * SD + 2 + 2 + 2 + 1;
   static constexpr int USED = OFF_BAR + NBAR * 8 + 16;
   // the tiles want 1024-byte alignment; the block has no other shared memory, so its
   // own usually starts there (checked)
@@ -87,10 +91,12 @@ __device__ __forceinline__ uint4 pt_codes8(uint32_t a, uint32_t b) {
                     pt_code_pair(__byte_perm(b, 0, 0x1404)), pt_code_pair(__byte_perm(b, 0, 0x3424)));
 }
 
-template <int HD, bool FP8>
-__global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnParams p) {
-  using C = PtCfg<HD, FP8>;
-  constexpr int NST = C::NST, NSUB = C::NSUB;
+template <int HD, bool FP8, int NQ>
+__global__ void __launch_bounds__(512, 1)
+    paged_tiles_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p) {
+  using C = PtCfg<HD, FP8, NQ>;
+  constexpr int NST = C::NST, NSUB = C::NSUB, SD = C::SD;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *sQ = smem + C::OFF_Q, *sK = smem + C::OFF_K, *sV = smem + C::OFF_V;
@@ -98,7 +104,9 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
   PtInfo *sInfo = reinterpret_cast<PtInfo *>(smem + C::OFF_INFO);
   uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR), *q_empty = q_full + 1;
   uint64_t *k_full = q_empty + 1, *k_empty = k_full + NST, *v_full = k_empty + NST, *v_empty = v_full + NST;
-  uint64_t *s_full = v_empty + NST, *p_full = s_full + 2, *o_full = p_full + 2, *drain = o_full + 2;
+  uint64_t *v_raw = v_empty + NST, *c_full = v_raw + NST;   // V landed but not yet cleared; codes of K and V landed [SD][2]
+  uint64_t *c_empty = c_full + 2 * SD;            // and read by the four converting warps
+  uint64_t *s_full = c_empty + 2 * SD, *p_full = s_full + 2, *o_full = p_full + 2, *drain = o_full + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
@@ -119,13 +127,18 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
     return;
   }
   if (tid == 0) {
-    mbar_init(q_full, 128);
+    mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&k_full[i], 128 + 1);             // and the note of the tile
-      mbar_init(&k_empty[i], 1 + 8);              // the S MMAs, and each softmax warp has read the tile's info
-      mbar_init(&v_full[i], 128);
+      mbar_init(&k_full[i], FP8 ? 128 : 1);
+      mbar_init(&k_empty[i], FP8 ? 1 + 8 : 1 + 9);   // the S MMAs, and each reader of the tile's note
+      mbar_init(&v_full[i], FP8 ? 128 : 1);
       mbar_init(&v_empty[i], 1);
+      mbar_init(&v_raw[i], 1);
+    }
+    for (int i = 0; i < 2 * SD; ++i) {
+      mbar_init(&c_full[i], 1);
+      mbar_init(&c_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
@@ -161,7 +174,7 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < HD / 16; ++k) {
-            const uint64_t a = dq + ((h * C::TILE_BYTES + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
+            const uint64_t a = dq + (((k >> 2) * (NQ * 128 * 128) + h * (128 * 128) + (k & 3) * 32) >> 4);
             const uint64_t b = dk + ((kst * C::TILE_BYTES + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
             umma_f16(tmem + kColS + h * 128, a, b, kIdS, k > 0);
           }
@@ -177,7 +190,6 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
           if (!mbar_wait_bounded(q_full, units & 1, abort_flag, limit)) return false;
           ++units;
         }
-        if (!FP8) fence_proxy_async_smem();       // the asynchronous copies' writes, before the tensor core reads them
         tc_fence_after_sync();
         return true;
       };
@@ -203,7 +215,6 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
         const int f = f_next;
         const bool last = f & kPtLast;
         if (!mbar_wait_bounded(&v_full[vst], vph, abort_flag, limit)) { ok = false; break; }
-        if (!FP8) fence_proxy_async_smem();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 0 || (f & kPtTwo)) {
@@ -250,210 +261,251 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
     setmaxnreg_dec<C::R_LOAD>();
     // ------------------------------------------------------------------ loaders
     const int lt = tid - 256;
+    const bool lead = warp == 8;
     bool ok = true, in_unit = it.j > it.j0, new_unit = true;
     int st = 0;
     uint32_t ph = 1, units = 0;                   // the stages start empty
-    // page numbers of a tile: lane i < 8 of each warp has that of keys 16 i ..; fetched ahead
+    const int box = min(1 << p.kv.page_shift, kTileK), n_box = kTileK / box;   // rows of a page in a tile, pages of a tile
+    // page numbers of a tile: lane i < n_box of the warp has that of keys i * box ..; -1: not in
+    // sight, P: no such page
     auto fetch_pages = [&](const PagedIter &u) {
-      const int x = u.j * kTileK + 16 * (lane & 7);
+      const int x = u.j * kTileK + box * lane;
       int page = -1;
-      if (x < u.hi && x + 16 > u.lo) {
+      if (lane < n_box && x < u.hi && x + box > u.lo) {
         page = paged_page(p.kv, u.b, x);
         if (page < 0 || page >= p.kv.P) {
           set_status(p.status, kDevBadInput);
-          page = -1;
+          page = p.kv.P;
         }
       }
       return page;
     };
-    auto write_info = [&](bool last) {
-      if (lt == 0) {
-        PtInfo f;
-        const bool ends = it.j + 1 == it.j1;
-        f.rows = it.nt * p.G;
-        f.flags = (new_unit ? kPtNew : 0) | (f.rows > 128 ? kPtTwo : 0) | (ends || last ? kPtUnitLast : 0) | (ends ? kPtEnds : 0) |
-                  (last ? kPtLast : 0) | (in_unit ? kPtInUnit : 0);
-        f.x0 = it.j * kTileK;
-        f.first_at = it.s.L + it.t0;
-        f.o_base = paged_row_off(p.o, p.c, it.s, it.b, it.t0, it.kvh * p.G);
-        f.b = it.b;
-        f.qt = it.qt;
-        f.kvh = it.kvh;
-        sInfo[st] = f;
-        mbar_arrive(&k_full[st]);
-      }
+    auto write_info = [&](bool last) {            // one lane
+      PtInfo f;
+      const bool ends = it.j + 1 == it.j1;
+      f.x0 = it.j * kTileK;
+      f.rows = it.nt * p.G;
+      f.valid = max(0, it.lo - f.x0) | (min(kTileK, it.hi - f.x0) << 16);
+      f.flags = (new_unit ? kPtNew : 0) | (f.rows > 128 ? kPtTwo : 0) | (ends || last ? kPtUnitLast : 0) | (ends ? kPtEnds : 0) |
+                (last ? kPtLast : 0) | (in_unit ? kPtInUnit : 0) | (f.valid != kTileK << 16 ? kPtEdge : 0);
+      f.first_at = it.s.L + it.t0;
+      f.o_base = paged_row_off(p.o, p.c, it.s, it.b, it.t0, it.kvh * p.G);
+      f.b = it.b;
+      f.qt = it.qt;
+      f.kvh = it.kvh;
+      sInfo[st] = f;
     };
-    // Q of the unit, both query tiles (rows past its last are zeros)
-    auto load_q = [&]() {
-      const int rows = it.nt * p.G, row16 = lt >> 3, c8 = lt & 7;
-      const int used = (rows + 127) & ~127;
-#pragma unroll 2
-      for (int r = row16; r < used; r += 16) {
-        const long long base = r < rows ? paged_unit_row(p.q, p, it.s, it.b, it.t0, it.kvh, r) : 0;
-        uint8_t *dst = sQ + (r >> 7) * C::TILE_BYTES + (r & 127) * 128 + ((c8 ^ (r & 7)) << 4);
+    // Q of the unit: its tokens' heads are the rows, in both tiles (rows past the sequence's last
+    // are whatever follows them, or zeros: they reach no other row)
+    auto load_q = [&]() {                         // one lane
+      mbar_arrive_expect_tx(q_full, NSUB * 128 * p.tt * p.G);
 #pragma unroll
-        for (int sub = 0; sub < NSUB; ++sub) {
-          uint4 w = make_uint4(0, 0, 0, 0);
-          if (r < rows) {
-            w = *reinterpret_cast<const uint4 *>(p.q.data + (base + sub * 64 + c8 * 8) * 2);
-            if (p.q_f16) {
-              uint32_t *u = reinterpret_cast<uint32_t *>(&w);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_f16x2(u[e]);
-                u[e] = pack_bf16x2(f.x, f.y);
-              }
-            }
-          }
-          *reinterpret_cast<uint4 *>(dst + sub * (128 * 128)) = w;
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
+      for (int sub = 0; sub < NSUB; ++sub)
+        tma_load_4d(sQ + sub * (NQ * 128 * 128), &tmQ, q_full, sub * 64, it.kvh * p.G, static_cast<int>(it.s.row0) + it.t0,
+                    p.c.row_start ? 0 : it.b);
     };
     if constexpr (!FP8) {
-      const int row16 = lt >> 3, c8 = lt & 7;     // row of 16, 16-byte piece of 128 bytes
-      // 16 rows at a time: one page, one base address, constant steps in shared memory
-      auto copy = [&](uint8_t *dst, const uint8_t *src, int pages) {
-        uint8_t *row = dst + row16 * 128 + ((c8 ^ (row16 & 7)) << 4);
-        const int x = it.j * kTileK + row16;
+      if (lead) {
+        // a box for each page and 64 columns; every lane issues its own page's
+        auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int page) {
+          const unsigned in = __ballot_sync(0xffffffffu, page >= 0);
+          if (lane == 0) mbar_arrive_expect_tx(bar, __popc(in) * box * HD * 2);
+          __syncwarp();
+          if (page >= 0) {
+            const int y = (it.kvh << p.kv.page_shift) + ((it.j * kTileK) & ((1 << p.kv.page_shift) - 1));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int page = __shfl_sync(0xffffffffu, pages, i);
-          const bool in = page >= 0 && x + 16 * i >= it.lo && x + 16 * i < it.hi;
-          const uint8_t *from = src + ((in ? paged_slot(p.kv, page, x + 16 * i, it.kvh) : 0) * HD + c8 * 8) * 2;
-#pragma unroll
-          for (int sub = 0; sub < NSUB; ++sub) cp_async16(row + sub * (128 * 128) + i * 2048, from + sub * 128, in);
+            for (int sub = 0; sub < NSUB; ++sub) tma_load_3d(dst + sub * (128 * 128) + lane * box * 128, map, bar, sub * 64, y, page);
+          }
+          __syncwarp();
+        };
+        int pages = fetch_pages(it);
+        uint32_t nk = 0, nv = 0, edges = 0, raw = 0;   // tiles asked for; stages whose V went to v_raw, and its phase
+        while (true) {
+          PagedIter nx = it;
+          paged_next(p, nx);
+          const bool last = it.left == 1;
+          const int cur = pages;
+          if (!last) pages = fetch_pages(nx);     // in use from the next round on
+          if (!mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit)) { ok = false; break; }
+          if (lane == 0) write_info(last);        // before this lane's arrival in copy()
+          copy(sK + st * C::TILE_BYTES, &tmK, &k_full[st], cur);
+          ++nk;
+          if (new_unit) {                         // Q behind the unit's first keys
+            if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
+            if (lane == 0) load_q();
+            __syncwarp();
+            ++units;
+          }
+          if (!mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit)) { ok = false; break; }
+          const bool edge = it.lo > it.j * kTileK || it.hi < (it.j + 1) * kTileK;
+          copy(sV + st * C::TILE_BYTES, &tmV, edge ? &v_raw[st] : &v_full[st], cur);
+          ++nv;
+          edges = (edges & ~(1u << st)) | (edge ? 1u << st : 0u);
+          if (edge) raw ^= 1u << st;
+          if (++st == NST) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (last) break;
+          new_unit = it.j + 1 == it.j1;
+          if (new_unit) in_unit = false;
+          it = nx;
         }
-      };
-      int pages = fetch_pages(it);
-      while (true) {
-        PagedIter nx = it;
-        paged_next(p, nx);
-        const bool last = it.left == 1;
-        const int cur = pages;
-        if (!last) pages = fetch_pages(nx);       // in use from the next round on
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit))) { ok = false; break; }
-        write_info(last);
-        copy(sK + st * C::TILE_BYTES, p.kv.k, cur);
-        cp_async_mbar_arrive(&k_full[st]);
-        if (new_unit) {                           // Q behind the unit's first keys
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit))) { ok = false; break; }
-          load_q();
-          ++units;
+        if (!ok) {
+          if (lane == 0) set_status(p.status, kPtTimeoutLoad);
+          *abort_flag = 1;
+          // what this warp has asked for lands before the block's shared memory goes
+          bool done = units == 0 || mbar_wait_drain(q_full, (units - 1) & 1);
+          for (uint32_t n = nk > NST ? nk - NST : 0; n < nk; ++n) done &= mbar_wait_drain(&k_full[n % NST], (n / NST) & 1);
+          for (uint32_t n = nv > NST ? nv - NST : 0; n < nv; ++n) {
+            const uint32_t s = n % NST;
+            done &= (edges >> s) & 1 ? mbar_wait_drain(&v_raw[s], ((raw >> s) & 1) ^ 1) : mbar_wait_drain(&v_full[s], (n / NST) & 1);
+          }
+          if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit))) { ok = false; break; }
-        copy(sV + st * C::TILE_BYTES, p.kv.v, cur);
-        cp_async_mbar_arrive(&v_full[st]);
-        if (++st == NST) {
-          st = 0;
-          ph ^= 1;
+      } else if (warp == 9) {
+        // V of tiles that reach past what the unit's rows see: zeros there
+        uint32_t raw = 0;                         // phase of each stage's v_raw
+        ph = 0;
+        while (true) {
+          if (!mbar_wait_bounded(&k_full[st], ph, abort_flag, limit)) { ok = false; break; }
+          const int f = sInfo[st].flags, valid = sInfo[st].valid;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&k_empty[st]);
+          if (f & kPtEdge) {
+            if (!mbar_wait_bounded(&v_raw[st], (raw >> st) & 1, abort_flag, limit)) { ok = false; break; }
+            raw ^= 1u << st;
+            const int from = valid & 0xffff, to = valid >> 16, gone = 128 - (to - from);
+            for (int i = lane; i < gone * 8 * NSUB; i += 32) {
+              int key = (i >> 3) % gone;
+              const int sub = (i >> 3) / gone;
+              if (key >= from) key += to - from;
+              *reinterpret_cast<uint4 *>(sV + st * C::TILE_BYTES + sub * (128 * 128) + key * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_full[st]);
+          }
+          if (++st == NST) {
+            st = 0;
+            ph ^= 1;
+          }
+          if (f & kPtLast) break;
         }
-        if (last) break;
-        new_unit = it.j + 1 == it.j1;
-        if (new_unit) in_unit = false;
-        it = nx;
+        if (!ok) {
+          if (lane == 0) set_status(p.status, kPtTimeoutLoad);
+          *abort_flag = 1;
+        }
       }
     } else {
-      // codes go to this thread's own places in shared memory SD tiles ahead of their
-      // conversion (in registers the prefetch spilled); piece i is keys i * RPP + frow
-      constexpr int SD = C::SD, NCH = C::NCH, RPP = 128 / NCH;
-      const int frow = lt / NCH, fc = lt % NCH;   // a row's hd bytes are NCH pieces
-      uint8_t *codes = smem + C::OFF_CODES + lt * 16;
-      // the scales of key lt go the same way; with one tile ahead they wait in registers
-      // (shared memory is full) and are fetched behind the last ones' use
-      float *codes_sc = reinterpret_cast<float *>(smem + C::OFF_CSC) + lt;
-      [[maybe_unused]] float ks = 0.f, vs = 0.f;
+      constexpr int NCH = HD / 16;                // 16-byte pieces of a key's codes
+      const int fc = lt % NCH;                    // piece i of this thread is piece fc of key (i * 128 + lt) / NCH
+      uint8_t *codes = smem + C::OFF_CODES;
+      // the scales of key lt of the next tile wait in registers, fetched behind the last ones' use
+      float ks = 0.f, vs = 0.f;
       PagedIter ahead = it;
       int slot = 0;
-      // (K or V of) tile `ahead` under way
-      auto fetch = [&](int which, const uint8_t *src, const float *sc, int pages) {
-        uint8_t *dst = codes + (slot * 2 + which) * NCH * 2048;
-        const int x0 = ahead.j * kTileK;
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-          const int key = i * RPP + frow, x = x0 + key;
-          const int page = __shfl_sync(0xffffffffu, pages, key >> 4);
-          const bool in = page >= 0 && x >= ahead.lo && x < ahead.hi;
-          cp_async16(dst + i * 2048, src + (in ? paged_slot(p.kv, page, x, ahead.kvh) * HD + fc * 16 : 0), in);
+      uint32_t cph = 0;                           // phase of the slots
+      uint32_t nc[2] = {0, 0}, units_q = 0;       // K and V tiles, and Q, asked for
+      // K or V of tile `ahead` under way (the leading warp)
+      auto fetch = [&](int which, const uint8_t *src, int pages) {
+        const unsigned in = __ballot_sync(0xffffffffu, pages >= 0 && pages < p.kv.P);
+        uint64_t *bar = &c_full[slot * 2 + which];
+        ++nc[which];
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(in) * box * HD);
+        __syncwarp();
+        if (pages >= 0 && pages < p.kv.P) {
+          const long long at = paged_slot(p.kv, pages, ahead.j * kTileK + lane * box, ahead.kvh);
+          bulk_load(codes + (slot * 2 + which) * 128 * HD + lane * box * HD, src + at * HD, box * HD, bar);
         }
-        if constexpr (SD > 1) {
-          const int page = __shfl_sync(0xffffffffu, pages, lt >> 4);
-          const bool in = page >= 0 && x0 + lt >= ahead.lo && x0 + lt < ahead.hi;
-          cp_async4(codes_sc + (slot * 2 + which) * 128, sc + (in ? paged_slot(p.kv, page, x0 + lt, ahead.kvh) : 0), in);
-        }
-        cp_async_commit();
+        __syncwarp();
       };
-      auto fetch_scales = [&](int pages) {
-        const int x = ahead.j * kTileK + lt;
-        const int page = __shfl_sync(0xffffffffu, pages, lt >> 4);
-        const bool in = page >= 0 && x >= ahead.lo && x < ahead.hi;
-        const long long at = in ? paged_slot(p.kv, page, x, ahead.kvh) : 0;
+      auto fetch_scales = [&](const PagedIter &u, int pages) {
+        const int x = u.j * kTileK + lt;
+        const int page = __shfl_sync(0xffffffffu, pages, lt / box);
+        const bool in = page >= 0 && page < p.kv.P && x >= u.lo && x < u.hi;
+        const long long at = in ? paged_slot(p.kv, page, x, u.kvh) : 0;
         ks = in ? __ldg(p.kv.ks + at) : 0.f;
         vs = in ? __ldg(p.kv.vs + at) : 0.f;
       };
-      auto convert = [&](uint8_t *dst, int which, int at) {
-        const uint8_t *src = codes + (at * 2 + which) * NCH * 2048;
+      // codes of a slot to an operand tile; keys out of sight, or without a page, become zeros
+      auto convert = [&](uint8_t *dst, int which, int pages) {
+        const uint8_t *src = codes + (slot * 2 + which) * 128 * HD + lt * 16;
+        const int x0 = it.j * kTileK;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-          const int key = i * RPP + frow, ch = fc * 2;       // two pieces of 8 bf16
-          const uint4 w = *reinterpret_cast<const uint4 *>(src + i * 2048);
+          const int key = (i * 128 + lt) / NCH, ch = fc * 2;   // two pieces of 8 bf16
+          const int page = __shfl_sync(0xffffffffu, pages, key / box);
+          uint4 w = *reinterpret_cast<const uint4 *>(src + i * 2048);
+          if (page < 0 || page >= p.kv.P || x0 + key < it.lo || x0 + key >= it.hi) w = make_uint4(0, 0, 0, 0);
           uint8_t *row = dst + (ch >> 3) * (128 * 128) + key * 128;
           *reinterpret_cast<uint4 *>(row + (((ch & 7) ^ (key & 7)) << 4)) = pt_codes8(w.x, w.y);
           *reinterpret_cast<uint4 *>(row + ((((ch + 1) & 7) ^ (key & 7)) << 4)) = pt_codes8(w.z, w.w);
         }
         fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c_empty[slot * 2 + which]);
       };
-      int pages = fetch_pages(ahead);
+      int pages = fetch_pages(ahead);             // of tile `ahead`
+      int held[SD];                               // of the tiles under way
 #pragma unroll
       for (int d = 0; d < SD; ++d) {
+        held[d] = pages;
         if (ahead.left > 0) {
-          fetch(0, p.kv.k, p.kv.ks, pages);
-          fetch(1, p.kv.v, p.kv.vs, pages);
-          if (SD == 1) fetch_scales(pages);
+          if (lead) {
+            fetch(0, p.kv.k, pages);
+            fetch(1, p.kv.v, pages);
+          }
+          if (d == 0) fetch_scales(it, pages);
           paged_next(p, ahead);
-          if (ahead.left > 0) pages = fetch_pages(ahead);
-        } else {
-          cp_async_commit();
-          cp_async_commit();
+          pages = ahead.left > 0 ? fetch_pages(ahead) : -1;
         }
         slot = slot + 1 == SD ? 0 : slot + 1;
       }
       while (true) {
         const bool last = it.left == 1, more = ahead.left > 0;
+        const int cur = held[0];
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit))) { ok = false; break; }
-        write_info(last);
-        cp_async_wait<2 * SD - 1>();              // this thread's codes of K
-        convert(sK + st * C::TILE_BYTES, 0, slot);
+        if (lt == 0) write_info(last);
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c_full[slot * 2], cph, abort_flag, limit))) { ok = false; break; }
+        convert(sK + st * C::TILE_BYTES, 0, cur);
         mbar_arrive(&k_full[st]);
-        if (more) fetch(0, p.kv.k, p.kv.ks, pages);
-        else cp_async_commit();
+        if (more && lead) {
+          if (!mbar_wait_bounded(&c_empty[slot * 2], cph, abort_flag, limit)) { ok = false; break; }
+          fetch(0, p.kv.k, pages);
+        }
         if (new_unit) {                           // Q behind the unit's first keys
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit))) { ok = false; break; }
-          load_q();
+          if (lead) {
+            if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
+            if (lane == 0) load_q();
+            __syncwarp();
+            ++units_q;
+          }
           ++units;
         }
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit))) { ok = false; break; }
-        cp_async_wait<2 * SD - 1>();              // of V
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c_full[slot * 2 + 1], cph, abort_flag, limit))) { ok = false; break; }
         // both scales go with V: the softmax reads them until it signals P, and V's
         // stage is free only after P V
-        if (SD > 1) {
-          ks = codes_sc[slot * 256];
-          vs = codes_sc[slot * 256 + 128];
-        }
         sSc[(st * 2) * 128 + lt] = ks * p.scale_log2;
         sSc[(st * 2 + 1) * 128 + lt] = vs;
-        convert(sV + st * C::TILE_BYTES, 1, slot);
+        convert(sV + st * C::TILE_BYTES, 1, cur);
         mbar_arrive(&v_full[st]);
+#pragma unroll
+        for (int d = 0; d + 1 < SD; ++d) held[d] = held[d + 1];
+        held[SD - 1] = pages;
         if (more) {
-          fetch(1, p.kv.v, p.kv.vs, pages);
-          if (SD == 1) fetch_scales(pages);
+          if (lead) {
+            if (!mbar_wait_bounded(&c_empty[slot * 2 + 1], cph, abort_flag, limit)) { ok = false; break; }
+            fetch(1, p.kv.v, pages);
+          }
           paged_next(p, ahead);
-          if (ahead.left > 0) pages = fetch_pages(ahead);
-        } else {
-          cp_async_commit();
+          pages = ahead.left > 0 ? fetch_pages(ahead) : -1;
         }
-        slot = slot + 1 == SD ? 0 : slot + 1;
+        if (++slot == SD) {
+          slot = 0;
+          cph ^= 1;
+        }
         if (++st == NST) {
           st = 0;
           ph ^= 1;
@@ -462,12 +514,19 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
         new_unit = it.j + 1 == it.j1;
         if (new_unit) in_unit = false;
         paged_next(p, it);
+        fetch_scales(it, held[0]);
       }
-    }
-    cp_async_wait<0>();
-    if (!ok) {
-      if (lane == 0) set_status(p.status, kPtTimeoutLoad);
-      *abort_flag = 1;
+      if (!ok) {
+        if (lane == 0) set_status(p.status, kPtTimeoutLoad);
+        *abort_flag = 1;
+        if (lead) {                               // what this warp has asked for lands first
+          bool done = units_q == 0 || mbar_wait_drain(q_full, (units_q - 1) & 1);
+#pragma unroll
+          for (int w = 0; w < 2; ++w)
+            for (uint32_t n = nc[w] > SD ? nc[w] - SD : 0; n < nc[w]; ++n) done &= mbar_wait_drain(&c_full[(n % SD) * 2 + w], (n / SD) & 1);
+          if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
+        }
+      }
     }
   } else {
     setmaxnreg_inc<C::R_SOFTMAX>();
@@ -599,8 +658,8 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
             const bool whole = (f & (kPtEnds | kPtInUnit)) == kPtEnds, live = r < rows;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const long long at = o_base + tok * p.o.row + head * p.o.head;
-            float *part = paged_part(p.ws, cta, f & kPtInUnit ? 0 : 1, 256, HD);
-            if (live && !whole) *reinterpret_cast<float2 *>(part + 256 * HD + 2 * r) = make_float2(m, l);
+            float *part = paged_part(p.ws, cta, f & kPtInUnit ? 0 : 1, NQ * 128, HD);
+            if (live && !whole) *reinterpret_cast<float2 *>(part + NQ * 128 * HD + 2 * r) = make_float2(m, l);
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
               uint32_t ov[32];
@@ -611,7 +670,7 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                   const float *g = o + 8 * q;
-                  const uint4 w = p.q_f16 ? make_uint4(pack_f16x2(g[0] * inv, g[1] * inv), pack_f16x2(g[2] * inv, g[3] * inv),
+                  const uint4 w = p.o_f16 ? make_uint4(pack_f16x2(g[0] * inv, g[1] * inv), pack_f16x2(g[2] * inv, g[3] * inv),
                                                        pack_f16x2(g[4] * inv, g[5] * inv), pack_f16x2(g[6] * inv, g[7] * inv))
                                           : make_uint4(pack_bf16x2(g[0] * inv, g[1] * inv), pack_bf16x2(g[2] * inv, g[3] * inv),
                                                        pack_bf16x2(g[4] * inv, g[5] * inv), pack_bf16x2(g[6] * inv, g[7] * inv));
@@ -647,32 +706,48 @@ __global__ void __launch_bounds__(512, 1) paged_tiles_kernel(const PagedAttnPara
   }
 }
 
-template <int HD, bool FP8>
+template <int HD, bool FP8, int NQ>
 cudaError_t launch_tiles(const PagedAttnParams &p, cudaStream_t st) {
-  using C = PtCfg<HD, FP8>;
-  cudaError_t e = ensure_smem_attr<paged_tiles_kernel<HD, FP8>>(C::SMEM);
+  using C = PtCfg<HD, FP8, NQ>;
+  cudaError_t e = ensure_smem_attr<paged_tiles_kernel<HD, FP8, NQ>>(C::SMEM);
   if (e != cudaSuccess) return e;
   // the register split adds up to 128 a thread: a build that starts with fewer would
   // wait for registers that never come
   static std::atomic<int> regs{0};
   if (regs.load(std::memory_order_relaxed) == 0) {
     cudaFuncAttributes a;
-    if ((e = cudaFuncGetAttributes(&a, paged_tiles_kernel<HD, FP8>)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&a, paged_tiles_kernel<HD, FP8, NQ>)) != cudaSuccess) return e;
     regs.store(a.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != 128) return cudaErrorInvalidConfiguration;
-  paged_tiles_kernel<HD, FP8><<<p.ctas, C::THREADS, C::SMEM, st>>>(p);
+  CUtensorMap tq, tk{}, tv{};
+  // q as [sequences][tokens][heads][hd]; a unit's box is its tokens' heads
+  const bool packed = p.c.row_start != nullptr;
+  const uint64_t qd[4] = {HD, (uint64_t)p.H, packed ? (uint64_t)p.c.rows : (uint64_t)p.c.T, packed ? 1ull : (uint64_t)p.c.B};
+  const uint64_t qs[3] = {(uint64_t)p.q.head * 2, (uint64_t)p.q.row * 2, (uint64_t)(packed ? HD : p.q.seq) * 2};
+  const uint32_t qb[4] = {64, (uint32_t)p.G, (uint32_t)p.tt, 1};
+  if (!make_tmap_nd(&tq, p.q.data, 2, 4, qd, qs, qb, 128)) return cudaErrorInvalidValue;
+  if (!FP8) {
+    const uint64_t page = 1ull << p.kv.page_shift;
+    const uint64_t d[3] = {HD, p.kv.KV * page, (uint64_t)p.kv.P}, s[2] = {HD * 2, p.kv.KV * page * HD * 2};
+    const uint32_t b[3] = {64, (uint32_t)(page < kTileK ? page : kTileK), 1};
+    if (!make_tmap_nd(&tk, p.kv.k, 2, 3, d, s, b, 128) || !make_tmap_nd(&tv, p.kv.v, 2, 3, d, s, b, 128))
+      return cudaErrorInvalidValue;
+  }
+  paged_tiles_kernel<HD, FP8, NQ><<<p.ctas, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
   return cudaGetLastError();
+}
+
+template <int HD, bool FP8>
+cudaError_t launch_tiles_q(const PagedAttnParams &p, cudaStream_t st) {
+  return (long long)p.c.T * p.G <= 128 ? launch_tiles<HD, FP8, 1>(p, st) : launch_tiles<HD, FP8, 2>(p, st);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_tiles(const PagedAttnParams &p0, cudaStream_t st) {
-  PagedAttnParams p = p0;
-  p.tt = 256 / p.G;
-  p.bk_shift = 7;
-  if (p.kv.hd == 64) return p.kv.e4m3 ? launch_tiles<64, true>(p, st) : launch_tiles<64, false>(p, st);
-  return p.kv.e4m3 ? launch_tiles<128, true>(p, st) : launch_tiles<128, false>(p, st);
+cudaError_t launch_paged_tiles(const PagedAttnParams &p, cudaStream_t st) {
+  if (p.kv.hd == 64) return p.kv.e4m3 ? launch_tiles_q<64, true>(p, st) : launch_tiles_q<64, false>(p, st);
+  return p.kv.e4m3 ? launch_tiles_q<128, true>(p, st) : launch_tiles_q<128, false>(p, st);
 }
 
 }  // namespace smol

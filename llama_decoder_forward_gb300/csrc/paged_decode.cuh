@@ -53,12 +53,9 @@ __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A pair of q's values (bf16, or f16 rounded to bf16).
-__device__ __forceinline__ uint32_t pd_q2(const uint8_t *q, long long off, int f16_q) {
-  const uint32_t u = *reinterpret_cast<const uint32_t *>(q + off * 2);
-  if (!f16_q) return u;
-  const float2 f = unpack_f16x2(u);
-  return pack_bf16x2(f.x, f.y);
+// A pair of q's values.
+__device__ __forceinline__ uint32_t pd_q2(const uint8_t *q, long long off) {
+  return *reinterpret_cast<const uint32_t *>(q + off * 2);
 }
 
 template <int HD, bool FP8, int RT>
@@ -180,8 +177,8 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
           // so step s of group g takes the dims 64 g + 16 c4 + 4 s .. + 3 there
           const int d0 = FP8 ? (ks >> 2) * 64 + 16 * c4 + 4 * (ks & 3) : 16 * ks + 2 * c4;
           const int d1 = FP8 ? d0 + 2 : d0 + 8;
-          qf[rt][ks][i] = live ? pd_q2(p.q.data, base + d0, p.q_f16) : 0u;
-          qf[rt][ks][2 + i] = live ? pd_q2(p.q.data, base + d1, p.q_f16) : 0u;
+          qf[rt][ks][i] = live ? pd_q2(p.q.data, base + d0) : 0u;
+          qf[rt][ks][2 + i] = live ? pd_q2(p.q.data, base + d1) : 0u;
         }
       }
 #pragma unroll
@@ -417,7 +414,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
                   const int dim = d * 8 + 4 * c4;
                   if (whole)
                     *reinterpret_cast<uint2 *>(p.o.data + (out + dim) * 2) =
-                        p.q_f16 ? make_uint2(pack_f16x2(x * inv, x1 * inv), pack_f16x2(y * inv, y1 * inv))
+                        p.o_f16 ? make_uint2(pack_f16x2(x * inv, x1 * inv), pack_f16x2(y * inv, y1 * inv))
                                 : make_uint2(pack_bf16x2(x * inv, x1 * inv), pack_bf16x2(y * inv, y1 * inv));
                   else
                     *reinterpret_cast<float4 *>(row + dim) = make_float4(x, x1, y, y1);
@@ -425,7 +422,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
                   const int dim = d * 8 + 2 * c4;
                   if (whole)
                     *reinterpret_cast<uint32_t *>(p.o.data + (out + dim) * 2) =
-                        p.q_f16 ? pack_f16x2(x * inv, y * inv) : pack_bf16x2(x * inv, y * inv);
+                        p.o_f16 ? pack_f16x2(x * inv, y * inv) : pack_bf16x2(x * inv, y * inv);
                   else
                     *reinterpret_cast<float2 *>(row + dim) = make_float2(x, y);
                 }

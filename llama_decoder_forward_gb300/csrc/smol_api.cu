@@ -754,8 +754,8 @@ int check_paged(const smol_paged_cache *c) {
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return SMOL_ERR_UNSUPPORTED_SHAPE;
   if ((long long)c->max_pages * c->page_size > (1ll << 30) || c->n_kv_heads > 65535 || c->n_layers > 65535)
     return SMOL_ERR_UNSUPPORTED_SHAPE;
-  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || (reinterpret_cast<uintptr_t>(c->k_scale) & 3u) ||
-      (reinterpret_cast<uintptr_t>(c->v_scale) & 3u) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || !aligned16(c->k_scale) || !aligned16(c->v_scale) ||
+       (reinterpret_cast<uintptr_t>(c->page_table) & 3u))
     return SMOL_ERR_MISALIGNED;
   return SMOL_OK;
 }
@@ -859,7 +859,7 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
   if (layer < 0 || layer >= cache->n_layers || n_heads <= 0 || window < 0 || !(scale >= 0.f) || !isfinite(scale) || !ws)
     return SMOL_ERR_INVALID_ARG;
   if (!paged_heads_ok(cache, n_heads) || chunk->B > kPagedMaxSeqs) return SMOL_ERR_UNSUPPORTED_SHAPE;
-  if (!(rc = check_rows(q, chunk, n_heads, 1, cache->head_dim, false)))
+  if (!(rc = check_rows(q, chunk, n_heads, 1, cache->head_dim, true)))
     rc = check_rows(out, chunk, n_heads, 1, cache->head_dim, true);
   if (rc) return rc;
   if (!aligned16(ws)) return SMOL_ERR_MISALIGNED;
