@@ -51,6 +51,12 @@ struct PtInfo {
 };
 enum : int { kPtNew = 1, kPtTwo = 2, kPtUnitLast = 4, kPtEnds = 8, kPtLast = 16, kPtInUnit = 32, kPtEdge = 64 };
 
+// The loader's note of a tile of codes, in the slot's place.
+struct PtCodes {
+  PtInfo info;
+  int page[8];                 // pages of the tile's keys
+};
+
 template <int HD, bool FP8, int NQ>
 struct PtCfg {
   static constexpr int THREADS = 512;
@@ -64,13 +70,14 @@ struct PtCfg {
   static constexpr int OFF_CODES = OFF_V + NST * TILE_BYTES; // [SD][K, V][128 keys][HD]
   static constexpr int OFF_SC = OFF_CODES + (FP8 ? SD * 2 * 128 * HD : 0);     // [NST][2][128] scales of keys and values
   static constexpr int OFF_INFO = OFF_SC + (FP8 ? NST * 2 * 128 * 4 : 0);
-  static constexpr int OFF_BAR = OFF_INFO + NST * sizeof(PtInfo);
+  static constexpr int OFF_NOTE = OFF_INFO + NST * sizeof(PtInfo);
+  static constexpr int OFF_BAR = OFF_NOTE + (FP8 ? SD * sizeof(PtCodes) : 0);
   static constexpr int NBAR = 2 + 5 * NST + 4 * SD + 2 + 2 + 2 + 1;
   static constexpr int USED = OFF_BAR + NBAR * 8 + 16;
   // the tiles want 1024-byte alignment; the block has no other shared memory, so its
   // own usually starts there (checked)
   static constexpr int SMEM = USED + 1008 <= 232448 ? USED + 1008 : 232448;
-  static constexpr int R_SOFTMAX = FP8 ? 184 : 192, R_LOAD = FP8 ? 104 : 88, R_MMA = 40;
+  static constexpr int R_SOFTMAX = FP8 ? 176 : 192, R_LOAD = FP8 ? 80 : 88, R_MMA = FP8 ? 80 : 40;
   static_assert(2 * R_SOFTMAX + R_LOAD + R_MMA <= 512, "registers of the block");
   static_assert(USED <= 232448, "shared memory per CTA");
 };
@@ -157,6 +164,48 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();                                // also: every thread has its copy of the schedule
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+
+  // ---- what the loading warps share
+  const int box = min(1 << p.kv.page_shift, kTileK), n_box = kTileK / box;   // rows of a page in a tile, pages of a tile
+  // page numbers of a tile: lane i < n_box of the warp has that of keys i * box ..; -1: not in
+  // sight, P: no such page
+  auto fetch_pages = [&](const PagedIter &u) {
+    const int x = u.j * kTileK + box * lane;
+    int page = -1;
+    if (lane < n_box && x < u.hi && x + box > u.lo) {
+      page = paged_page(p.kv, u.b, x);
+      if (page < 0 || page >= p.kv.P) {
+        set_status(p.status, kDevBadInput);
+        page = p.kv.P;
+      }
+    }
+    return page;
+  };
+  auto note_of = [&](const PagedIter &it, bool new_unit, bool in_unit) {
+    PtInfo f;
+    const bool last = it.left == 1;
+    const bool ends = it.j + 1 == it.j1;
+    f.x0 = it.j * kTileK;
+    f.rows = it.nt * p.G;
+    f.valid = max(0, it.lo - f.x0) | (min(kTileK, it.hi - f.x0) << 16);
+    f.flags = (new_unit ? kPtNew : 0) | (f.rows > 128 ? kPtTwo : 0) | (ends || last ? kPtUnitLast : 0) | (ends ? kPtEnds : 0) |
+              (last ? kPtLast : 0) | (in_unit ? kPtInUnit : 0) | (f.valid != kTileK << 16 ? kPtEdge : 0);
+    f.first_at = it.s.L + it.t0;
+    f.o_base = paged_row_off(p.o, p.c, it.s, it.b, it.t0, it.kvh * p.G);
+    f.b = it.b;
+    f.qt = it.qt;
+    f.kvh = it.kvh;
+    return f;
+  };
+  // Q of the unit: its tokens' heads are the rows, in both tiles (rows past the sequence's last
+  // are whatever follows them, or zeros: they reach no other row)
+  auto load_q = [&](const PagedIter &it) {        // one lane
+    mbar_arrive_expect_tx(q_full, NSUB * 128 * p.tt * p.G);
+#pragma unroll
+    for (int sub = 0; sub < NSUB; ++sub)
+      tma_load_4d(sQ + sub * (NQ * 128 * 128), &tmQ, q_full, sub * 64, it.kvh * p.G, static_cast<int>(it.s.row0) + it.t0,
+                  p.c.row_start ? 0 : it.b);
+  };
 
   if (warp >= 12) {
     setmaxnreg_dec<C::R_MMA>();
@@ -257,55 +306,74 @@ __global__ void __launch_bounds__(512, 1)
         if (!mbar_wait_drain(drain, 0)) set_status(p.status, kPtTimeoutDrain);
       }
     }
+    if (FP8 && warp == 13) {
+      // ---------------------------------------------------------------- codes on their way, SD tiles ahead
+      bool ok = true, in_unit = it.j > it.j0, new_unit = true;
+      int slot = 0;
+      uint32_t cph = 1, n = 0, units = 0;         // the slots start empty
+      uint8_t *codes = smem + C::OFF_CODES;
+      PtCodes *notes = reinterpret_cast<PtCodes *>(smem + C::OFF_NOTE);
+      auto fetch = [&](int which, const uint8_t *src, int page) {
+        const bool mine = page >= 0 && page < p.kv.P;
+        const unsigned in = __ballot_sync(0xffffffffu, mine);
+        uint64_t *bar = &c_full[slot * 2 + which];
+        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(in) * box * HD);
+        __syncwarp();
+        if (mine)
+          bulk_load(codes + (slot * 2 + which) * 128 * HD + lane * box * HD,
+                    src + paged_slot(p.kv, page, it.j * kTileK + lane * box, it.kvh) * HD, box * HD, bar);
+        __syncwarp();
+      };
+      int pages = fetch_pages(it);
+      while (true) {
+        PagedIter nx = it;
+        paged_next(p, nx);
+        const bool last = it.left == 1;
+        const int cur = pages;
+        if (!last) pages = fetch_pages(nx);       // in use from the next round on
+        if (!mbar_wait_bounded(&c_empty[slot * 2], cph, abort_flag, limit)) { ok = false; break; }
+        if (!mbar_wait_bounded(&c_empty[slot * 2 + 1], cph, abort_flag, limit)) { ok = false; break; }
+        if (lane < 8) notes[slot].page[lane] = cur;
+        if (lane == 0) notes[slot].info = note_of(it, new_unit, in_unit);
+        __syncwarp();                             // before lane 0's arrivals
+        fetch(0, p.kv.k, cur);
+        fetch(1, p.kv.v, cur);
+        ++n;
+        if (new_unit) {                           // Q behind the unit's first keys
+          if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
+          if (lane == 0) load_q(it);
+          __syncwarp();
+          ++units;
+        }
+        if (++slot == SD) {
+          slot = 0;
+          cph ^= 1;
+        }
+        if (last) break;
+        new_unit = it.j + 1 == it.j1;
+        if (new_unit) in_unit = false;
+        it = nx;
+      }
+      if (!ok) {
+        if (lane == 0) set_status(p.status, kPtTimeoutLoad);
+        *abort_flag = 1;
+        // what this warp has asked for lands before the block's shared memory goes
+        bool done = units == 0 || mbar_wait_drain(q_full, (units - 1) & 1);
+        for (uint32_t k = n > SD ? n - SD : 0; k < n; ++k)
+          for (int w = 0; w < 2; ++w) done &= mbar_wait_drain(&c_full[(k % SD) * 2 + w], (k / SD) & 1);
+        if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
+      }
+    }
   } else if (warp >= 8) {
     setmaxnreg_dec<C::R_LOAD>();
     // ------------------------------------------------------------------ loaders
-    const int lt = tid - 256;
-    const bool lead = warp == 8;
-    bool ok = true, in_unit = it.j > it.j0, new_unit = true;
+    bool ok = true;
     int st = 0;
-    uint32_t ph = 1, units = 0;                   // the stages start empty
-    const int box = min(1 << p.kv.page_shift, kTileK), n_box = kTileK / box;   // rows of a page in a tile, pages of a tile
-    // page numbers of a tile: lane i < n_box of the warp has that of keys i * box ..; -1: not in
-    // sight, P: no such page
-    auto fetch_pages = [&](const PagedIter &u) {
-      const int x = u.j * kTileK + box * lane;
-      int page = -1;
-      if (lane < n_box && x < u.hi && x + box > u.lo) {
-        page = paged_page(p.kv, u.b, x);
-        if (page < 0 || page >= p.kv.P) {
-          set_status(p.status, kDevBadInput);
-          page = p.kv.P;
-        }
-      }
-      return page;
-    };
-    auto write_info = [&](bool last) {            // one lane
-      PtInfo f;
-      const bool ends = it.j + 1 == it.j1;
-      f.x0 = it.j * kTileK;
-      f.rows = it.nt * p.G;
-      f.valid = max(0, it.lo - f.x0) | (min(kTileK, it.hi - f.x0) << 16);
-      f.flags = (new_unit ? kPtNew : 0) | (f.rows > 128 ? kPtTwo : 0) | (ends || last ? kPtUnitLast : 0) | (ends ? kPtEnds : 0) |
-                (last ? kPtLast : 0) | (in_unit ? kPtInUnit : 0) | (f.valid != kTileK << 16 ? kPtEdge : 0);
-      f.first_at = it.s.L + it.t0;
-      f.o_base = paged_row_off(p.o, p.c, it.s, it.b, it.t0, it.kvh * p.G);
-      f.b = it.b;
-      f.qt = it.qt;
-      f.kvh = it.kvh;
-      sInfo[st] = f;
-    };
-    // Q of the unit: its tokens' heads are the rows, in both tiles (rows past the sequence's last
-    // are whatever follows them, or zeros: they reach no other row)
-    auto load_q = [&]() {                         // one lane
-      mbar_arrive_expect_tx(q_full, NSUB * 128 * p.tt * p.G);
-#pragma unroll
-      for (int sub = 0; sub < NSUB; ++sub)
-        tma_load_4d(sQ + sub * (NQ * 128 * 128), &tmQ, q_full, sub * 64, it.kvh * p.G, static_cast<int>(it.s.row0) + it.t0,
-                    p.c.row_start ? 0 : it.b);
-    };
+    uint32_t ph = 1;                              // the stages start empty
     if constexpr (!FP8) {
-      if (lead) {
+      if (warp == 8) {
+        bool in_unit = it.j > it.j0, new_unit = true;
+        uint32_t units = 0;
         // a box for each page and 64 columns; every lane issues its own page's
         auto copy = [&](uint8_t *dst, const CUtensorMap *map, uint64_t *bar, int page) {
           const unsigned in = __ballot_sync(0xffffffffu, page >= 0);
@@ -327,12 +395,12 @@ __global__ void __launch_bounds__(512, 1)
           const int cur = pages;
           if (!last) pages = fetch_pages(nx);     // in use from the next round on
           if (!mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit)) { ok = false; break; }
-          if (lane == 0) write_info(last);        // before this lane's arrival in copy()
+          if (lane == 0) sInfo[st] = note_of(it, new_unit, in_unit);   // before this lane's arrival in copy()
           copy(sK + st * C::TILE_BYTES, &tmK, &k_full[st], cur);
           ++nk;
           if (new_unit) {                         // Q behind the unit's first keys
             if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
-            if (lane == 0) load_q();
+            if (lane == 0) load_q(it);
             __syncwarp();
             ++units;
           }
@@ -398,110 +466,52 @@ __global__ void __launch_bounds__(512, 1)
         }
       }
     } else {
-      constexpr int NCH = HD / 16;                // 16-byte pieces of a key's codes
-      const int fc = lt % NCH;                    // piece i of this thread is piece fc of key (i * 128 + lt) / NCH
-      uint8_t *codes = smem + C::OFF_CODES;
-      // the scales of key lt of the next tile wait in registers, fetched behind the last ones' use
-      float ks = 0.f, vs = 0.f;
-      PagedIter ahead = it;
+      // ---- codes of a slot to the operand tiles
+      constexpr int NCH = HD / 16, RPP = 128 / NCH;   // 16-byte pieces of a key's codes; keys of a pass
+      const int lt = tid - 256, frow = lt / NCH, fc = lt % NCH;   // this thread's key of a pass, and piece
+      const uint8_t *codes = smem + C::OFF_CODES + lt * 16;
+      // where its two pieces of 8 bf16 go; hd 128: the upper half writes them in the other
+      // order, so that the halves' stores meet different banks
+      const int swap = HD == 128 ? fc >> 2 : 0;
+      const uint32_t to0 = ((fc * 2) >> 3) * (128 * 128) + frow * 128 + (((fc * 2 + swap) & 7) ^ (frow & 7)) * 16;
+      const uint32_t to1 = ((fc * 2) >> 3) * (128 * 128) + frow * 128 + (((fc * 2 + 1 - swap) & 7) ^ (frow & 7)) * 16;
       int slot = 0;
-      uint32_t cph = 0;                           // phase of the slots
-      uint32_t nc[2] = {0, 0}, units_q = 0;       // K and V tiles, and Q, asked for
-      // K or V of tile `ahead` under way (the leading warp)
-      auto fetch = [&](int which, const uint8_t *src, int pages) {
-        const unsigned in = __ballot_sync(0xffffffffu, pages >= 0 && pages < p.kv.P);
-        uint64_t *bar = &c_full[slot * 2 + which];
-        ++nc[which];
-        if (lane == 0) mbar_arrive_expect_tx(bar, __popc(in) * box * HD);
-        __syncwarp();
-        if (pages >= 0 && pages < p.kv.P) {
-          const long long at = paged_slot(p.kv, pages, ahead.j * kTileK + lane * box, ahead.kvh);
-          bulk_load(codes + (slot * 2 + which) * 128 * HD + lane * box * HD, src + at * HD, box * HD, bar);
-        }
-        __syncwarp();
-      };
-      auto fetch_scales = [&](const PagedIter &u, int pages) {
-        const int x = u.j * kTileK + lt;
-        const int page = __shfl_sync(0xffffffffu, pages, lt / box);
-        const bool in = page >= 0 && page < p.kv.P && x >= u.lo && x < u.hi;
-        const long long at = in ? paged_slot(p.kv, page, x, u.kvh) : 0;
-        ks = in ? __ldg(p.kv.ks + at) : 0.f;
-        vs = in ? __ldg(p.kv.vs + at) : 0.f;
-      };
-      // codes of a slot to an operand tile; keys out of sight, or without a page, become zeros
-      auto convert = [&](uint8_t *dst, int which, int pages) {
-        const uint8_t *src = codes + (slot * 2 + which) * 128 * HD + lt * 16;
-        const int x0 = it.j * kTileK;
+      uint32_t cph = 0;
+      auto convert = [&](uint8_t *dst, int which, int valid, bool edge) {
+        const uint8_t *src = codes + (slot * 2 + which) * 128 * HD;
+        const int from = valid & 0xffff, to = valid >> 16;
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-          const int key = (i * 128 + lt) / NCH, ch = fc * 2;   // two pieces of 8 bf16
-          const int page = __shfl_sync(0xffffffffu, pages, key / box);
           uint4 w = *reinterpret_cast<const uint4 *>(src + i * 2048);
-          if (page < 0 || page >= p.kv.P || x0 + key < it.lo || x0 + key >= it.hi) w = make_uint4(0, 0, 0, 0);
-          uint8_t *row = dst + (ch >> 3) * (128 * 128) + key * 128;
-          *reinterpret_cast<uint4 *>(row + (((ch & 7) ^ (key & 7)) << 4)) = pt_codes8(w.x, w.y);
-          *reinterpret_cast<uint4 *>(row + ((((ch + 1) & 7) ^ (key & 7)) << 4)) = pt_codes8(w.z, w.w);
+          // keys out of sight: zeros, whatever is there
+          if (edge && (i * RPP + frow < from || i * RPP + frow >= to)) w = make_uint4(0, 0, 0, 0);
+          const uint4 a = pt_codes8(w.x, w.y), b = pt_codes8(w.z, w.w);
+          *reinterpret_cast<uint4 *>(dst + to0 + i * RPP * 128) = swap ? b : a;
+          *reinterpret_cast<uint4 *>(dst + to1 + i * RPP * 128) = swap ? a : b;
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&c_empty[slot * 2 + which]);
       };
-      int pages = fetch_pages(ahead);             // of tile `ahead`
-      int held[SD];                               // of the tiles under way
-#pragma unroll
-      for (int d = 0; d < SD; ++d) {
-        held[d] = pages;
-        if (ahead.left > 0) {
-          if (lead) {
-            fetch(0, p.kv.k, pages);
-            fetch(1, p.kv.v, pages);
-          }
-          if (d == 0) fetch_scales(it, pages);
-          paged_next(p, ahead);
-          pages = ahead.left > 0 ? fetch_pages(ahead) : -1;
-        }
-        slot = slot + 1 == SD ? 0 : slot + 1;
-      }
       while (true) {
-        const bool last = it.left == 1, more = ahead.left > 0;
-        const int cur = held[0];
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit))) { ok = false; break; }
-        if (lt == 0) write_info(last);
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c_full[slot * 2], cph, abort_flag, limit))) { ok = false; break; }
-        convert(sK + st * C::TILE_BYTES, 0, cur);
+        const PtCodes &note = reinterpret_cast<const PtCodes *>(smem + C::OFF_NOTE)[slot];
+        const int valid = note.info.valid, f = note.info.flags, page = note.page[lt / box];
+        const bool edge = f & kPtEdge, in = page >= 0 && page < p.kv.P && lt >= (valid & 0xffff) && lt < valid >> 16;
+        const long long at = in ? paged_slot(p.kv, page, note.info.x0 + lt, note.info.kvh) : 0;
+        const float ks = in ? __ldg(p.kv.ks + at) : 0.f, vs = in ? __ldg(p.kv.vs + at) : 0.f;   // of key lt, for later
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit))) { ok = false; break; }
+        if (lt == 0) sInfo[st] = note.info;
+        convert(sK + st * C::TILE_BYTES, 0, valid, edge);
         mbar_arrive(&k_full[st]);
-        if (more && lead) {
-          if (!mbar_wait_bounded(&c_empty[slot * 2], cph, abort_flag, limit)) { ok = false; break; }
-          fetch(0, p.kv.k, pages);
-        }
-        if (new_unit) {                           // Q behind the unit's first keys
-          if (lead) {
-            if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
-            if (lane == 0) load_q();
-            __syncwarp();
-            ++units_q;
-          }
-          ++units;
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit))) { ok = false; break; }
         if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c_full[slot * 2 + 1], cph, abort_flag, limit))) { ok = false; break; }
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit))) { ok = false; break; }
         // both scales go with V: the softmax reads them until it signals P, and V's
         // stage is free only after P V
         sSc[(st * 2) * 128 + lt] = ks * p.scale_log2;
         sSc[(st * 2 + 1) * 128 + lt] = vs;
-        convert(sV + st * C::TILE_BYTES, 1, cur);
+        convert(sV + st * C::TILE_BYTES, 1, valid, edge);
         mbar_arrive(&v_full[st]);
-#pragma unroll
-        for (int d = 0; d + 1 < SD; ++d) held[d] = held[d + 1];
-        held[SD - 1] = pages;
-        if (more) {
-          if (lead) {
-            if (!mbar_wait_bounded(&c_empty[slot * 2 + 1], cph, abort_flag, limit)) { ok = false; break; }
-            fetch(1, p.kv.v, pages);
-          }
-          paged_next(p, ahead);
-          pages = ahead.left > 0 ? fetch_pages(ahead) : -1;
-        }
         if (++slot == SD) {
           slot = 0;
           cph ^= 1;
@@ -510,22 +520,11 @@ __global__ void __launch_bounds__(512, 1)
           st = 0;
           ph ^= 1;
         }
-        if (last) break;
-        new_unit = it.j + 1 == it.j1;
-        if (new_unit) in_unit = false;
-        paged_next(p, it);
-        fetch_scales(it, held[0]);
+        if (f & kPtLast) break;
       }
       if (!ok) {
         if (lane == 0) set_status(p.status, kPtTimeoutLoad);
         *abort_flag = 1;
-        if (lead) {                               // what this warp has asked for lands first
-          bool done = units_q == 0 || mbar_wait_drain(q_full, (units_q - 1) & 1);
-#pragma unroll
-          for (int w = 0; w < 2; ++w)
-            for (uint32_t n = nc[w] > SD ? nc[w] - SD : 0; n < nc[w]; ++n) done &= mbar_wait_drain(&c_full[(n % SD) * 2 + w], (n / SD) & 1);
-          if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
-        }
       }
     }
   } else {
