@@ -34,7 +34,7 @@ struct PagedRows {
 struct PagedSeq {
   int L;                       // position of its row 0
   int n;                       // rows
-  long long row0;              // packed: index of its row 0 (0 otherwise)
+  int row0;                    // packed: index of its row 0 (0 otherwise)
   bool bad;                    // a value was out of its range
 };
 
@@ -47,10 +47,10 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedChunk &c, int b, int ca
   s.row0 = 0;
   if (c.row_start) {
     const long long a = c.row_start[b], e = c.row_start[b + 1];
-    s.row0 = min(max(a, 0ll), c.rows);
-    const long long end = min(max(e, s.row0), c.rows);
-    s.bad |= s.row0 != a || end != e;
-    n = end - s.row0;
+    const long long from = min(max(a, 0ll), c.rows), end = min(max(e, from), c.rows);   // c.rows < 2^31
+    s.row0 = static_cast<int>(from);
+    s.bad |= from != a || end != e;
+    n = end - from;
   } else if (c.n_new) {
     n = c.n_new[b];
   }
@@ -63,7 +63,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedChunk &c, int b, int ca
 // The address offset (in elements) of row t, head h of sequence b.
 __device__ __forceinline__ long long paged_row_off(const PagedRows &r, const PagedChunk &c, const PagedSeq &s,
                                                    int b, int t, int h) {
-  return (c.row_start ? 0 : b * r.seq) + (s.row0 + t) * r.row + h * r.head;
+  return (c.row_start ? 0 : b * r.seq) + (static_cast<long long>(s.row0) + t) * r.row + h * r.head;
 }
 
 // Page of a position of sequence b (x < max_pages << page_shift); outside
@@ -98,6 +98,8 @@ struct PagedAttnParams {
   int *status;
 };
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T);
+bool paged_map_q(CUtensorMap *map, const PagedAttnParams &p);
+bool paged_map_pages(CUtensorMap *map, const PagedKv &kv, const void *base, int box_rows);
 cudaError_t launch_paged_tiles(const PagedAttnParams &p, cudaStream_t st);   // units of 256 rows, on tcgen05
 cudaError_t launch_paged_attention(const PagedAttnParams &p, int sms, cudaStream_t st, int *launches);
 

@@ -14,83 +14,30 @@ namespace {
 
 constexpr int kCombThreads = 256;
 
-// Units cut by a border between CTAs: CTA c's combines the unit that CTA c began
-// and did not finish, from its place 1 and the place 0 of the CTAs behind it up
-// to the one in which the unit ends, in that order (the same bits every time).
+// The many-rows kernel's units that a border between CTAs cuts: CTA c's of this
+// grid combines the unit that CTA c began and did not finish, from that one's place 1
+// and the place 0 of the CTAs behind it up to the one in which the unit ends.
 // One warp for each row; blockIdx.y splits the rows.
 template <int HD>
 __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const PagedAttnParams p, int rows) {
-  __shared__ int list[kPagedMaxCtas], n_warp[8], first_end;
+  __shared__ int first_end;
   __shared__ float weight[8][kPagedMaxCtas];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, c = blockIdx.x;
   griddep_wait();
   const PagedMeta *metas = paged_meta(p.ws);
   const PagedMeta mine = metas[c];
   if (!mine.out) return;
-  if (tid == 0) first_end = p.ctas;
+  if (tid == 0) first_end = p.ctas - 1;
   __syncthreads();
-  const int other = c + tid;                      // tid 0: this CTA's own place 1
-  PagedMeta mo{};
-  if (tid > 0 && other < p.ctas) mo = metas[other];
-  if (mo.in && mo.ends) atomicMin(&first_end, other);
+  const int other = c + 1 + tid;
+  if (other < p.ctas && metas[other].in && metas[other].ends) atomicMin(&first_end, other);
   __syncthreads();
-  const bool in = tid == 0 || (mo.in && other <= first_end);
-  const unsigned vote = __ballot_sync(0xffffffffu, in);
-  if (lane == 0) n_warp[warp] = __popc(vote);
-  __syncthreads();
-  int at = __popc(vote & ((1u << lane) - 1)), n = 0;
-  for (int w = 0; w < 8; ++w) {
-    if (w < warp) at += n_warp[w];
-    n += n_warp[w];
-  }
-  if (in) list[at] = other;
-  __syncthreads();
+  const int n = first_end - c + 1;
   const PagedSeq s = paged_seq(p.c, mine.b, paged_cap(p));
   int t0, nt, lo, hi, j0, j1;
   paged_unit_tiles(p, s, mine.qt, t0, nt, lo, hi, j0, j1);
-  const int live = nt * p.G;
-  for (int r = blockIdx.y * 8 + warp; r < live; r += gridDim.y * 8) {
-    float mx = -INFINITY, sum = 0.f;
-    for (int i = lane; i < n; i += 32)
-      mx = fmaxf(mx, paged_part(p.ws, list[i], i == 0, rows, HD)[rows * HD + 2 * r]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    for (int i = lane; i < n; i += 32) {
-      const float2 ml = *reinterpret_cast<const float2 *>(paged_part(p.ws, list[i], i == 0, rows, HD) + rows * HD + 2 * r);
-      const float a = mx == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-      weight[warp][i] = a;
-      sum += a * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    __syncwarp();
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    float acc[HD / 32];
-#pragma unroll
-    for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float *row = paged_part(p.ws, list[i], i == 0, rows, HD) + r * HD + lane * (HD / 32);
-      const float a = weight[warp][i];
-      if constexpr (HD == 64) {
-        const float2 v = *reinterpret_cast<const float2 *>(row);
-        acc[0] += a * v.x;
-        acc[1] += a * v.y;
-      } else {
-        const float4 v = *reinterpret_cast<const float4 *>(row);
-        acc[0] += a * v.x;
-        acc[1] += a * v.y;
-        acc[2] += a * v.z;
-        acc[3] += a * v.w;
-      }
-    }
-    uint32_t *out = reinterpret_cast<uint32_t *>(
-        p.o.data + (paged_unit_row(p.o, p, s, mine.b, t0, mine.kvh, r) + lane * (HD / 32)) * 2);
-#pragma unroll
-    for (int e = 0; e < HD / 64; ++e)
-      out[e] = p.o_f16 ? pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    __syncwarp();                                 // the weights are rewritten
-  }
+  for (int r = blockIdx.y * 8 + warp; r < nt * p.G; r += gridDim.y * 8)
+    paged_combine_row<HD>(p, rows, c, n, r, weight[warp], paged_unit_row(p.o, p, s, mine.b, t0, mine.kvh, r));
 }
 
 template <int HD, bool FP8, int RT>
@@ -100,7 +47,10 @@ cudaError_t launch_few(const PagedAttnParams &p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   PagedAttnParams q = p;
   q.bk_shift = C::BK_SHIFT;
-  paged_few_rows_kernel<HD, FP8, RT><<<p.ctas, C::THREADS, C::SMEM, st>>>(q);
+  CUtensorMap tq, tk, tv;
+  if (!paged_map_q(&tq, p) || !paged_map_pages(&tk, p.kv, p.kv.k, C::KC) || !paged_map_pages(&tv, p.kv, p.kv.v, C::KC))
+    return cudaErrorInvalidValue;
+  paged_few_rows_kernel<HD, FP8, RT><<<p.ctas, C::THREADS, C::SMEM, st>>>(tq, tk, tv, q);
   return cudaGetLastError();
 }
 
@@ -120,10 +70,28 @@ cudaError_t launch_combine(const PagedAttnParams &p, int rows, cudaStream_t st) 
 
 }  // namespace
 
+// q as [sequences][tokens][heads][hd]: a unit's box is its tokens' heads, 64 columns.
+bool paged_map_q(CUtensorMap *map, const PagedAttnParams &p) {
+  const bool packed = p.c.row_start != nullptr;
+  const uint64_t d[4] = {(uint64_t)p.kv.hd, (uint64_t)p.H, packed ? (uint64_t)p.c.rows : (uint64_t)p.c.T, packed ? 1ull : (uint64_t)p.c.B};
+  const uint64_t s[3] = {(uint64_t)p.q.head * 2, (uint64_t)p.q.row * 2, (uint64_t)(packed ? p.kv.hd : p.q.seq) * 2};
+  const uint32_t b[4] = {64, (uint32_t)p.G, (uint32_t)p.tt, 1};
+  return make_tmap_nd(map, p.q.data, 2, 4, d, s, b, 128);
+}
+
+// One layer's pages as [page][kv heads' rows][hd]: boxes of up to box_rows rows of a
+// page, 64 columns of bf16 or a row of codes.
+bool paged_map_pages(CUtensorMap *map, const PagedKv &kv, const void *base, int box_rows) {
+  const uint64_t page = 1ull << kv.page_shift, row = (uint64_t)kv.hd * (kv.e4m3 ? 1 : 2);
+  const uint64_t d[3] = {(uint64_t)kv.hd, kv.KV * page, (uint64_t)kv.P}, s[2] = {row, kv.KV * page * row};
+  const uint32_t b[3] = {kv.e4m3 ? (uint32_t)kv.hd : 64u, (uint32_t)(page < (uint64_t)box_rows ? page : box_rows), 1};
+  return make_tmap_nd(map, base, kv.e4m3 ? 1 : 2, 3, d, s, b, kv.e4m3 && kv.hd == 64 ? 64 : 128);
+}
+
 // Rows of a unit: the tile of the kernel that takes the call.
 static int unit_rows(int G, int T) {
   const long long r = (long long)T * G;
-  return r <= 16 ? 16 : r <= 128 ? 128 : 256;
+  return r <= 16 ? 16 : r <= 32 ? 32 : r <= 128 ? 128 : 256;
 }
 
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {
@@ -151,6 +119,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   prof_after(SMOL_K_DEC_ATTN, st);
   if (e != cudaSuccess) return e;
   *launches = 1;
+  if (rows < 128) return cudaSuccess;             // that kernel combines its parts itself
   prof_before(SMOL_K_OTHER, st);
   e = h64 ? launch_combine<64>(p, rows, st) : launch_combine<128>(p, rows, st);
   prof_after(SMOL_K_OTHER, st);

@@ -720,19 +720,8 @@ cudaError_t launch_tiles(const PagedAttnParams &p, cudaStream_t st) {
   }
   if (regs.load(std::memory_order_relaxed) != 128) return cudaErrorInvalidConfiguration;
   CUtensorMap tq, tk{}, tv{};
-  // q as [sequences][tokens][heads][hd]; a unit's box is its tokens' heads
-  const bool packed = p.c.row_start != nullptr;
-  const uint64_t qd[4] = {HD, (uint64_t)p.H, packed ? (uint64_t)p.c.rows : (uint64_t)p.c.T, packed ? 1ull : (uint64_t)p.c.B};
-  const uint64_t qs[3] = {(uint64_t)p.q.head * 2, (uint64_t)p.q.row * 2, (uint64_t)(packed ? HD : p.q.seq) * 2};
-  const uint32_t qb[4] = {64, (uint32_t)p.G, (uint32_t)p.tt, 1};
-  if (!make_tmap_nd(&tq, p.q.data, 2, 4, qd, qs, qb, 128)) return cudaErrorInvalidValue;
-  if (!FP8) {
-    const uint64_t page = 1ull << p.kv.page_shift;
-    const uint64_t d[3] = {HD, p.kv.KV * page, (uint64_t)p.kv.P}, s[2] = {HD * 2, p.kv.KV * page * HD * 2};
-    const uint32_t b[3] = {64, (uint32_t)(page < kTileK ? page : kTileK), 1};
-    if (!make_tmap_nd(&tk, p.kv.k, 2, 3, d, s, b, 128) || !make_tmap_nd(&tv, p.kv.v, 2, 3, d, s, b, 128))
-      return cudaErrorInvalidValue;
-  }
+  if (!paged_map_q(&tq, p)) return cudaErrorInvalidValue;
+  if (!FP8 && (!paged_map_pages(&tk, p.kv, p.kv.k, kTileK) || !paged_map_pages(&tv, p.kv, p.kv.v, kTileK))) return cudaErrorInvalidValue;
   paged_tiles_kernel<HD, FP8, NQ><<<p.ctas, C::THREADS, C::SMEM, st>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }

@@ -4,21 +4,25 @@
 //
 // Bound by memory: every key and value is read once for at most 32 rows.  What
 // counts is bytes in flight, so each of the CTA's eight warps runs by itself: its
-// own ring of stages in shared memory, filled by 16-byte asynchronous copies
-// (keys outside the rows' sight, and pages that are not there, are filled with
-// zeros, so nothing that lies in unused slots is ever computed with), and its own
-// running maximum, sum and accumulator over an eighth of each key tile.  No
-// barrier is met until a unit ends; then the eight states are merged through
-// shared memory, two at a time.
+// own ring of stages in shared memory, filled by TMA boxes that one lane asks for
+// (a box for each page), and its own running maximum, sum and accumulator over an
+// eighth of each key tile.  No barrier of the CTA is met until a unit ends; then the
+// eight states are merged through shared memory, two at a time.  A unit that
+// several CTAs share is finished by the one that comes last: it combines all their
+// parts, in the CTAs' order (the same bits every time).
 //
 // mma.sync m16n8k16 (bf16, fp32 sums): a tcgen05 tile has 128 rows, of which 3 to
 // 32 would be used, and its score tile's trip through tensor memory is longer than
-// the whole step here.  The fragments of a step stay in registers.
+// the whole step here.  The fragments of a step stay in registers; with 32 rows the
+// queries' are read from shared memory each time (they would spill).
 //
 // e4m3 codes become bf16 exactly: the code's 7 bits moved to the bf16 exponent and
 // mantissa are the value times 2^-120 (subnormal codes included), one exact
 // product restores it.  The keys' scales multiply the scores, the values' scales
 // the weights, so no dequantised value is rounded.
+//
+// Slots outside the rows' sight may hold anything: their scores are replaced before
+// they are looked at, their values (bf16) or scales (e4m3) set to zero.
 #pragma once
 
 #include "paged_sched.cuh"
@@ -44,6 +48,16 @@ __device__ __forceinline__ void pd_ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+__device__ __forceinline__ uint4 pd_lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 pd_lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
 
 // Two e4m3 codes in the high bytes of the halves of x to a bf16 pair.
 __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x) {
@@ -53,220 +67,371 @@ __device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// A pair of q's values.
-__device__ __forceinline__ uint32_t pd_q2(const uint8_t *q, long long off) {
-  return *reinterpret_cast<const uint32_t *>(q + off * 2);
-}
-
 template <int HD, bool FP8, int RT>
 struct PdCfg {
   static constexpr int NW = 8, THREADS = 32 * NW;
   static constexpr int KC = (HD == 128 && !FP8) ? 16 : 32;     // keys of a warp's step: 4 or 8 KB of K and V
-  static constexpr int ROWB = HD * (FP8 ? 1 : 2);              // bytes of a key
-  static constexpr int CPR = ROWB / 16;                        // 16-byte pieces of a key
-  static constexpr int KV_BYTES = KC * ROWB;
-  static constexpr int STAGE = 2 * KV_BYTES + (FP8 ? 2 * KC * 4 : 0);
-  static constexpr int NS = (FP8 && HD == 64) ? 5 : (FP8 && RT == 2) ? 2 : 3;
+  static constexpr int NSUB = FP8 ? 1 : HD / 64;               // boxes across a key (128 bytes each, or 64)
+  static constexpr int ROWB = FP8 ? HD : 128;                  // bytes of a key in a box
+  static constexpr int SUB_BYTES = KC * ROWB;
+  static constexpr int KV_BYTES = NSUB * SUB_BYTES;
+  static constexpr int STAGE = 2 * KV_BYTES;
+  static constexpr int NS = STAGE == 4096 ? 5 : RT == 2 && HD == 128 ? 2 : 3;
   static constexpr int BK_SHIFT = KC == 32 ? 8 : 7;            // keys of a tile: NW * KC
   static constexpr int NT8 = KC / 8;                           // key columns of the score fragments
   static constexpr int ND8 = HD / 8;
+  static constexpr bool Q_REGS = RT == 1;                      // the queries' fragments stay in registers
+  static constexpr int Q_BYTES = RT * 16 * HD * 2;             // [HD / 64][RT * 16 rows][64]
   static constexpr int MERGE_WORDS = RT * (ND8 * 4 + 4);       // a thread's state
-  static constexpr int OFF_MERGE = NW * NS * STAGE;
-  static constexpr int SMEM = OFF_MERGE + 2 * 32 * MERGE_WORDS * 4;   // two warps' states at a time
-  static_assert(SMEM <= 227 * 1024 - 1024, "shared memory per CTA");
+  static constexpr int OFF_SC = NW * NS * STAGE;               // of each stage: scales of the keys, and of the values
+  static constexpr int OFF_NOTE = OFF_SC + (FP8 ? NW * NS * 2 * KC * 4 : 0);
+  static constexpr int OFF_Q = (OFF_NOTE + NW * NS * 64 + 1023) / 1024 * 1024;   // [2] this unit's and the next one's
+  static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;        // two warps' states at a time
+  static constexpr int MERGE_BYTES = 2 * 32 * MERGE_WORDS * 4;
+  static constexpr int OFF_BAR = OFF_MERGE + MERGE_BYTES;      // [NW][NS] stages, [2] Q
+  static constexpr int USED = OFF_BAR + (NW * NS + 2) * 8 + 16;
+  static constexpr int SMEM = USED + 1008 <= 232448 ? USED + 1008 : 232448;
+  static_assert(USED <= 232448, "shared memory per CTA");
+  static_assert(MERGE_BYTES >= 8 * kPagedMaxCtas * 4 + (int)sizeof(PagedSchedSmem), "room for the parts' weights, and the schedule");
 };
 
-// Byte offset of 16-byte piece c of key row `key`, swizzled so that eight rows'
-// same piece (ldmatrix) and, for codes, two rows' four neighbouring pieces (the
-// fragment loads of K) meet no bank twice.
-template <int CPR>
-__device__ __forceinline__ uint32_t pd_off(int key, int c) {
-  if constexpr (CPR == 4) return key * 64 + ((c ^ ((key >> 1) & 3)) << 4);          // 64-byte rows
-  else if constexpr (CPR == 8) return key * 128 + ((c ^ (((key & 1) << 2) | ((key >> 1) & 3))) << 4);
-  else return key * 256 + ((c ^ (key & 7)) << 4);
-}
+// A warp's note of a step, beside its keys.
+struct PdNote {
+  int x0, lo, hi;              // the warp's first position; the positions that some row of the unit sees
+  int first_at, rows;          // the unit's first row's position; its rows
+  int flags;                   // kPd*
+  int b, kvh, t0, row0;        // the unit
+  int j01;                     // its key tiles, and the first one's place in the line
+  long long u0;
+  int pad[2];
+};
+static_assert(sizeof(PdNote) == 64, "note");
+
+enum : int { kPdFirst = 1, kPdEnds = 2, kPdLast = 4 };       // the unit's first tile here, its last tile, this CTA's last
+enum : int { kPdTimeout = 0x209 };
 
 template <int HD, bool FP8, int RT>
-__global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows_kernel(const PagedAttnParams p) {
+__global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
+    paged_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                          const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p) {
   using C = PdCfg<HD, FP8, RT>;
-  constexpr int KC = C::KC, NS = C::NS, CPR = C::CPR, ND8 = C::ND8, NT8 = C::NT8;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ PagedSchedSmem sched;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
+  constexpr int KC = C::KC, NS = C::NS, ND8 = C::ND8, NT8 = C::NT8, NSUB = C::NSUB;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), cta = blockIdx.x;
   const int g8 = lane >> 2, c4 = lane & 3;        // fragment row and column pair
-  uint8_t *ring = smem + warp * NS * C::STAGE;
-  float *merge = reinterpret_cast<float *>(smem + C::OFF_MERGE);
-
-  griddep_launch_dependents();
-  PagedIter cur = paged_locate<C::THREADS>(p, cta, p.ctas, sched);
-  PagedMeta meta{};
-  if (cur.left == 0) {
-    if (threadIdx.x == 0) paged_meta(p.ws)[cta] = meta;
+  if (smem + C::USED > smem_raw + C::SMEM) {      // no room left by the alignment
+    if (tid == 0) set_status(p.status, kPdTimeout);
     return;
   }
-  const bool first_in = cur.j > cur.j0;           // begun by an earlier CTA
+  uint8_t *ring = smem + warp * NS * C::STAGE;
+  float *ring_sc = reinterpret_cast<float *>(smem + C::OFF_SC) + warp * NS * 2 * KC;
+  PdNote *notes = reinterpret_cast<PdNote *>(smem + C::OFF_NOTE + warp * NS * 64);   // 64 bytes each
+  float *merge = reinterpret_cast<float *>(smem + C::OFF_MERGE);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * NS;
+  uint64_t *q_full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + C::NW * NS;
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(q_full + 2);
+  volatile int *s_parts = abort_flag + 1;         // [2] a unit to combine: its first CTA, and how many
+
+  PagedSchedSmem &sched = *reinterpret_cast<PagedSchedSmem *>(merge);
+  PagedIter ld = paged_locate<C::THREADS>(p, cta, p.ctas, sched);
+  if (ld.left == 0) return;                       // the same for the whole CTA
+  const long long total = sched.total;
+  const int workers = sched.workers;
+  if (lane == 0)
+    for (int i = 0; i < NS; ++i) mbar_init(&full[i], 1);
+  if (tid == 0) {
+    mbar_init(&q_full[0], 1);
+    mbar_init(&q_full[1], 1);
+    *abort_flag = 0;
+  }
+  if (lane == 0) fence_barrier_init();
+  __syncthreads();
+
+  bool alive = true;                              // false: a wait gave up, nothing more is asked for
+  // ---- Q of a unit by TMA: its tokens' heads are the rows (rows past its last are
+  // whatever follows, or zeros: they reach no other row)
+  PagedIter qn = ld;                              // the unit whose Q is asked for next (warp 0)
+  uint32_t nq = 0;
+  auto ask_q = [&]() {
+    if (qn.left > 0 && alive) {
+      if (lane == 0) {
+        uint64_t *bar = &q_full[nq & 1];
+        mbar_arrive_expect_tx(bar, (HD / 64) * 128 * p.tt * p.G);
+#pragma unroll
+        for (int sub = 0; sub < HD / 64; ++sub)
+          tma_load_4d(smem + C::OFF_Q + (nq & 1) * C::Q_BYTES + sub * (RT * 16 * 128), &tmQ, bar, sub * 64, qn.kvh * p.G,
+                      qn.s.row0 + qn.t0, p.c.row_start ? 0 : qn.b);
+      }
+      ++nq;
+      qn.left -= qn.j1 - qn.j - 1;                // to the unit's last tile, and over it
+      qn.j = qn.j1 - 1;
+      paged_next(p, qn);
+    }
+    __syncwarp();
+  };
 
   // ---- loads: this warp's KC keys of a tile; the page numbers are fetched one
-  // step ahead of the copies that need them
-  PagedIter ld = cur;
-  int page0 = -1, page1 = -1;                     // pages of the first and the second half of the keys
-  auto fetch_pages = [&]() {
-    page0 = page1 = -1;
-    if (ld.left <= 0) return;
-    const int x0 = (ld.j << C::BK_SHIFT) + warp * KC, x1 = x0 + 16;
-    if (x0 < ld.hi && x0 + 16 > ld.lo) page0 = paged_page(p.kv, ld.b, x0);
-    if (KC == 32 && x1 < ld.hi && x1 + 16 > ld.lo) page1 = paged_page(p.kv, ld.b, x1);
+  // step ahead of the boxes that need them
+  const int box = min(1 << p.kv.page_shift, KC), n_box = KC / box;
+  int page = -1;                                  // lane i < n_box: of keys i * box ..
+  bool first_tile = true;
+  const bool started_inside = ld.j > ld.j0;       // the first unit was begun by an earlier CTA
+  uint32_t asked = 0;                             // steps asked for
+  auto fetch_page = [&]() {
+    page = -1;
+    if (ld.left > 0 && lane < n_box) {
+      const int x = (ld.j << C::BK_SHIFT) + warp * KC + lane * box;
+      if (x < ld.hi && x + box > ld.lo) page = paged_page(p.kv, ld.b, x);
+    }
   };
-  fetch_pages();
+  fetch_page();
   int ld_stage = 0;
   auto produce = [&]() {
     if (ld.left > 0) {
+      uint8_t *st = ring + ld_stage * C::STAGE;
+      uint64_t *bar = &full[ld_stage];
       const int x0 = (ld.j << C::BK_SHIFT) + warp * KC;
-      if (x0 < ld.hi && x0 + KC > ld.lo) {
-        uint8_t *st = ring + ld_stage * C::STAGE;
-        bool ok0 = page0 >= 0 && page0 < p.kv.P, ok1 = page1 >= 0 && page1 < p.kv.P;
-        if ((!ok0 && x0 + 16 > ld.lo) || (KC == 32 && !ok1 && x0 + 16 < ld.hi)) set_status(p.status, kDevBadInput);
-        const long long s0 = ok0 ? paged_slot(p.kv, page0, x0, ld.kvh) : 0;
-        const long long s1 = ok1 ? paged_slot(p.kv, page1, x0 + 16, ld.kvh) : 0;
+      const bool mine = lane < n_box && x0 + lane * box < ld.hi && x0 + (lane + 1) * box > ld.lo;
+      const bool there = page >= 0 && page < p.kv.P;
+      if (mine && !there) set_status(p.status, kDevBadInput);
+      const unsigned in = __ballot_sync(0xffffffffu, mine), good = __ballot_sync(0xffffffffu, mine && there);
+      if (lane == 0) {
+        PdNote *note = &notes[ld_stage];
+        note->x0 = x0;
+        note->lo = ld.lo;
+        note->hi = ld.hi;
+        note->first_at = ld.s.L + ld.t0;
+        note->rows = ld.nt * p.G;
+        note->flags = (first_tile ? kPdFirst : 0) | (ld.j + 1 == ld.j1 ? kPdEnds : 0) | (ld.left == 1 ? kPdLast : 0);
+        note->b = ld.b;
+        note->kvh = ld.kvh;
+        note->t0 = ld.t0;
+        note->row0 = ld.s.row0;
+        note->j01 = ld.j1 - ld.j0;
+        note->u0 = ld.u0;
+        // a box on no page comes as zeros (its scales stay what they were)
+        if (alive) mbar_arrive_expect_tx(bar, __popc(in) * box * C::ROWB * NSUB * 2 + (FP8 ? __popc(good) * box * 8 : 0));
+      }
+      __syncwarp();
+      if (mine && alive) {
+        const int y = (ld.kvh << p.kv.page_shift) + (x0 & ((1 << p.kv.page_shift) - 1)), z = there ? page : p.kv.P;
 #pragma unroll
-        for (int i = lane; i < KC * CPR; i += 32) {
-          const int key = i / CPR, c = i % CPR, x = x0 + key;
-          const bool second = KC == 32 && key >= 16;
-          const bool ok = (second ? ok1 : ok0) && x >= ld.lo && x < ld.hi;
-          const long long slot = (second ? s1 : s0) + (key & 15);
-          const long long at = ok ? slot * C::ROWB + c * 16 : 0;
-          cp_async16(st + pd_off<CPR>(key, c), p.kv.k + at, ok);
-          cp_async16(st + C::KV_BYTES + pd_off<CPR>(key, c), p.kv.v + at, ok);
+        for (int sub = 0; sub < NSUB; ++sub) {
+          tma_load_3d(st + sub * C::SUB_BYTES + lane * box * C::ROWB, &tmK, bar, sub * 64, y, z);
+          tma_load_3d(st + C::KV_BYTES + sub * C::SUB_BYTES + lane * box * C::ROWB, &tmV, bar, sub * 64, y, z);
         }
-        if constexpr (FP8) {
-          const int x = x0 + lane;
-          const bool second = lane >= 16;
-          const bool ok = (second ? ok1 : ok0) && x >= ld.lo && x < ld.hi;
-          const long long slot = ok ? (second ? s1 : s0) + (lane & 15) : 0;
-          cp_async4(st + 2 * C::KV_BYTES + lane * 4, p.kv.ks + slot, ok);
-          cp_async4(st + 2 * C::KV_BYTES + (KC + lane) * 4, p.kv.vs + slot, ok);
+        if (FP8 && there) {
+          const long long at = paged_slot(p.kv, page, x0 + lane * box, ld.kvh);
+          bulk_load(ring_sc + ld_stage * 2 * KC + lane * box, p.kv.ks + at, box * 4, bar);
+          bulk_load(ring_sc + ld_stage * 2 * KC + KC + lane * box, p.kv.vs + at, box * 4, bar);
         }
       }
+      __syncwarp();
+      if (alive) ++asked;
+      first_tile = ld.j + 1 == ld.j1;
       paged_next(p, ld);
-      fetch_pages();
+      fetch_page();
     }
-    cp_async_commit();
     ld_stage = ld_stage + 1 == NS ? 0 : ld_stage + 1;
   };
+  if (warp == 0) {
+    ask_q();
+    ask_q();
+  }
 #pragma unroll
   for (int i = 0; i < NS - 1; ++i) produce();
 
   // ---- state of the rows: row g8 + 8 i of m-tile rt
   float o[RT][ND8][4], m[RT][2], l[RT][2];
-  uint32_t qf[RT][HD / 16][4];
-  int at[RT][2];                                  // a row's own position, -1: no such row
-  auto begin_unit = [&]() {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = rt * 16 + g8 + 8 * i;
-        const bool live = r < cur.nt * p.G;
-        at[rt][i] = live ? cur.s.L + cur.t0 + r / p.G : -1;
-        m[rt][i] = -INFINITY;
-        l[rt][i] = 0.f;
-        const long long base = live ? paged_unit_row(p.q, p, cur.s, cur.b, cur.t0, cur.kvh, r) : 0;
-#pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          // codes: a lane's fragments of four k-steps are 16 neighbouring bytes of the key,
-          // so step s of group g takes the dims 64 g + 16 c4 + 4 s .. + 3 there
-          const int d0 = FP8 ? (ks >> 2) * 64 + 16 * c4 + 4 * (ks & 3) : 16 * ks + 2 * c4;
-          const int d1 = FP8 ? d0 + 2 : d0 + 8;
-          qf[rt][ks][i] = live ? pd_q2(p.q.data, base + d0) : 0u;
-          qf[rt][ks][2 + i] = live ? pd_q2(p.q.data, base + d1) : 0u;
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < ND8; ++d)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[rt][d][e] = 0.f;
+  [[maybe_unused]] uint32_t qf[RT][HD / 16][4];
+  uint32_t units = 0, phase = 0;
+  int stage = 0;
+  // A fragments of k-step ks.  Codes: a lane's B fragments of four k-steps are 16
+  // neighbouring bytes of the key, so step s of group g takes the dims
+  // 64 g + 16 c4 + 4 s .. + 3 there, and the queries' fragments the same.
+  auto load_a = [&](uint32_t q_s, int rt, int ks, uint32_t (&a)[4]) {
+    const uint32_t sub = q_s + (ks >> 2) * (RT * 16 * 128) + rt * (16 * 128);
+    if constexpr (FP8) {
+      const int ch = 2 * c4 + ((ks & 3) >> 1);
+      const uint2 u = pd_lds64(sub + g8 * 128 + ((ch ^ g8) << 4) + (ks & 1) * 8);
+      const uint2 v = pd_lds64(sub + (g8 + 8) * 128 + ((ch ^ g8) << 4) + (ks & 1) * 8);
+      a[0] = u.x;
+      a[1] = v.x;
+      a[2] = u.y;
+      a[3] = v.y;
+    } else {
+      pd_ldsm4(a, sub + (lane & 15) * 128 + ((((ks & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
     }
   };
-  begin_unit();
-
-  int stage = 0;
-  bool in_unit = first_in;
+  // where this lane's pieces of the keys and values lie in a box (the boxes' swizzle:
+  // 128-byte rows by the row's last three bits, 64-byte rows by its bits 1 and 2)
+  // codes of hd 128: fragment column n reads key (n >> 1) + 4 (n & 1) of eight, so that
+  // two rows' pieces meet different banks; the weights' columns follow
+  constexpr bool PERM = FP8 && HD == 128;
+  auto key_of = [](int n) { return PERM ? (n & ~7) | ((n & 7) >> 1) | ((n & 1) << 2) : n; };
   while (true) {
-    cp_async_wait<NS - 2>();
-    __syncwarp();                                 // every lane's copies, and its reads of the stage to refill
-    produce();
-    const int x0 = (cur.j << C::BK_SHIFT) + warp * KC;
-    if (x0 < cur.hi && x0 + KC > cur.lo) {
-      const uint8_t *st = ring + stage * C::STAGE;
-      const uint32_t k_s = smem_u32(st), v_s = k_s + C::KV_BYTES;
-      const float *scales = reinterpret_cast<const float *>(st + 2 * C::KV_BYTES);
-      // ---- S = Q K^T
-      float s[RT][NT8][4];
-#pragma unroll
-      for (int n = 0; n < NT8; ++n) {
+    if (alive && !__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, abort_flag, p.wait_ns))) {
+      // give up: what was asked for has a second to land, and the rest is done without
+      set_status(p.status, kPdTimeout);
+      *abort_flag = 1;
+      alive = false;
+    }
+    __syncwarp();
+    produce();                                    // into the stage read last, which every lane has left
+    const uint8_t *st = ring + stage * C::STAGE;
+    const PdNote *note = &notes[stage];
+    const int x0 = note->x0, lo = note->lo, hi = note->hi, first_at = note->first_at, rows = note->rows, flags = note->flags;
+    const uint32_t q_s = smem_u32(smem + C::OFF_Q + (units & 1) * C::Q_BYTES);
+    if (flags & kPdFirst) {
+      // ---- a new unit
+      if (alive && !__all_sync(0xffffffffu, mbar_wait_bounded(&q_full[units & 1], (units >> 1) & 1, abort_flag, p.wait_ns))) {
+        set_status(p.status, kPdTimeout);
+        *abort_flag = 1;
+        alive = false;
+      }
+      if constexpr (C::Q_REGS) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[rt][n][e] = 0.f;
+          for (int ks = 0; ks < HD / 16; ++ks) load_a(q_s, rt, ks, qf[rt][ks]);
+      }
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          m[rt][i] = -INFINITY;
+          l[rt][i] = 0.f;
+        }
+#pragma unroll
+        for (int d = 0; d < ND8; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[rt][d][e] = 0.f;
+      }
+    }
+    if (x0 < hi && x0 + KC > lo) {
+      const uint32_t k_s = smem_u32(st), v_s = k_s + C::KV_BYTES;
+      float *scales = ring_sc + stage * 2 * KC;
+      if (x0 < lo || x0 + KC > hi) {
+        // keys out of sight: their values, or the values' scales, become zeros
         if constexpr (FP8) {
-          const int key = n * 8 + g8;
-#pragma unroll
-          for (int gr = 0; gr < HD / 64; ++gr) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(st + pd_off<CPR>(key, gr * 4 + c4));
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              const uint32_t b0 = e4m3_bf16x2(__byte_perm(ws[q4], 0, 0x1404)), b1 = e4m3_bf16x2(__byte_perm(ws[q4], 0, 0x3424));
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) pd_mma(s[rt][n], qf[rt][gr * 4 + q4], b0, b1);
-            }
-          }
+          if (lane < KC && (x0 + lane < lo || x0 + lane >= hi)) scales[KC + lane] = 0.f;
         } else {
+          for (int i = lane; i < KC * 8 * NSUB; i += 32) {
+            const int key = (i >> 3) % KC;
+            if (x0 + key < lo || x0 + key >= hi)
+              *reinterpret_cast<uint4 *>(ring + stage * C::STAGE + C::KV_BYTES + (i >> 3) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_proxy_async_smem();                 // before the stage's next boxes
+        __syncwarp();
+      }
+      // ---- S = Q K^T
+      float s[RT][NT8][4];
 #pragma unroll
-          for (int k2 = 0; k2 < HD / 32; ++k2) {
-            uint32_t b[4];
-            pd_ldsm4(b, k_s + pd_off<CPR>(n * 8 + (lane & 7), k2 * 4 + (lane >> 3)));
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int n = 0; n < NT8; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[rt][n][e] = 0.f;
+      if constexpr (FP8) {
+#pragma unroll
+        for (int gr = 0; gr < HD / 64; ++gr) {
+          uint4 w[NT8];
+#pragma unroll
+          for (int n = 0; n < NT8; ++n) {
+            const int key = n * 8 + key_of(g8);
+            const uint32_t ch = gr * 4 + c4;
+            w[n] = pd_lds128(k_s + key * C::ROWB + ((HD == 64 ? ch ^ ((key >> 1) & 3) : ch ^ (key & 7)) << 4));
+          }
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t a[RT][4];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
-              pd_mma(s[rt][n], qf[rt][2 * k2], b[0], b[1]);
-              pd_mma(s[rt][n], qf[rt][2 * k2 + 1], b[2], b[3]);
+              if constexpr (C::Q_REGS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[rt][e] = qf[rt][gr * 4 + q4][e];
+              } else {
+                load_a(q_s, rt, gr * 4 + q4, a[rt]);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NT8; ++n) {
+              const uint32_t u = q4 == 0 ? w[n].x : q4 == 1 ? w[n].y : q4 == 2 ? w[n].z : w[n].w;
+              const uint32_t b0 = e4m3_bf16x2(__byte_perm(u, 0, 0x1404)), b1 = e4m3_bf16x2(__byte_perm(u, 0, 0x3424));
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) pd_mma(s[rt][n], a[rt], b0, b1);
+            }
+          }
+        }
+      } else {
+        const uint32_t k_lane = k_s + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+#pragma unroll
+        for (int k2 = 0; k2 < HD / 32; ++k2) {
+          uint32_t a[RT][2][4];
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if constexpr (C::Q_REGS) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a[rt][h][e] = qf[rt][2 * k2 + h][e];
+              } else {
+                load_a(q_s, rt, 2 * k2 + h, a[rt][h]);
+              }
+            }
+#pragma unroll
+          for (int n = 0; n < NT8; ++n) {
+            uint32_t b[4];
+            pd_ldsm4(b, (k_lane ^ ((k2 & 1) * 64)) + (k2 >> 1) * C::SUB_BYTES + n * 1024);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              pd_mma(s[rt][n], a[rt][0], b[0], b[1]);
+              pd_mma(s[rt][n], a[rt][1], b[2], b[3]);
             }
           }
         }
       }
-      // ---- scores in the exp2 domain, masked where a row does not see the key
-      const int first_at = cur.s.L + cur.t0;      // the first row's position
-      const bool edge = x0 + KC - 1 > first_at || x0 < cur.lo || (p.window > 0 && x0 <= first_at + cur.nt - 1 - p.window) ||
-                        RT * 16 > cur.nt * p.G;
+      // ---- scores in the exp2 domain, replaced where a row does not see the key
+      const bool edge = x0 + KC - 1 > first_at || x0 < lo || (p.window > 0 && x0 <= first_at + (rows - 1) / p.G - p.window);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
+        if constexpr (FP8) {
+#pragma unroll
+          for (int n = 0; n < NT8; ++n) {
+            const float k0 = scales[n * 8 + key_of(2 * c4)] * p.scale_log2, k1 = scales[n * 8 + key_of(2 * c4 + 1)] * p.scale_log2;
+            s[rt][n][0] *= k0;
+            s[rt][n][1] *= k1;
+            s[rt][n][2] *= k0;
+            s[rt][n][3] *= k1;
+          }
+        }
+        if (edge) {
+          int own[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) own[i] = first_at + (rt * 16 + g8 + 8 * i) / p.G;   // past the unit's rows: not written
+#pragma unroll
+          for (int n = 0; n < NT8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int x = x0 + n * 8 + key_of(2 * c4 + (e & 1));
+              if (x > own[e >> 1] || (p.window > 0 && x <= own[e >> 1] - p.window)) s[rt][n][e] = -INFINITY;
+            }
+        }
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int n = 0; n < NT8; ++n) {
-          float2 ks = make_float2(p.scale_log2, p.scale_log2);
-          if constexpr (FP8) {
-            const float2 t = *reinterpret_cast<const float2 *>(scales + n * 8 + 2 * c4);
-            ks.x *= t.x;
-            ks.y *= t.y;
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v = s[rt][n][e] * ((e & 1) ? ks.y : ks.x);
-            if (edge) {
-              const int x = x0 + n * 8 + 2 * c4 + (e & 1), own = at[rt][e >> 1];
-              if (x > own || x < cur.lo || (p.window > 0 && x <= own - p.window)) v = -INFINITY;
-            }
-            s[rt][n][e] = v;
-            mx[e >> 1] = fmaxf(mx[e >> 1], v);
-          }
+          mx[0] = fmax3(mx[0], s[rt][n][0], s[rt][n][1]);
+          mx[1] = fmax3(mx[1], s[rt][n][2], s[rt][n][3]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
           mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+          if (!FP8) mx[i] *= p.scale_log2;        // scale > 0; -inf stays -inf
         }
-        const bool grows = mx[0] > m[rt][0] || mx[1] > m[rt][1];
-        if (__any_sync(0xffffffffu, grows)) {
+        if (__any_sync(0xffffffffu, mx[0] > m[rt][0] || mx[1] > m[rt][1])) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float mn = fmaxf(m[rt][i], mx[i]);
@@ -280,15 +445,23 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
             }
           }
         }
-        const float mu[2] = {m[rt][0] == -INFINITY ? 0.f : m[rt][0], m[rt][1] == -INFINITY ? 0.f : m[rt][1]};
 #pragma unroll
-        for (int n = 0; n < NT8; ++n)
+        for (int i = 0; i < 2; ++i) {
+          const float mu = m[rt][i] == -INFINITY ? 0.f : m[rt][i];
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float w = ex2_approx(s[rt][n][e] - mu[e >> 1]);
-            l[rt][e >> 1] += w;
-            s[rt][n][e] = w;
+          for (int n = 0; n < NT8; ++n) {
+            float2 x;
+            if constexpr (FP8) x = fadd2(s[rt][n][2 * i], s[rt][n][2 * i + 1], -mu, -mu);
+            else x = ffma2(s[rt][n][2 * i], s[rt][n][2 * i + 1], p.scale_log2, -mu);
+            x.x = ex2_approx(x.x);
+            x.y = ex2_approx(x.y);
+            sum = fadd2(sum.x, sum.y, x.x, x.y);
+            s[rt][n][2 * i] = x.x;
+            s[rt][n][2 * i + 1] = x.y;
           }
+          l[rt][i] += sum.x + sum.y;
+        }
       }
       // ---- O += P V; P rounded to bf16, the tensor core's operand type
 #pragma unroll
@@ -296,8 +469,8 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
         uint32_t a[RT][4];
         float2 vs0 = make_float2(1.f, 1.f), vs1 = vs0;
         if constexpr (FP8) {
-          vs0 = *reinterpret_cast<const float2 *>(scales + KC + k16 * 16 + 2 * c4);
-          vs1 = *reinterpret_cast<const float2 *>(scales + KC + k16 * 16 + 8 + 2 * c4);
+          vs0 = make_float2(scales[KC + k16 * 16 + key_of(2 * c4)], scales[KC + k16 * 16 + key_of(2 * c4 + 1)]);
+          vs1 = make_float2(scales[KC + k16 * 16 + 8 + key_of(2 * c4)], scales[KC + k16 * 16 + 8 + key_of(2 * c4 + 1)]);
         }
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -307,14 +480,16 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
           a[rt][2] = pack_bf16x2(g[0] * vs1.x, g[1] * vs1.y);
           a[rt][3] = pack_bf16x2(g[2] * vs1.x, g[3] * vs1.y);
         }
-        const int key = k16 * 16 + (lane & 15), half = lane >> 4;
         if constexpr (FP8) {
           // a transposed load gives pairs of neighbouring dims: the even dims of 16 go
           // to one accumulator column block, the odd ones to the next
+          const int key = k16 * 16 + key_of(lane & 15);
+          const uint32_t row = v_s + key * C::ROWB;
 #pragma unroll
-          for (int c2 = 0; c2 < CPR / 2; ++c2) {
+          for (int c2 = 0; c2 < HD / 32; ++c2) {
             uint32_t b[4];
-            pd_ldsm4_t(b, v_s + pd_off<CPR>(key, 2 * c2 + half));
+            const uint32_t ch = 2 * c2 + (lane >> 4);
+            pd_ldsm4_t(b, row + ((HD == 64 ? ch ^ ((key >> 1) & 3) : ch ^ (key & 7)) << 4));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const uint32_t e0 = e4m3_bf16x2(__byte_perm(b[2 * h], 0, 0x2404)), e1 = e4m3_bf16x2(__byte_perm(b[2 * h + 1], 0, 0x2404));
@@ -327,10 +502,11 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
             }
           }
         } else {
+          const uint32_t v_lane = v_s + k16 * 2048 + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
 #pragma unroll
-          for (int c2 = 0; c2 < CPR / 2; ++c2) {
+          for (int c2 = 0; c2 < HD / 16; ++c2) {
             uint32_t b[4];
-            pd_ldsm4_t(b, v_s + pd_off<CPR>(key, 2 * c2 + half));
+            pd_ldsm4_t(b, (v_lane ^ ((c2 & 3) * 32)) + (c2 >> 2) * C::SUB_BYTES);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
               pd_mma(o[rt][2 * c2], a[rt], b[0], b[1]);
@@ -340,10 +516,13 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
         }
       }
     }
-    stage = stage + 1 == NS ? 0 : stage + 1;
-    const bool unit_ends = cur.j + 1 == cur.j1, last = cur.left == 1;
-    if (unit_ends || last) {
-      // ---- merge the warps' states: 4, 5 into 0, 1; 6, 7 into 2, 3; 2, 3 into 0, 1; 1 into 0
+    if (flags & (kPdEnds | kPdLast)) {
+      // ---- the unit, or this CTA's part of it, is done: merge the warps' states: 4, 5
+      // into 0, 1; 6, 7 into 2, 3; 2, 3 into 0, 1; 1 into 0
+      const PdNote u = *note;
+      const bool in_unit = units == 0 && started_inside, whole = (flags & kPdEnds) && !in_unit;
+      PagedSeq us{};
+      us.row0 = u.row0;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -392,7 +571,6 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
         }
         __syncthreads();
       }
-      const bool whole = unit_ends && !in_unit;
       if (warp == 0) {
         float *part = paged_part(p.ws, cta, in_unit ? 0 : 1, RT * 16, HD);
 #pragma unroll
@@ -400,56 +578,73 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1) paged_few_rows
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = rt * 16 + g8 + 8 * i;
-            const bool live = at[rt][i] >= 0;
+            if (r >= rows) continue;
             const float inv = l[rt][i] > 0.f ? 1.f / l[rt][i] : 0.f;
-            const long long out = live && whole ? paged_unit_row(p.o, p, cur.s, cur.b, cur.t0, cur.kvh, r) : 0;
+            const long long out = whole ? paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r) : 0;
             float *row = part + r * HD;
-            if (live) {
 #pragma unroll
-              for (int d = 0; d < ND8; ++d) {
-                const float x = o[rt][d][2 * i], y = o[rt][d][2 * i + 1];
-                if constexpr (FP8) {
-                  if (d & 1) continue;
-                  const float x1 = o[rt][d + 1][2 * i], y1 = o[rt][d + 1][2 * i + 1];   // the odd dims
-                  const int dim = d * 8 + 4 * c4;
-                  if (whole)
-                    *reinterpret_cast<uint2 *>(p.o.data + (out + dim) * 2) =
-                        p.o_f16 ? make_uint2(pack_f16x2(x * inv, x1 * inv), pack_f16x2(y * inv, y1 * inv))
-                                : make_uint2(pack_bf16x2(x * inv, x1 * inv), pack_bf16x2(y * inv, y1 * inv));
-                  else
-                    *reinterpret_cast<float4 *>(row + dim) = make_float4(x, x1, y, y1);
-                } else {
-                  const int dim = d * 8 + 2 * c4;
-                  if (whole)
-                    *reinterpret_cast<uint32_t *>(p.o.data + (out + dim) * 2) =
-                        p.o_f16 ? pack_f16x2(x * inv, y * inv) : pack_bf16x2(x * inv, y * inv);
-                  else
-                    *reinterpret_cast<float2 *>(row + dim) = make_float2(x, y);
-                }
+            for (int d = 0; d < ND8; ++d) {
+              const float x = o[rt][d][2 * i], y = o[rt][d][2 * i + 1];
+              if constexpr (FP8) {
+                if (d & 1) continue;
+                const float x1 = o[rt][d + 1][2 * i], y1 = o[rt][d + 1][2 * i + 1];   // the odd dims
+                const int dim = d * 8 + 4 * c4;
+                if (whole)
+                  *reinterpret_cast<uint2 *>(p.o.data + (out + dim) * 2) =
+                      p.o_f16 ? make_uint2(pack_f16x2(x * inv, x1 * inv), pack_f16x2(y * inv, y1 * inv))
+                              : make_uint2(pack_bf16x2(x * inv, x1 * inv), pack_bf16x2(y * inv, y1 * inv));
+                else
+                  __stcg(reinterpret_cast<float4 *>(row + dim), make_float4(x, x1, y, y1));
+              } else {
+                const int dim = d * 8 + 2 * c4;
+                if (whole)
+                  *reinterpret_cast<uint32_t *>(p.o.data + (out + dim) * 2) =
+                      p.o_f16 ? pack_f16x2(x * inv, y * inv) : pack_bf16x2(x * inv, y * inv);
+                else
+                  __stcg(reinterpret_cast<float2 *>(row + dim), make_float2(x, y));
               }
-              if (!whole && c4 == 0) *reinterpret_cast<float2 *>(part + RT * 16 * HD + 2 * r) = make_float2(m[rt][i], l[rt][i]);
             }
+            if (!whole && c4 == 0) __stcg(reinterpret_cast<float2 *>(part + RT * 16 * HD + 2 * r), make_float2(m[rt][i], l[rt][i]));
           }
       }
-      if (in_unit) {
-        meta.in = 1;
-        meta.ends = unit_ends;
-      } else if (!unit_ends) {
-        meta.out = 1;
-        meta.b = cur.b;
-        meta.qt = cur.qt;
-        meta.kvh = cur.kvh;
+      if (!whole) {
+        // ---- the CTA that brings a unit's last part combines them all
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+          const int c0 = paged_worker_of(u.u0, total, workers), n = paged_worker_of(u.u0 + u.j01 - 1, total, workers) - c0 + 1;
+          int *count = reinterpret_cast<int *>(p.ws + kPagedCountOff) + c0;
+          const bool mine = atomicAdd(count, 1) == n - 1;
+          if (mine) atomicExch(count, 0);         // for the next call
+          s_parts[0] = c0;
+          s_parts[1] = mine ? n : 0;
+        }
+        __syncthreads();
+        const int c0 = s_parts[0], n = s_parts[1];
+        if (n > 0) {
+          __threadfence();
+          float *weight = merge + warp * kPagedMaxCtas;
+          for (int r = warp; r < rows; r += C::NW)
+            paged_combine_row<HD>(p, RT * 16, c0, n, r, weight, paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r));
+          __syncthreads();
+        }
       }
-      if (last) break;
-      in_unit = false;
-      paged_next(p, cur);
-      begin_unit();
-    } else {
-      paged_next(p, cur);
+      ++units;
+      if (flags & kPdLast) break;
+      if (warp == 0) ask_q();                     // of the unit after the next
+    }
+    if (++stage == NS) {
+      stage = 0;
+      phase ^= 1;
     }
   }
-  cp_async_wait<0>();
-  if (threadIdx.x == 0) paged_meta(p.ws)[cta] = meta;
+  if (!alive) {
+    // what this warp asked for lands before the block's shared memory goes
+    bool done = true;
+    for (uint32_t k = asked > NS ? asked - NS : 0; k < asked; ++k) done &= mbar_wait_drain(&full[k % NS], (k / NS) & 1);
+    for (uint32_t k = nq > 2 ? nq - 2 : 0; k < nq; ++k) done &= mbar_wait_drain(&q_full[k & 1], (k >> 1) & 1);
+    if (!done) set_status(p.status, kPdTimeout);
+  }
 }
 
 }  // namespace

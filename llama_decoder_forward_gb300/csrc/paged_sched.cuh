@@ -22,7 +22,8 @@ struct PagedIter {
   int t0, nt;                  // its first token, and how many
   int lo, hi;                  // the positions that some row of it sees: [lo, hi)
   PagedSeq s;
-  long long left;              // tiles of this worker still to do, this one included
+  int left;                    // tiles of this worker still to do, this one included
+  long long u0;                // the unit's first tile in the line
 };
 
 __device__ __forceinline__ int paged_cap(const PagedAttnParams &p) { return p.kv.max_pages << p.kv.page_shift; }
@@ -45,6 +46,7 @@ __device__ __forceinline__ void paged_set_unit(const PagedAttnParams &p, PagedIt
 __device__ __forceinline__ void paged_next(const PagedAttnParams &p, PagedIter &it) {
   if (--it.left <= 0) return;
   if (++it.j < it.j1) return;
+  it.u0 += it.j1 - it.j0;
   if (++it.kvh == p.kv.KV) {
     it.kvh = 0;
     if (++it.qt * p.tt >= it.s.n) {
@@ -71,12 +73,19 @@ __device__ __forceinline__ long long paged_seq_tiles(const PagedAttnParams &p, c
 }
 
 struct PagedSchedSmem {
-  long long warp_sum[32];
+  long long warp_sum[32], total;
+  int workers;
   PagedIter start;
 };
 
-// Worker `w` of `workers`: its first tile and how many it has (left == 0: none).
-// Called by all THREADS threads of the CTA.
+// The worker that has tile x of the line.
+__device__ __forceinline__ int paged_worker_of(long long x, long long total, int workers) {
+  return static_cast<int>(((x + 1) * workers - 1) / total);
+}
+
+// Worker `w` of `workers`: its first tile and how many it has (left == 0: none; the
+// line is cut for as many workers as it has tiles, at most).  Called by all THREADS
+// threads of the CTA.
 template <int THREADS>
 __device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int w, int workers, PagedSchedSmem &sm) {
   constexpr int W = THREADS / 32;
@@ -99,9 +108,14 @@ __device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int 
 #pragma unroll
   for (int i = 0; i < W; ++i) total += sm.warp_sum[i];
   __syncthreads();
-  const long long from = total * w / workers, to = total * (w + 1) / workers;
   PagedIter it{};
-  if (from == to) return it;                      // the same for the whole CTA
+  if (total < workers) workers = static_cast<int>(total);
+  if (tid == 0) {
+    sm.total = total;
+    sm.workers = workers;
+  }
+  if (w >= workers) return it;                    // the same for the whole CTA
+  const long long from = total * w / workers, to = total * (w + 1) / workers;
   // the sequence that holds tile `from`, THREADS sequences at a time
   long long before = 0;
   for (int base = 0; base < p.c.B; base += THREADS) {
@@ -131,7 +145,7 @@ __device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int 
     if (pre <= from && from < pre + n) {
       it.b = b;
       it.s = s;
-      it.left = to - from;
+      it.left = static_cast<int>(to - from);
       long long off = from - pre;
       for (it.qt = 0;; ++it.qt) {
         paged_set_unit(p, it);
@@ -139,6 +153,7 @@ __device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int 
         if (off < all) {
           it.kvh = static_cast<int>(off / unit);
           it.j = it.j0 + static_cast<int>(off - it.kvh * unit);
+          it.u0 = from - (it.j - it.j0);
           break;
         }
         off -= all;
@@ -160,14 +175,64 @@ struct PagedMeta {
   int out;                     // place 1 is used
   int b, qt, kvh;              // place 1's unit
 };
+// (The few-rows kernel needs no note: it finds a unit's CTAs by arithmetic.)
 constexpr int kPagedMaxCtas = 160;
-constexpr size_t kPagedMetaOff = 1024, kPagedPartOff = kPagedMetaOff + kPagedMaxCtas * sizeof(PagedMeta) + 256;
+// After the status word: a counter for each CTA, of the parts of the unit that it
+// began (zero between calls); the notes; the parts.
+constexpr size_t kPagedCountOff = 256, kPagedMetaOff = 1024, kPagedPartOff = kPagedMetaOff + kPagedMaxCtas * sizeof(PagedMeta) + 256;
 
 // Place of CTA c: rows of HD sums, then (maximum, sum) of each row.
 __device__ __forceinline__ float *paged_part(uint8_t *ws, int c, int place, int rows, int hd) {
   return reinterpret_cast<float *>(ws + kPagedPartOff) + (static_cast<long long>(c) * 2 + place) * rows * (hd + 2);
 }
 __device__ __forceinline__ PagedMeta *paged_meta(uint8_t *ws) { return reinterpret_cast<PagedMeta *>(ws + kPagedMetaOff); }
+
+// Row r of a unit from its n parts: CTA c0's place 1 and the place 0 of the ones
+// behind it, in that order; o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  One
+// warp; `weight`: n floats of shared memory of its own; `out`: the row's offset.
+template <int HD>
+__device__ __forceinline__ void paged_combine_row(const PagedAttnParams &p, int rows, int c0, int n, int r, float *weight,
+                                                  long long out) {
+  const int lane = threadIdx.x & 31;
+  float mx = -INFINITY, sum = 0.f;
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, __ldcg(paged_part(p.ws, c0 + i, i == 0, rows, HD) + rows * HD + 2 * r));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  for (int i = lane; i < n; i += 32) {
+    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(paged_part(p.ws, c0 + i, i == 0, rows, HD) + rows * HD + 2 * r));
+    const float a = mx == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
+    weight[i] = a;
+    sum += a * ml.y;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  __syncwarp();
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  float acc[HD / 32];
+#pragma unroll
+  for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float *row = paged_part(p.ws, c0 + i, i == 0, rows, HD) + r * HD + lane * (HD / 32);
+    const float a = weight[i];
+    if constexpr (HD == 64) {
+      const float2 v = __ldcg(reinterpret_cast<const float2 *>(row));
+      acc[0] += a * v.x;
+      acc[1] += a * v.y;
+    } else {
+      const float4 v = __ldcg(reinterpret_cast<const float4 *>(row));
+      acc[0] += a * v.x;
+      acc[1] += a * v.y;
+      acc[2] += a * v.z;
+      acc[3] += a * v.w;
+    }
+  }
+  uint32_t *to = reinterpret_cast<uint32_t *>(p.o.data + (out + lane * (HD / 32)) * 2);
+#pragma unroll
+  for (int e = 0; e < HD / 64; ++e)
+    to[e] = p.o_f16 ? pack_f16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv) : pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  __syncwarp();                                   // the weights are rewritten
+}
 
 // Element offset of row r (token r / g, head r % g) of a unit in q or out.
 __device__ __forceinline__ long long paged_unit_row(const PagedRows &x, const PagedAttnParams &p, const PagedSeq &s, int b,
