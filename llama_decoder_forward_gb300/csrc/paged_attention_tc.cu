@@ -86,16 +86,10 @@ enum : int { kPtTimeoutLoad = 0x205, kPtTimeoutMma = 0x206, kPtTimeoutSoftmax = 
 
 constexpr uint32_t kColS = 0, kColO = 256;                   // tensor memory columns: S (and P), O
 
-__device__ __forceinline__ uint32_t pt_code_pair(uint32_t x) {
-  const uint32_t u = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u), two120 = 0x7b807b80u;
-  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&u), *reinterpret_cast<const __nv_bfloat162 *>(&two120));
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// Eight codes (two words) to eight bf16.
+// Eight codes (two words) to eight bf16, exactly.
 __device__ __forceinline__ uint4 pt_codes8(uint32_t a, uint32_t b) {
-  return make_uint4(pt_code_pair(__byte_perm(a, 0, 0x1404)), pt_code_pair(__byte_perm(a, 0, 0x3424)),
-                    pt_code_pair(__byte_perm(b, 0, 0x1404)), pt_code_pair(__byte_perm(b, 0, 0x3424)));
+  const float2 f0 = unpack_e4m3x2(a), f1 = unpack_e4m3x2(a >> 16), f2 = unpack_e4m3x2(b), f3 = unpack_e4m3x2(b >> 16);
+  return make_uint4(pack_bf16x2(f0.x, f0.y), pack_bf16x2(f1.x, f1.y), pack_bf16x2(f2.x, f2.y), pack_bf16x2(f3.x, f3.y));
 }
 
 template <int HD, bool FP8, int NQ>

@@ -16,13 +16,13 @@
 // the whole step here.  The fragments of a step stay in registers; with 32 rows the
 // queries' are read from shared memory each time (they would spill).
 //
-// e4m3 codes become bf16 exactly: the code's 7 bits moved to the bf16 exponent and
-// mantissa are the value times 2^-120 (subnormal codes included), one exact
-// product restores it.  The keys' scales multiply the scores, the values' scales
-// the weights, so no dequantised value is rounded.
+// e4m3 codes become bf16 exactly, by way of f16 and fp32: four cycles of the integer
+// pipe for a pair (shifting the bits into place took eight).
+// The keys' scales multiply the scores, the values' scales the weights, so no
+// dequantised value is rounded.
 //
 // Slots outside the rows' sight may hold anything: their scores are replaced before
-// they are looked at, their values (bf16) or scales (e4m3) set to zero.
+// they are looked at, their values (and values' scales) set to zero.
 #pragma once
 
 #include "paged_sched.cuh"
@@ -57,14 +57,6 @@ __device__ __forceinline__ uint2 pd_lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
-}
-
-// Two e4m3 codes in the high bytes of the halves of x to a bf16 pair.
-__device__ __forceinline__ uint32_t e4m3_bf16x2(uint32_t x) {
-  const uint32_t u = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-  const uint32_t two120 = 0x7b807b80u;
-  const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&u), *reinterpret_cast<const __nv_bfloat162 *>(&two120));
-  return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 template <int HD, bool FP8, int RT>
@@ -313,15 +305,12 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
       const uint32_t k_s = smem_u32(st), v_s = k_s + C::KV_BYTES;
       float *scales = ring_sc + stage * 2 * KC;
       if (x0 < lo || x0 + KC > hi) {
-        // keys out of sight: their values, or the values' scales, become zeros
-        if constexpr (FP8) {
-          if (lane < KC && (x0 + lane < lo || x0 + lane >= hi)) scales[KC + lane] = 0.f;
-        } else {
-          for (int i = lane; i < KC * 8 * NSUB; i += 32) {
-            const int key = (i >> 3) % KC;
-            if (x0 + key < lo || x0 + key >= hi)
-              *reinterpret_cast<uint4 *>(ring + stage * C::STAGE + C::KV_BYTES + (i >> 3) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
+        // keys out of sight: their values (and the values' scales) become zeros
+        if (FP8 && lane < KC && (x0 + lane < lo || x0 + lane >= hi)) scales[KC + lane] = 0.f;
+        for (int i = lane; i < C::KV_BYTES / 16; i += 32) {
+          const int key = i / (C::ROWB / 16) % KC;
+          if (x0 + key < lo || x0 + key >= hi)
+            *reinterpret_cast<uint4 *>(ring + stage * C::STAGE + C::KV_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();                 // before the stage's next boxes
         __syncwarp();
@@ -359,7 +348,8 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
 #pragma unroll
             for (int n = 0; n < NT8; ++n) {
               const uint32_t u = q4 == 0 ? w[n].x : q4 == 1 ? w[n].y : q4 == 2 ? w[n].z : w[n].w;
-              const uint32_t b0 = e4m3_bf16x2(__byte_perm(u, 0, 0x1404)), b1 = e4m3_bf16x2(__byte_perm(u, 0, 0x3424));
+              const float2 f0 = unpack_e4m3x2(u), f1 = unpack_e4m3x2(u >> 16);
+              const uint32_t b0 = pack_bf16x2(f0.x, f0.y), b1 = pack_bf16x2(f1.x, f1.y);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) pd_mma(s[rt][n], a[rt], b0, b1);
             }
@@ -492,8 +482,10 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
             pd_ldsm4_t(b, row + ((HD == 64 ? ch ^ ((key >> 1) & 3) : ch ^ (key & 7)) << 4));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t e0 = e4m3_bf16x2(__byte_perm(b[2 * h], 0, 0x2404)), e1 = e4m3_bf16x2(__byte_perm(b[2 * h + 1], 0, 0x2404));
-              const uint32_t d0 = e4m3_bf16x2(b[2 * h] & 0xff00ff00u), d1 = e4m3_bf16x2(b[2 * h + 1] & 0xff00ff00u);
+              const float2 p0 = unpack_e4m3x2(b[2 * h]), p1 = unpack_e4m3x2(b[2 * h] >> 16);
+              const float2 p2 = unpack_e4m3x2(b[2 * h + 1]), p3 = unpack_e4m3x2(b[2 * h + 1] >> 16);
+              const uint32_t e0 = pack_bf16x2(p0.x, p1.x), e1 = pack_bf16x2(p2.x, p3.x);
+              const uint32_t d0 = pack_bf16x2(p0.y, p1.y), d1 = pack_bf16x2(p2.y, p3.y);
 #pragma unroll
               for (int rt = 0; rt < RT; ++rt) {
                 pd_mma(o[rt][4 * c2 + 2 * h], a[rt], e0, e1);

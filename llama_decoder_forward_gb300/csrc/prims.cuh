@@ -624,6 +624,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// Two e4m3 codes (the low 16 bits) as floats: exact, by way of f16.
+__device__ __forceinline__ float2 unpack_e4m3x2(uint32_t codes) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(h) : "r"(codes));
+  const __half2 v = *reinterpret_cast<const __half2 *>(&h);
+  return __half22float2(v);
+}
+
 __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
   __nv_bfloat162 v = *reinterpret_cast<__nv_bfloat162 *>(&u);
   return __bfloat1622float2(v);

@@ -8,6 +8,7 @@ there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from ctypes import POINTER, c_float, c_int, c_size_t, c_void_p
@@ -179,9 +180,17 @@ def _p(t: Optional[torch.Tensor]):
     return None if t is None else c_void_p(t.data_ptr())
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else None
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return c_void_p(s.cuda_stream)
+    """The stream's handle: the given one's, else the current device's current stream's (without building a
+    torch.cuda.Stream for it, which costs 3 us a call)."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _dev(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
@@ -462,36 +471,41 @@ class Chunk:
         return ctypes.byref(_ChunkStruct(*self._fields, rows)) if self.packed else self._ref
 
 
-def _rows(t: torch.Tensor, name: str, cache: PagedCache, chunk: Chunk, heads: int, layers: bool) -> _Rows:
-    """bf16 rows [(layers,) B, T, heads, head_dim], or [(layers,) rows, heads, head_dim] of a packed chunk."""
-    shape, strides = t.shape, t.stride()
-    lead = 1 if layers else 0
-    if t.dtype != torch.bfloat16 or t.device != cache.device or strides[-1] != 1:
-        raise ValueError(f"{name} must be bfloat16 on the cache's device, its last axis contiguous")
-    if layers and shape[0] != cache.n_layers:
-        raise ValueError(f"{name} must have a first axis of {cache.n_layers} layers")
-    if shape[lead + (1 if chunk.packed else 2):] != (heads, cache.head_dim) or (
-            not chunk.packed and shape[lead:lead + 2] != (chunk.B, chunk.T)):
-        raise ValueError(f"{name}: {tuple(shape)} does not fit the chunk ({heads} heads of {cache.head_dim}, "
-                         f"{'packed rows' if chunk.packed else (chunk.B, chunk.T)})")
+@functools.lru_cache(maxsize=1024)
+def _row_strides(shape, strides, lead, n_layers, packed, B, T, heads, hd):
+    """(layer, seq, row, head) strides of bf16 rows of that layout; a text where it does not fit."""
+    if strides[-1] != 1:
+        return "its last axis must be contiguous"
+    if lead and shape[0] != n_layers:
+        return f"it must have a first axis of {n_layers} layers"
+    if shape[lead + (1 if packed else 2):] != (heads, hd) or (not packed and shape[lead:lead + 2] != (B, T)):
+        return f"{tuple(shape)} does not fit the chunk ({heads} heads of {hd}, {'packed rows' if packed else (B, T)})"
     # the strides of axes of one entry say nothing (torch may give them any value)
-    st = [s if n > 1 else cache.head_dim for s, n in zip(strides[lead:-1], shape[lead:-1])]
-    seq = 0 if chunk.packed else st[0]
-    return _Rows(t.data_ptr(), strides[0] if layers and shape[0] > 1 else (cache.head_dim if layers else 0), seq, st[-2],
-                 st[-1])
+    st = [s if n > 1 else hd for s, n in zip(strides[:-1], shape[:-1])]
+    return st[0] if lead else hd, 0 if packed else st[lead], st[-2], st[-1]
+
+
+def _rows(t: torch.Tensor, name: str, cache: PagedCache, chunk: Chunk, heads: int, lead: int) -> _Rows:
+    """bf16 rows [(layers,) B, T, heads, head_dim], or [(layers,) rows, heads, head_dim] of a packed chunk."""
+    if t.dtype != torch.bfloat16 or t.device != cache.device:
+        raise ValueError(f"{name} must be bfloat16 on the cache's device")
+    st = _row_strides(t.shape, t.stride(), lead, cache.n_layers, chunk.packed, chunk.B, chunk.T, heads, cache.head_dim)
+    if isinstance(st, str):
+        raise ValueError(f"{name}: {st}")
+    return _Rows(t.data_ptr(), *st)
 
 
 def _same_place(cache: PagedCache, chunk: Chunk) -> None:
     if chunk.device != cache.device or cache.device.index != torch.cuda.current_device():
-        raise ValueError("the cache, the chunk and the current device must be the same")
+        raise ValueError("the cache, the chunk and the current device must be one and the same")
     if chunk.B > cache.n_seqs:
         raise ValueError(f"{chunk.B} sequences, and {cache.n_seqs} rows of the page table")
 
 
 def _paged_copy(fn, where, cache, chunk, k, v, names, stream):
     _same_place(cache, chunk)
-    kr = _rows(k, names[0], cache, chunk, cache.n_kv_heads, True)
-    vr = _rows(v, names[1], cache, chunk, cache.n_kv_heads, True)
+    kr = _rows(k, names[0], cache, chunk, cache.n_kv_heads, 1)
+    vr = _rows(v, names[1], cache, chunk, cache.n_kv_heads, 1)
     if k.shape != v.shape:
         raise ValueError(f"{names[0]} and {names[1]} must have the same rows")
     _check(fn(cache.ref, chunk.ref(k.shape[1]), ctypes.byref(kr), ctypes.byref(vr), _stream(stream)), where)
@@ -522,8 +536,8 @@ def paged_attention(cache: PagedCache, layer: int, chunk: Chunk, q: torch.Tensor
     q, out: [B, T, n_heads, head_dim] or [rows, n_heads, head_dim] packed, bf16; scale 0: 1 / sqrt(head_dim)."""
     _same_place(cache, chunk)
     heads = q.shape[-2]
-    qr = _rows(q, "q", cache, chunk, heads, False)
-    orr = _rows(out, "out", cache, chunk, heads, False)
+    qr = _rows(q, "q", cache, chunk, heads, 0)
+    orr = _rows(out, "out", cache, chunk, heads, 0)
     if q.shape != out.shape:
         raise ValueError("q and out must have the same rows")
     if ws.device != cache.device:
