@@ -479,6 +479,28 @@ int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_ch
                          size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------------
+ * smol_prefill_paged: T new tokens per sequence through the model over a paged
+ * cache (smol_prefill_with_cache's counterpart).  In every block the new tokens'
+ * post-RoPE keys and values are written to their pages (smol_paged_append) and
+ * the attention reads them there with the earlier ones (smol_paged_attention);
+ * NoPE blocks and windows apply as in the other calls.  T = 1 is a decode step, T
+ * of a few a drafted continuation for smol_verify_drafts.
+ *   ids      device int32 [B, T].
+ *   cache    of cfg's layers, kv heads and head_dim; its pages are written.
+ *   pos      device int32 [B]: tokens of sequence b already in its pages, each in
+ *            [0, min(max_pages * page_size, max_pos) - T] (SMOL_ERR_INPUT in the
+ *            status word otherwise); new token t stands at position pos[b] + t.
+ *   logits   device [B, T, V] bf16.
+ *   ws       >= smol_prefill_paged_workspace_bytes(cfg, cache, B, T) bytes, zeroed
+ *            once.
+ * B up to 4096; T < max_pos and T <= max_pages * page_size (SMOL_ERR_TOO_LONG).
+ * ------------------------------------------------------------------------- */
+size_t smol_prefill_paged_workspace_bytes(const smol_config *cfg, const smol_paged_cache *cache, int B, int T);
+int smol_prefill_paged(const smol_config *cfg, const void *packed, const int32_t *ids, int B, int T,
+                       const smol_paged_cache *cache, const int32_t *pos, void *logits, void *ws,
+                       size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
  * smol_verify_drafts: which of a sequence's drafted tokens stay, and its next
  * token, from the target's logits and the caller's random numbers.
  *   With p_i the target's distribution in row i (the softmax of logits /
@@ -531,7 +553,7 @@ int smol_workspace_status(void *ws, void *stream);
 int smol_last_launch_count(void);
 
 /* For tests of the failure path only (no counterpart on the pages): the limit,
- * in nanoseconds, of the bounded waits of the prefill attention kernel in
+ * in nanoseconds, of the bounded waits of the prefill and paged attention kernels in
  * launches made from now on by any thread (0 restores the default of 1 s).  A
  * limit shorter than the kernel's own latencies makes a wait give up: the
  * kernel drains the copies and MMAs it issued (those drains keep the 1 s

@@ -63,10 +63,11 @@ struct GemmParams {
   float *ssq_out;         // kEpiResidual: atomically accumulates sum(out^2) per row
   float *ssq_zero;        // rows of this buffer are cleared by the n-block-0 tiles
   // kEpiQkvRope
-  f16 *q, *k, *v;         // f16 [B, H, T, hd], [B, KV, T, hd], [B, KV, T, hd]; k, v optional
+  f16 *q, *k, *v;         // f16 [B, H, T, hd], [B, KV, T, hd], [B, KV, T, hd]; each optional
   f16 *v_t;               // optional f16 V transposed: [B, KV, hd, T_pad] (keys contiguous)
   int T_pad;              // row pitch of v_t in elements (T rounded up to a multiple of 8)
   bf16 *k_bf, *v_bf;      // optional bf16 copies of k and v (cache entries), same layout
+  bf16 *q_bf;             // optional bf16 copy of q, same layout
   int T, H, KV, hd;
   const float2 *rope;     // [rope_table_rows(max_pos)][hd/2] (cos, sin), two-level;
                           // nullptr: q and k are not rotated (a NoPE block)

@@ -516,7 +516,7 @@ __device__ __forceinline__ void epi_qkv_rope(const GemmParams &p, EpiCtx &e) {
     const int hsub = is_q ? gh : (is_k ? gh - p.H : gh - p.H - p.KV);
     const long long my_row = (is_q ? q_row : kv_row) + hsub * head_stride;
     f16 *dst = is_q ? p.q : (is_k ? p.k : p.v);
-    bf16 *dst_bf = is_q ? nullptr : (is_k ? p.k_bf : p.v_bf);
+    bf16 *dst_bf = is_q ? p.q_bf : (is_k ? p.k_bf : p.v_bf);
     auto row_off = [&](int rr) { return __shfl_sync(0xffffffffu, my_row, rr) * 2; };
     float y1[32], y2[32];
     int seg1, seg2;                               // element offsets of the two 32-wide segments

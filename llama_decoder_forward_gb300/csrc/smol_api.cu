@@ -102,6 +102,11 @@ WsLayout ws_layout(const smol_config *c, int B, int T, bool chain = false) {
 // below max_pos and the cached rows fit the S_max slots.
 int cache_lmax(const smol_config *c, int T, int S_max) { return min(S_max, c->max_pos - T); }
 
+// Positions accepted by a forward over a paged cache of T new tokens.
+int paged_lmax(const smol_config *c, const smol_paged_cache *p, int T) {
+  return min(p->max_pages * p->page_size, c->max_pos) - T;
+}
+
 // The block workspace plus one layer's left-padded keys/values over Tk = lmax + T.
 WsLayout ws_layout_cache(const smol_config *c, int B, int T, int S_max) {
   WsLayout W = ws_layout(c, B, T);
@@ -212,6 +217,16 @@ struct CacheCtx {
   int S_max, lmax;
 };
 
+// A block over a paged cache: the new keys and values go to the pages, and the
+// attention reads them there.
+struct PagedCtx {
+  const smol_paged_cache *cache;
+  const int32_t *pos;              // [B] device
+  int layer;
+  uint8_t *ws;                     // the paged attention's workspace
+};
+PagedKv paged_kv(const smol_paged_cache *c, int layer);
+
 // Row-block completion flags of the model forward, zeroed before its first
 // kernel: per layer two arrays of row_blocks ints, written by the attention
 // (read by the O projection) and by the down projection (read by the next
@@ -231,7 +246,8 @@ int gemm_arrivals(int N, int bn) { return 8 * static_cast<int>((N + bn - 1) / bn
 
 int run_block(const smol_config *c, const void *packed, int layer, const BlockIO &io, int B, int T,
               const int32_t *valid_start, const uint8_t *key_mask, const WsLayout &W, uint8_t *ws, int sms,
-              cudaStream_t st, const CacheCtx *cc = nullptr, const FlagCtx *fc = nullptr) {
+              cudaStream_t st, const CacheCtx *cc = nullptr, const FlagCtx *fc = nullptr,
+              const PagedCtx *pc = nullptr) {
   const long long M = (long long)B * T;
   const int d = c->hidden, H = c->n_heads, KV = c->n_kv_heads, hd = c->head_dim, I = c->intermediate;
   const LayerPtrs lp = layer_ptrs(c, packed, layer);
@@ -270,6 +286,16 @@ int run_block(const smol_config *c, const void *packed, int layer, const BlockIO
     p.pos_add = cc->cache_len;
     p.pos_limit = cc->lmax;
   }
+  if (pc) {                        // as above; q, k and v in bf16, the pages' and their attention's type
+    p.pos_add = pc->pos;
+    p.pos_limit = paged_lmax(c, pc->cache, T);
+    p.q = nullptr;
+    p.k = nullptr;
+    p.v_t = nullptr;
+    p.q_bf = reinterpret_cast<bf16 *>(q);
+    p.k_bf = reinterpret_cast<bf16 *>(k);
+    p.v_bf = reinterpret_cast<bf16 *>(v);
+  }
   // every kernel of the block is a programmatic dependent of the one before
   // (each waits for it with griddepcontrol.wait before touching its data, or,
   // in the model forward, for the flags of the row blocks it reads)
@@ -294,7 +320,29 @@ int run_block(const smol_config *c, const void *packed, int layer, const BlockIO
   ap.wait_ns = g_attn_wait_ns.load(std::memory_order_relaxed);
   ap.pdl = 1;
   if (attn_flags) ap.done_out = fc->at(layer, 0);
-  if (cc) {
+  if (pc) {
+    const long long th = (long long)T * hd;
+    const PagedChunk chunk{B, T, pc->pos, nullptr, nullptr, 0};
+    LAUNCH(launch_paged_append(paged_kv(pc->cache, layer), 1, chunk, PagedRows{reinterpret_cast<uint8_t *>(k), 0, KV * th, hd, th},
+                               PagedRows{reinterpret_cast<uint8_t *>(v), 0, KV * th, hd, th}, st));
+    PagedAttnParams pa{};
+    pa.kv = paged_kv(pc->cache, layer);
+    pa.c = chunk;
+    pa.q = PagedRows{reinterpret_cast<uint8_t *>(q), 0, H * th, hd, th};
+    pa.o = PagedRows{reinterpret_cast<uint8_t *>(o), 0, (long long)T * H * hd, (long long)H * hd, hd};
+    pa.o_f16 = 1;
+    pa.H = H;
+    pa.G = H / KV;
+    pa.scale_log2 = ap.scale_log2;
+    pa.window = ap.window;
+    pa.wait_ns = ap.wait_ns ? ap.wait_ns : kWaitTimeoutNs;
+    pa.ws = pc->ws;
+    pa.status = status;
+    int n = 0;
+    const cudaError_t e = launch_paged_attention(pa, sms, st, &n);
+    if (e != cudaSuccess) return cuda_fail(e);
+    g_launches += n;
+  } else if (cc) {
     // the cached slice and the new keys as one left-padded sequence of Tk keys;
     // the queries are its last T
     const int Tk = cc->lmax + T;
@@ -812,13 +860,13 @@ int paged_copy(bool append, const smol_paged_cache *cache, const smol_chunk *chu
   g_launches = 0;
   int rc = check_paged(cache);
   if (!rc) rc = check_chunk(chunk);
+  if (!rc && chunk->row_start && chunk->rows == 0) return SMOL_OK;   // no rows: their pointers may be NULL
   if (!rc) rc = check_rows(k, chunk, cache->n_kv_heads, cache->n_layers, cache->head_dim, !append);
   if (!rc) rc = check_rows(v, chunk, cache->n_kv_heads, cache->n_layers, cache->head_dim, !append);
   if (rc) return rc;
   int sms;
   if ((rc = device_sms(&sms))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (chunk->row_start && chunk->rows == 0) return SMOL_OK;
   LAUNCH((append ? launch_paged_append : launch_paged_read)(paged_kv(cache, 0), cache->n_layers, paged_chunk(chunk),
                                                             paged_rows(k), paged_rows(v), st));
   return SMOL_OK;
@@ -859,6 +907,7 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
   if (layer < 0 || layer >= cache->n_layers || n_heads <= 0 || window < 0 || !(scale >= 0.f) || !isfinite(scale) || !ws)
     return SMOL_ERR_INVALID_ARG;
   if (!paged_heads_ok(cache, n_heads) || chunk->B > kPagedMaxSeqs) return SMOL_ERR_UNSUPPORTED_SHAPE;
+  if (chunk->row_start && chunk->rows == 0) return SMOL_OK;   // no rows: their pointers may be NULL
   if (!(rc = check_rows(q, chunk, n_heads, 1, cache->head_dim, true)))
     rc = check_rows(out, chunk, n_heads, 1, cache->head_dim, true);
   if (rc) return rc;
@@ -867,7 +916,6 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
     return SMOL_ERR_WORKSPACE;
   int sms;
   if ((rc = device_sms(&sms))) return rc;
-  if (chunk->row_start && chunk->rows == 0) return SMOL_OK;
   PagedAttnParams p{};
   p.kv = paged_kv(cache, layer);
   p.c = paged_chunk(chunk);
@@ -885,6 +933,69 @@ SMOL_API int smol_paged_attention(const smol_paged_cache *cache, int layer, cons
   const cudaError_t e = launch_paged_attention(p, sms, static_cast<cudaStream_t>(stream), &n);
   g_launches = n;
   return e == cudaSuccess ? SMOL_OK : cuda_fail(e);
+}
+
+namespace {
+// A paged cache that fits the model, for B sequences of T new tokens.
+int check_prefill_paged(const smol_config *cfg, const smol_paged_cache *cache, int B, int T) {
+  int rc = check_cfg(cfg);
+  if (!rc) rc = check_paged(cache);
+  if (rc) return rc;
+  if (B <= 0 || T <= 0 || cfg->vocab <= 0) return SMOL_ERR_INVALID_ARG;
+  if (cache->n_layers != cfg->n_layers || cache->n_kv_heads != cfg->n_kv_heads || cache->head_dim != cfg->head_dim)
+    return SMOL_ERR_INVALID_ARG;
+  if (B > kPagedMaxSeqs || (long long)B * T > 0x7fffffffLL) return SMOL_ERR_UNSUPPORTED_SHAPE;
+  return T >= cfg->max_pos || T > cache->max_pages * cache->page_size ? SMOL_ERR_TOO_LONG : SMOL_OK;
+}
+}  // namespace
+
+SMOL_API size_t smol_prefill_paged_workspace_bytes(const smol_config *cfg, const smol_paged_cache *cache, int B, int T) {
+  if (check_prefill_paged(cfg, cache, B, T) != SMOL_OK) return 0;
+  return ws_layout(cfg, B, T).total + paged_attention_ws_bytes(cfg->head_dim, cfg->n_heads, cfg->n_kv_heads, B, T);
+}
+
+SMOL_API int smol_prefill_paged(const smol_config *cfg, const void *packed, const int32_t *ids, int B, int T,
+                                const smol_paged_cache *cache, const int32_t *pos, void *logits, void *ws,
+                                size_t ws_bytes, void *stream) {
+  g_launches = 0;
+  int rc = check_prefill_paged(cfg, cache, B, T);
+  if (rc) return rc;
+  if (!packed || !ids || !pos || !logits || !ws) return SMOL_ERR_INVALID_ARG;
+  if (!aligned16(packed) || !aligned16(logits) || !aligned16(ws) || (reinterpret_cast<uintptr_t>(ids) & 3u) ||
+      (reinterpret_cast<uintptr_t>(pos) & 3u))
+    return SMOL_ERR_MISALIGNED;
+  const WsLayout W = ws_layout(cfg, B, T);
+  if (ws_bytes < smol_prefill_paged_workspace_bytes(cfg, cache, B, T)) return SMOL_ERR_WORKSPACE;
+  int sms;
+  if ((rc = device_sms(&sms))) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t *wsb = static_cast<uint8_t *>(ws);
+  const long long M = (long long)B * T;
+  const PackLayout L = pack_layout(cfg, cfg->n_layers, 1);
+  const uint8_t *pk = static_cast<const uint8_t *>(packed);
+  f16 *x = reinterpret_cast<f16 *>(wsb + W.x);
+  float *ssq_a = reinterpret_cast<float *>(wsb + W.ssq_a);
+  int *status = reinterpret_cast<int *>(wsb + W.status);
+  LAUNCH_K(SMOL_K_EMBED, st, launch_embed_rows(ids, reinterpret_cast<const bf16 *>(pk + L.embed_off), cfg->vocab, cfg->hidden,
+                                               M, x, nullptr, ssq_a, status, SeqCheck{pos, T, paged_lmax(cfg, cache, T)}, st));
+  BlockIO io{};
+  io.x16 = x;
+  io.resid_f16 = x;
+  io.out16 = x;
+  io.out16_is_f16 = 1;
+  for (int l = 0; l < cfg->n_layers; ++l) {
+    const PagedCtx pc{cache, pos, l, wsb + W.total};
+    if ((rc = run_block(cfg, packed, l, io, B, T, nullptr, nullptr, W, wsb, sms, st, nullptr, nullptr, &pc))) return rc;
+  }
+  GemmParams p{};
+  p.M = (int)M; p.N = cfg->vocab; p.K = cfg->hidden;
+  p.out = logits; p.out_is_f16 = 0; p.ldo = cfg->vocab;
+  p.ssq_in = ssq_a; p.inv_dim = 1.0f / cfg->hidden; p.eps = cfg->rms_eps;
+  p.status = status;
+  p.pdl = 1;
+  LAUNCH_K(SMOL_K_HEAD, st, launch_gemm(kEpiScale, gemm_pick_bn(kEpiScale, cfg->vocab, cfg->head_dim), x,
+                     pk + L.head_off, p, sms, st));
+  return SMOL_OK;
 }
 
 SMOL_API size_t smol_verify_workspace_bytes(int B, int T) {

@@ -104,6 +104,9 @@ _SIGS = {
     "smol_paged_workspace_bytes": (c_size_t, [_PC, c_int, c_int, c_int]),
     "smol_paged_attention": (c_int, [_PC, c_int, _CK, c_int, _RW, _RW, c_float, c_int, c_void_p, c_size_t,
                                      c_void_p]),
+    "smol_prefill_paged_workspace_bytes": (c_size_t, [_CFG, _PC, c_int, c_int]),
+    "smol_prefill_paged": (c_int, [_CFG, c_void_p, c_void_p, c_int, c_int, _PC, c_void_p, c_void_p, c_void_p,
+                                   c_size_t, c_void_p]),
     "smol_verify_workspace_bytes": (c_size_t, [c_int, c_int]),
     "smol_verify_drafts": (c_int, [c_void_p, ctypes.c_longlong, c_void_p, c_void_p, c_void_p, ctypes.c_longlong,
                                    c_int, c_int, c_int, c_float, c_int, c_float, c_int, c_void_p, c_void_p,
@@ -544,6 +547,27 @@ def paged_attention(cache: PagedCache, layer: int, chunk: Chunk, q: torch.Tensor
         raise ValueError("ws must be on the cache's device")
     _check(_lib.smol_paged_attention(cache.ref, layer, chunk.ref(q.shape[0]), heads, ctypes.byref(qr), ctypes.byref(orr), scale,
                                      window, ws.data_ptr(), ws.numel(), _stream(stream)), "smol_paged_attention")
+
+
+def prefill_paged_workspace(cfg: Config, cache: PagedCache, B: int, T: int) -> torch.Tensor:
+    n = _lib.smol_prefill_paged_workspace_bytes(ctypes.byref(cfg), cache.ref, B, T)
+    if n == 0:
+        raise SmolError(ERR_UNSUPPORTED_SHAPE, "smol_prefill_paged_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def prefill_paged(cfg: Config, packed: torch.Tensor, ids: torch.Tensor, cache: PagedCache, pos: torch.Tensor,
+                  logits: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """T new tokens per sequence, ids [B, T], through the model over a paged cache, whose pages receive their keys
+    and values; pos [B] (int32): tokens already there.  logits [B, T, V]."""
+    B, T = ids.shape
+    _dev(ids, torch.int32, "ids")
+    _dev(pos, torch.int32, "pos")
+    _dev(logits, torch.bfloat16, "logits")
+    if pos.shape != (B,) or logits.shape != (B, T, cfg.vocab) or B > cache.n_seqs:
+        raise ValueError("pos must be [B], logits [B, T, V], and the page table have B rows")
+    _check(_lib.smol_prefill_paged(ctypes.byref(cfg), packed.data_ptr(), ids.data_ptr(), B, T, cache.ref, pos.data_ptr(),
+                                   logits.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), "smol_prefill_paged")
 
 
 def alloc_verify_workspace(B: int, T: int, device="cuda") -> torch.Tensor:
