@@ -1000,7 +1000,7 @@ SMOL_API int smol_prefill_paged(const smol_config *cfg, const void *packed, cons
 
 SMOL_API size_t smol_verify_workspace_bytes(int B, int T) {
   if (B <= 0 || T <= 0 || T > 512 || ((long long)T + 1) * B > (1 << 24)) return 0;
-  return 1024 + sizeof(VerifyRow) * (size_t)B * ((size_t)T + 1);
+  return 1024 + (sizeof(VerifyRow) + kVerifyList * sizeof(VerifyToken)) * (size_t)B * ((size_t)T + 1);
 }
 
 SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t *drafts, const int32_t *n_draft,
@@ -1046,7 +1046,8 @@ SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t 
   p.next = next;
   p.p_draft = p_draft;
   p.status = static_cast<int *>(ws);
-  p.rows = reinterpret_cast<VerifyRow *>(static_cast<uint8_t *>(ws) + 1024);
+  p.lists = reinterpret_cast<VerifyToken *>(static_cast<uint8_t *>(ws) + 1024);
+  p.rows = reinterpret_cast<VerifyRow *>(p.lists + (size_t)B * (T + 1) * kVerifyList);
   int n = 0;
   const cudaError_t e = launch_verify(p, static_cast<cudaStream_t>(stream), &n);
   g_launches = n;

@@ -25,8 +25,13 @@
 //           sum, the k-th largest value and the top-p cut are prefix sums over
 //           the histogram.  Where the k largest are all >= 0, the rest is not
 //           looked at.
+//           With top-k up to 512 there is a shorter way: the k-th largest of the
+//           threads' own maxima is a bound below which none of the k largest lies,
+//           and what reaches it, rarely more than twice k tokens, goes to a list in
+//           shared memory on which the filters work token by token.
 //   choice  one cluster of eight CTAs for each sequence: the acceptances, then
-//           the draw over one row, an eighth of the vocabulary for each CTA.
+//           the draw over one row, an eighth of the vocabulary for each CTA (or from
+//           the row's list, one token for each thread of one CTA).
 #include <math.h>
 
 #include "common.cuh"
@@ -40,6 +45,8 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kRowThreads = 1024;
+constexpr int kMaxK = 512;           // the largest top-k of the short way
+constexpr int kCand = 1024;          // tokens of its list (one for each thread)
 constexpr int kBatch = 6;            // 16-byte loads in flight in each thread
 constexpr int kBins = 32768;         // values of one sign
 constexpr int kBinRows = kBins / 32;
@@ -131,6 +138,29 @@ __device__ __forceinline__ u64 scaled_floor(float q, u64 z) {
   const u64 lo = man * z, hi = __umul64hi(man, z);
   if (s >= 64) return s >= 128 ? 0 : hi >> (s - 64);
   return (hi << (64 - s)) | (lo >> s);
+}
+
+// z as a sum of two floats, to 2^-48.
+__device__ __forceinline__ float rest_of(u64 z, float zh) {
+  return __ll2float_rn(static_cast<long long>(z - __float2ull_rn(zh)));
+}
+
+// max(m - q z, 0), the product as a sum of two floats: off by less than a unit where
+// it matters, next to a mass of at most 2^44.
+__device__ __forceinline__ u64 mass_less(u64 m, float q, float zh, float zl) {
+  constexpr float kMagic = 12582912.f;
+  const float ph = __fmul_rn(q, zh), pl = __fmaf_rn(q, zl, __fmaf_rn(q, zh, -ph));
+  if (!(ph > 0.f)) return m;                      // also a NaN
+  if (ph >= 17592186044416.f) return 0;           // 2^44: no mass is larger
+  const float his = __fmaf_rn(ph, 1.1920928955078125e-7f, kMagic);
+  const float los = __fadd_rn(__fadd_rn(__fmaf_rn(__fsub_rn(his, kMagic), -8388608.f, ph), pl), kMagic);
+  const long long have = static_cast<long long>(__float_as_int(his) - 0x4b400000) * 8388608ll + (__float_as_int(los) - 0x4b400000);
+  const long long left = static_cast<long long>(m) - have;
+  return left > 0 ? static_cast<u64>(left) : 0;
+}
+__device__ __forceinline__ u64 mass_less(u64 m, float q, u64 z) {
+  const float zh = __ull2float_rn(z);
+  return mass_less(m, q, zh, rest_of(z, zh));
 }
 
 // ---------------------------------------------------------------- rows in chunks
@@ -245,6 +275,11 @@ struct RowSmem {
   u64 before_mass, z, t_cut;
   unsigned before_count;
   int found, bin, x_cut;
+  // the short way's list
+  u64 cand_mass[kCand];
+  uint32_t cand_key[kCand];
+  int cand_x[kCand];
+  unsigned n_cand, n_out;
 };
 
 __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const VerifyParams p) {
@@ -299,8 +334,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   };
 
   // ---- the largest value, with the histogram of the values >= 0 on the way
+  const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f, brief = !p.greedy && use_k && p.top_k <= kMaxK;
   u64 best = 0;
-  if (p.greedy) {
+  uint32_t my_max = 0;                            // the short way: this thread's largest key
+  if (brief) {
+    uint32_t top2 = 0;
+    for_chunks([&](int, const uint4 &k) { top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(k.x, k.y)), __vmaxu2(k.z, k.w)); }, nothing);
+    my_max = max(top2 & 0xffffu, top2 >> 16);
+    best = argmax_pack(my_max, 0);
+  } else if (p.greedy) {
     for_chunks([&](int c, const uint4 &k) {       // chunks ascend: the first of equal values stays
       const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w)), t = max(t2 & 0xffffu, t2 >> 16);
       if (t > static_cast<uint32_t>(best >> 32)) {
@@ -317,7 +359,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   best = warp_max(best);
   if (lane == 0) S.red[warp] = best;
   for (int k = tid; k < 257; k += kRowThreads) S.table[k] = kPow2.v[k];
-  if (tid == 0) S.x_cut = p.V;
+  if (tid == 0) {
+    S.x_cut = p.V;
+    S.n_cand = S.n_out = 0;
+  }
   __syncthreads();
   best = warp_max(S.red[lane]);
   __syncthreads();
@@ -325,6 +370,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   const float lmax = key_value(kmax);
   const bool fine = lmax > -INFINITY && lmax < INFINITY;              // NaN and infinities: no distribution
   VerifyRow out{};
+  out.listed = -1;
   out.argmax = fine && p.greedy ? argmax_index(best) : -1;
   out.lmax = lmax;
   const int x = i < n ? p.drafts[at] : -1;
@@ -343,187 +389,262 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   // a value below l_max - 32 temperature has mass 0 (45 ln 2 = 31.2); it is not counted
   const uint32_t kmin = bf16_order_key(static_cast<uint16_t>(__float_as_uint(lmax - 32.f * p.temperature) >> 16));
   const uint32_t kcount = kmin > 0 ? kmin - 1 : 0;   // the smallest key counted (one to spare for the truncation)
-  const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f;
 
-  // ---- counts and masses of rows of 32 neighbouring values, the largest first
-  auto sum_rows = [&](int half, uint32_t from) {
-    const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
-    const int r_end = static_cast<int>((0x10000u - from + 31) >> 5);
-    for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
-      unsigned c[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k * (kRowThreads / 32);
-        unsigned cs = 0;
-        u64 ms = 0;
-        if (r < r_end && __any_sync(0xffffffffu, c[k] != 0)) {
-          ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c[k];
-          cs = __reduce_add_sync(0xffffffffu, c[k]);
-#pragma unroll
-          for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
-        }
-        if (lane == 0) {
-          S.row_count[half * kBinRows + r] = cs;
-          S.row_mass[half * kBinRows + r] = ms;
-        }
-      }
-    }
-    __syncthreads();
-  };
-  int resident = 0;
-  sum_rows(0, 0x8000u);
-  // the negative values: not where none of them counts, nor where the k largest are all >= 0
-  bool negative = kcount <= 0x7fffu;
-  if (use_k && negative) {
-    unsigned c = __reduce_add_sync(0xffffffffu, S.row_count[tid]);
-    if (lane == 0) S.red[warp] = c;
-    __syncthreads();
-    c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(S.red[lane]));
-    negative = c < static_cast<unsigned>(p.top_k);
-    __syncthreads();
-  }
-  if (negative) {
-    resident = 1;
-    count(1, kcount + 0x8000u);
-    __syncthreads();
-    sum_rows(1, kcount + 0x8000u);
-  } else {
-    S.row_count[kBinRows + tid] = 0;
-    S.row_mass[kBinRows + tid] = 0;
-  }
-  __syncthreads();
-  // prefix sums over the 2048 rows of values, two for each thread
-  u64 total_c, total_m;
-  const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
-  const u64 m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
-  const u64 pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
-  const u64 pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
-
-  // the counters of one row of 32 values, into S.bins
-  auto fetch_bins = [&](int r) {
-    const bool here = r / kBinRows == resident;
-    if (tid < 32) S.bins[tid] = here ? S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)] : 0u;
-    __syncthreads();
-    if (here) return;
-    const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
-    for_chunks([&](int, const uint4 &k) {
+  uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
+  int xcut = p.V;
+  u64 z = 0;
+  bool done = false;
+  if (brief) {
+    // the largest bound that k of the maxima reach, bit by bit; then what reaches it
+    auto bound_of = [&](auto &&reach) {
+      uint32_t t = 0;
+#pragma unroll 1
+      for (uint32_t bit = 0x8000u; bit; bit >>= 1)
+        if (reach(t | bit) >= p.top_k) t |= bit;
+      return t;
+    };
+    const uint32_t least = bound_of([&](uint32_t t) { return __syncthreads_count(my_max >= t); });
+    for_chunks([&](int c, const uint4 &k) {
+      const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w));
+      if (max(t2 & 0xffffu, t2 >> 16) < least) return;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t d = top - chunk_half(k, e);
-        if (d < 32u) atomicAdd(&S.bins[d], 1u);
+        const int x = row.base + 8 * c + e;
+        if (chunk_half(k, e) < least || x < 0 || x >= p.V) continue;
+        const unsigned at = atomicAdd(&S.n_cand, 1u);
+        if (at < kCand) {
+          S.cand_key[at] = chunk_half(k, e);
+          S.cand_x[at] = x;
+        }
       }
     }, nothing);
     __syncthreads();
-  };
-  auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
-
-  // ---- top-k: the k-th largest value; where fewer than k have a mass, all stay
-  uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
-  int xcut = p.V;
-  u64 z = total_m;
-  const u64 k_th = static_cast<u64>(max(p.top_k, 0));
-  if (use_k && total_c >= k_th) {
-    if (pc < k_th && k_th <= pc + c0 + c1) {
-      const bool second = k_th > pc + c0;
-      S.found = 2 * tid + second;
-      S.before_count = static_cast<unsigned>(pc + (second ? c0 : 0));
-      S.before_mass = pm + (second ? m0 : 0);
-    }
-    __syncthreads();
-    const int r = S.found;
-    fetch_bins(r);
-    if (warp == 0) {
-      const unsigned c = S.bins[lane];
-      unsigned ci = c;
-      const u64 m = c ? mass_of(mc, key_value(key_of(r, lane))) * c : 0;
-      u64 mi = m;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned tc = __shfl_up_sync(0xffffffffu, ci, o);
-        const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
-        if (lane >= o) {
-          ci += tc;
-          mi += tm;
+    const int n = static_cast<int>(S.n_cand);
+    done = n >= p.top_k && n <= kCand;            // else: fewer maxima than k, or many equal values
+    if (done) {
+      const bool mine = tid < n;
+      const uint32_t key = mine ? S.cand_key[tid] : 0;
+      const int mx = mine ? S.cand_x[tid] : 0;
+      vcut = bound_of([&](uint32_t t) { return __syncthreads_count(mine && key >= t); });   // the k-th largest
+      const u64 mass = mine && key >= vcut ? mass_of(mc, key_value(key)) : 0;
+      if (mine) S.cand_mass[tid] = mass;
+      block_scan<kRowThreads>(mass, S.red, &z);
+      bool stays = mass != 0;
+      if (use_p) {
+        // a token stays while what comes before it in descending order (equal values
+        // in index order) does not exceed top_p of the whole
+        if (tid == 0) S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
+        __syncthreads();
+        if (stays) {
+          u64 before = 0;
+          for (int i = 0; i < n; ++i) {
+            const uint32_t k = S.cand_key[i];
+            if (k > key || (k == key && S.cand_x[i] < mx)) before += S.cand_mass[i];
+          }
+          stays = before <= S.t_cut;
         }
+        if (tid == 0) S.found = 0x10000;
+        __syncthreads();
+        block_scan<kRowThreads>(stays ? mass : 0, S.red, &z);
+        if (stays) atomicMin(&S.found, static_cast<int>(key));
+        if (tid == 0) S.x_cut = -1;
+        __syncthreads();
+        vcut = static_cast<uint32_t>(S.found);
+        if (stays && key == vcut) atomicMax(&S.x_cut, mx);
+        __syncthreads();
+        xcut = S.x_cut;
       }
-      const int bin = __ffs(__ballot_sync(0xffffffffu, S.before_count + ci >= k_th)) - 1;
-      if (lane == bin) {
-        S.bin = bin;
-        S.z = S.before_mass + mi;
+      VerifyToken *list = p.lists + static_cast<long long>(blockIdx.x) * kVerifyList;
+      if (stays) {
+        const unsigned at = atomicAdd(&S.n_out, 1u);
+        if (at < kVerifyList) list[at] = VerifyToken{mass, mx, 0};
       }
+      __syncthreads();
+      if (S.n_out <= kVerifyList) out.listed = static_cast<int>(S.n_out);
+    } else {
+      count(0, 0x8000u);                          // the long way after all
+      __syncthreads();
     }
-    __syncthreads();
-    vcut = key_of(r, S.bin);
-    z = S.z;
-    __syncthreads();
   }
-  // ---- top-p: the value at which the running mass first exceeds top_p of the whole
-  if (use_p) {
-    if (tid == 0) {
-      S.found = -1;
-      S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
-    }
-    __syncthreads();
-    const u64 goal = S.t_cut;                     // a whole sum exceeds top_p z iff it exceeds its floor
-    auto over = [&](u64 v) { return v > goal; };
-    if (!over(pm) && over(pm + m0 + m1)) {
-      const bool second = !over(pm + m0);
-      S.found = 2 * tid + second;
-      S.before_mass = pm + (second ? m0 : 0);
-    }
-    __syncthreads();
-    const int r = S.found;                        // found: z > goal
-    if (r >= 0) {
-      fetch_bins(r);
-      if (warp == 0) {
-        const unsigned c = S.bins[lane];
-        const u64 one = c ? mass_of(mc, key_value(key_of(r, lane))) : 0, m = one * c;
-        u64 mi = m;
+  if (!done) {
+    // ---- counts and masses of rows of 32 neighbouring values, the largest first
+    auto sum_rows = [&](int half, uint32_t from) {
+      const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
+      const int r_end = static_cast<int>((0x10000u - from + 31) >> 5);
+      for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
+        unsigned c[8];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
-          if (lane >= o) mi += tm;
-        }
-        const int bin = __ffs(__ballot_sync(0xffffffffu, over(S.before_mass + mi))) - 1;
-        if (lane == bin) {
-          // equal values have equal masses: the first t + 1 of them in index order stay
-          const u64 above = S.before_mass + mi - m;
-          const u64 tc = min((goal - above) / one, static_cast<u64>(c - 1));
-          S.bin = bin;
-          S.t_cut = tc + 1 < c ? tc : ~0ull;      // ~0: all of them
-          S.z = above + (tc + 1) * one;
+        for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = r0 + k * (kRowThreads / 32);
+          unsigned cs = 0;
+          u64 ms = 0;
+          if (r < r_end && __any_sync(0xffffffffu, c[k] != 0)) {
+            ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c[k];
+            cs = __reduce_add_sync(0xffffffffu, c[k]);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
+          }
+          if (lane == 0) {
+            S.row_count[half * kBinRows + r] = cs;
+            S.row_mass[half * kBinRows + r] = ms;
+          }
         }
       }
       __syncthreads();
-      const uint32_t v = key_of(r, S.bin);
-      const u64 tc = S.t_cut;
-      z = S.z;
-      vcut = v;
-      if (tc != ~0ull) {
-        // the index of the (t + 1)-th token of this value: counts in vocabulary
-        // order, a round of 1024 chunks at a time
-        u64 seen = 0;
-        for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
-          const int c = c_first + tid;
-          uint4 k = make_uint4(0, 0, 0, 0);       // key 0 is a NaN, never the cut
-          if (c < row.chunks) k = chunk_keys(load_chunk(row, c));
-          unsigned mine = 0;
+    };
+    int resident = 0;
+    sum_rows(0, 0x8000u);
+    // the negative values: not where none of them counts, nor where the k largest are all >= 0
+    bool negative = kcount <= 0x7fffu;
+    if (use_k && negative) {
+      unsigned c = __reduce_add_sync(0xffffffffu, S.row_count[tid]);
+      if (lane == 0) S.red[warp] = c;
+      __syncthreads();
+      c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(S.red[lane]));
+      negative = c < static_cast<unsigned>(p.top_k);
+      __syncthreads();
+    }
+    if (negative) {
+      resident = 1;
+      count(1, kcount + 0x8000u);
+      __syncthreads();
+      sum_rows(1, kcount + 0x8000u);
+    } else {
+      S.row_count[kBinRows + tid] = 0;
+      S.row_mass[kBinRows + tid] = 0;
+    }
+    __syncthreads();
+    // prefix sums over the 2048 rows of values, two for each thread
+    u64 total_c, total_m;
+    const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
+    const u64 m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
+    const u64 pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
+    const u64 pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
+
+    // the counters of one row of 32 values, into S.bins
+    auto fetch_bins = [&](int r) {
+      const bool here = r / kBinRows == resident;
+      if (tid < 32) S.bins[tid] = here ? S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)] : 0u;
+      __syncthreads();
+      if (here) return;
+      const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
+      for_chunks([&](int, const uint4 &k) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) mine += chunk_half(k, e) == v;
-          u64 all;
-          u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
-          if (rank <= tc && tc < rank + mine) {
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t d = top - chunk_half(k, e);
+          if (d < 32u) atomicAdd(&S.bins[d], 1u);
+        }
+      }, nothing);
+      __syncthreads();
+    };
+    auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
+
+    // ---- top-k: the k-th largest value; where fewer than k have a mass, all stay
+    z = total_m;
+    const u64 k_th = static_cast<u64>(max(p.top_k, 0));
+    if (use_k && total_c >= k_th) {
+      if (pc < k_th && k_th <= pc + c0 + c1) {
+        const bool second = k_th > pc + c0;
+        S.found = 2 * tid + second;
+        S.before_count = static_cast<unsigned>(pc + (second ? c0 : 0));
+        S.before_mass = pm + (second ? m0 : 0);
+      }
+      __syncthreads();
+      const int r = S.found;
+      fetch_bins(r);
+      if (warp == 0) {
+        const unsigned c = S.bins[lane];
+        unsigned ci = c;
+        const u64 m = c ? mass_of(mc, key_value(key_of(r, lane))) * c : 0;
+        u64 mi = m;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (chunk_half(k, e) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned tc = __shfl_up_sync(0xffffffffu, ci, o);
+          const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
+          if (lane >= o) {
+            ci += tc;
+            mi += tm;
           }
-          seen += all;
-          if (seen > tc) break;                   // the same for every thread
+        }
+        const int bin = __ffs(__ballot_sync(0xffffffffu, S.before_count + ci >= k_th)) - 1;
+        if (lane == bin) {
+          S.bin = bin;
+          S.z = S.before_mass + mi;
+        }
+      }
+      __syncthreads();
+      vcut = key_of(r, S.bin);
+      z = S.z;
+      __syncthreads();
+    }
+    // ---- top-p: the value at which the running mass first exceeds top_p of the whole
+    if (use_p) {
+      if (tid == 0) {
+        S.found = -1;
+        S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
+      }
+      __syncthreads();
+      const u64 goal = S.t_cut;                     // a whole sum exceeds top_p z iff it exceeds its floor
+      auto over = [&](u64 v) { return v > goal; };
+      if (!over(pm) && over(pm + m0 + m1)) {
+        const bool second = !over(pm + m0);
+        S.found = 2 * tid + second;
+        S.before_mass = pm + (second ? m0 : 0);
+      }
+      __syncthreads();
+      const int r = S.found;                        // found: z > goal
+      if (r >= 0) {
+        fetch_bins(r);
+        if (warp == 0) {
+          const unsigned c = S.bins[lane];
+          const u64 one = c ? mass_of(mc, key_value(key_of(r, lane))) : 0, m = one * c;
+          u64 mi = m;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
+            if (lane >= o) mi += tm;
+          }
+          const int bin = __ffs(__ballot_sync(0xffffffffu, over(S.before_mass + mi))) - 1;
+          if (lane == bin) {
+            // equal values have equal masses: the first t + 1 of them in index order stay
+            const u64 above = S.before_mass + mi - m;
+            const u64 tc = min((goal - above) / one, static_cast<u64>(c - 1));
+            S.bin = bin;
+            S.t_cut = tc + 1 < c ? tc : ~0ull;      // ~0: all of them
+            S.z = above + (tc + 1) * one;
+          }
         }
         __syncthreads();
-        xcut = S.x_cut;
+        const uint32_t v = key_of(r, S.bin);
+        const u64 tc = S.t_cut;
+        z = S.z;
+        vcut = v;
+        if (tc != ~0ull) {
+          // the index of the (t + 1)-th token of this value: counts in vocabulary
+          // order, a round of 1024 chunks at a time
+          u64 seen = 0;
+          for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
+            const int c = c_first + tid;
+            uint4 k = make_uint4(0, 0, 0, 0);       // key 0 is a NaN, never the cut
+            if (c < row.chunks) k = chunk_keys(load_chunk(row, c));
+            unsigned mine = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mine += chunk_half(k, e) == v;
+            u64 all;
+            u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
+            if (rank <= tc && tc < rank + mine) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (chunk_half(k, e) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
+            }
+            seen += all;
+            if (seen > tc) break;                   // the same for every thread
+          }
+          __syncthreads();
+          xcut = S.x_cut;
+        }
       }
     }
   }
@@ -582,6 +703,40 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
     if (rank == 0 && tid == 0) p.next[b] = r.argmax;
     return;
   }
+  if (r.listed >= 0) {
+    // ---- the draw from a row's list, in its order of vocabulary: one CTA, a token for each thread
+    if (rank != 0) return;
+    __shared__ u64 l_mass[kVerifyList];
+    __shared__ int l_x[kVerifyList];
+    const bool here = tid < r.listed, given = kept < n;
+    const long long of = static_cast<long long>(b) * p.T + kept;
+    u64 mass = 0, w = 0;
+    int x = 0;
+    if (here) {
+      const VerifyToken t = p.lists[(static_cast<long long>(b) * (p.T + 1) + kept) * kVerifyList + tid];
+      x = t.x;
+      mass = w = t.mass;
+      if (given) w = p.probs ? mass_less(mass, p.probs[of * p.ldq + x], r.z) : x == p.drafts[of] ? 0 : mass;
+    }
+    u64 whole;
+    block_scan<kChoiceThreads>(w, red, &whole);
+    if (whole == 0) {                             // nothing is left of p - q: draw from p
+      w = mass;
+      block_scan<kChoiceThreads>(w, red, &whole);
+    }
+    if (here) {
+      l_mass[tid] = w;
+      l_x[tid] = x;
+    }
+    __syncthreads();
+    const u64 goal = min(scaled_floor(p.uniform[static_cast<long long>(b) * (p.T + 1) + p.T], whole), whole - 1);
+    if (here && w) {
+      u64 before = 0;
+      for (int i = 0; i < r.listed; ++i) before += l_x[i] < x ? l_mass[i] : 0;
+      if (before <= goal && goal < before + w) p.next[b] = x;
+    }
+    return;
+  }
   // ---- the draw
   const Row row = make_row(p.logits + (static_cast<long long>(b) * (p.T + 1) + kept) * p.ld, p.V);
   const MassCtx mc = MassCtx{r.lmax, p.c_hi, p.c_lo, table};
@@ -593,21 +748,7 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   const int per = (row.chunks + kChoiceCtas * kChoiceThreads - 1) / (kChoiceCtas * kChoiceThreads);
   const int first = min(row.chunks, (static_cast<int>(rank) * kChoiceThreads + tid) * per), last = min(row.chunks, first + per);
   bool rest = refused;                            // weights max(p - q, 0), else p
-  // max(m - q z, 0), the product as a sum of two floats (z = zh + zl to 2^-48, so it
-  // is off by less than a unit where it matters, next to a mass of at most 2^44)
-  const float zh = __ull2float_rn(r.z);
-  const float zl = __ll2float_rn(static_cast<long long>(r.z - __float2ull_rn(zh)));
-  auto less = [&](u64 m, float qx) -> u64 {
-    constexpr float kMagic = 12582912.f;
-    const float ph = __fmul_rn(qx, zh), pl = __fmaf_rn(qx, zl, __fmaf_rn(qx, zh, -ph));
-    if (!(ph > 0.f)) return m;                    // also a NaN
-    if (ph >= 17592186044416.f) return 0;         // 2^44: no mass is larger
-    const float his = __fmaf_rn(ph, 1.1920928955078125e-7f, kMagic);
-    const float los = __fadd_rn(__fadd_rn(__fmaf_rn(__fsub_rn(his, kMagic), -8388608.f, ph), pl), kMagic);
-    const long long have = static_cast<long long>(__float_as_int(his) - 0x4b400000) * 8388608ll + (__float_as_int(los) - 0x4b400000);
-    const long long left = static_cast<long long>(m) - have;
-    return left > 0 ? static_cast<u64>(left) : 0;
-  };
+  const float zh = __ull2float_rn(r.z), zl = rest_of(r.z, zh);
   const uint32_t vcut2 = r.vcut | (r.vcut << 16);
   auto weights = [&](int c, u64 (&w)[8]) -> u64 {
     const uint4 keys = chunk_keys(load_chunk(row, c));
@@ -631,7 +772,7 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
       const uint32_t key = chunk_half(keys, e);
       u64 m = mass_of(mc, key_value(key));        // 0 outside the row: -infinity
       if (key < r.vcut || (key == r.vcut && x > r.xcut)) m = 0;
-      if (rest) m = q ? less(m, qv[e]) : x == gone ? 0 : m;
+      if (rest) m = q ? mass_less(m, qv[e], zh, zl) : x == gone ? 0 : m;
       w[e] = m;
       sum += m;
     }

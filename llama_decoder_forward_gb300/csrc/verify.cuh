@@ -5,6 +5,13 @@
 
 namespace smol {
 
+// A token that stays, and its mass.
+struct VerifyToken {
+  unsigned long long mass;
+  int x, pad;
+};
+constexpr int kVerifyList = 256;   // tokens of a row's list
+
 // What the choice needs of one target row.
 struct VerifyRow {
   unsigned long long z;        // mass of the tokens that stay (0: no distribution)
@@ -13,6 +20,8 @@ struct VerifyRow {
   unsigned vcut;               // order key: values above stay, and of this one
   int xcut;                    //   the tokens with index <= xcut
   int argmax;
+  int listed;                  // tokens that stay, all in the row's list; -1: no list
+  int pad[3];
 };
 
 struct VerifyParams {
@@ -30,6 +39,7 @@ struct VerifyParams {
   int *n_accepted, *next;      // [B]
   float *p_draft;              // [B, T] or nullptr
   VerifyRow *rows;             // [B, T + 1], workspace
+  VerifyToken *lists;          // [B, T + 1][kVerifyList], workspace
   int *status;
 };
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st, int *launches);

@@ -130,6 +130,19 @@ def test_flat_and_tied_rows(S):
             check(S, logits, drafts, u, None, **kw)
 
 
+@pytest.mark.parametrize("top_k", [1, 2, 7, 255, 256, 257, 511, 512, 513, 900])
+@pytest.mark.parametrize("V", [600, 5003, 49152])
+def test_filters_on_both_ways(S, V, top_k):
+    """top-k around the sizes at which the row's work changes, few and many equal values among them."""
+    B, T = 4, 2
+    logits, drafts, u, probs = case(B, T, V, seed=V + top_k, spread=1.0)
+    coarse = (logits.float() * 4).round().div(4).to(torch.bfloat16)       # many ties
+    for lg in (logits, coarse, -logits.abs()):
+        for kw in (dict(), dict(top_p=0.9), dict(top_p=0.3333, temperature=2.0)):
+            check(S, lg, drafts, u, probs, top_k=top_k, **kw)
+            check(S, lg, drafts, u, None, top_k=top_k, **kw)
+
+
 def test_zeros_of_both_signs_are_equal(S):
     B, T, V = 12, 2, 3000
     g = torch.Generator("cuda").manual_seed(21)
