@@ -25,10 +25,12 @@
 //           sum, the k-th largest value and the top-p cut are prefix sums over
 //           the histogram.  Where the k largest are all >= 0, the rest is not
 //           looked at.
-//           With top-k up to 512 there is a shorter way: the k-th largest of the
-//           threads' own maxima is a bound below which none of the k largest lies,
-//           and what reaches it, rarely more than twice k tokens, goes to a list in
-//           shared memory on which the filters work token by token.
+//           With top-k up to 256 another kernel does this without a histogram, two
+//           CTAs on an SM: the k-th largest of the threads' own maxima is a bound
+//           below which none of the k largest lies, and what reaches it, a little
+//           more than k tokens, goes to a list in shared memory on which the filters
+//           work token by token (64 sequences of up to 5 drafts, V = 49152, top-k 50:
+//           the whole call takes 26 us, with the histogram 54).
 //   choice  one cluster of eight CTAs for each sequence: the acceptances, then
 //           the draw over one row, an eighth of the vocabulary for each CTA (or from
 //           the row's list, one token for each thread of one CTA).
@@ -45,8 +47,8 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kRowThreads = 1024;
-constexpr int kMaxK = 512;           // the largest top-k of the short way
-constexpr int kCand = 1024;          // tokens of its list (one for each thread)
+constexpr int kTopThreads = 512;     // of the kernel for a small top-k, and the tokens of its list
+constexpr int kTopMaxK = 256;        // the largest top-k it takes
 constexpr int kBatch = 6;            // 16-byte loads in flight in each thread
 constexpr int kBins = 32768;         // values of one sign
 constexpr int kBinRows = kBins / 32;
@@ -275,11 +277,6 @@ struct RowSmem {
   u64 before_mass, z, t_cut;
   unsigned before_count;
   int found, bin, x_cut;
-  // the short way's list
-  u64 cand_mass[kCand];
-  uint32_t cand_key[kCand];
-  int cand_x[kCand];
-  unsigned n_cand, n_out;
 };
 
 __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const VerifyParams p) {
@@ -334,15 +331,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   };
 
   // ---- the largest value, with the histogram of the values >= 0 on the way
-  const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f, brief = !p.greedy && use_k && p.top_k <= kMaxK;
+  const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f;
   u64 best = 0;
-  uint32_t my_max = 0;                            // the short way: this thread's largest key
-  if (brief) {
-    uint32_t top2 = 0;
-    for_chunks([&](int, const uint4 &k) { top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(k.x, k.y)), __vmaxu2(k.z, k.w)); }, nothing);
-    my_max = max(top2 & 0xffffu, top2 >> 16);
-    best = argmax_pack(my_max, 0);
-  } else if (p.greedy) {
+  if (p.greedy) {
     for_chunks([&](int c, const uint4 &k) {       // chunks ascend: the first of equal values stays
       const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w)), t = max(t2 & 0xffffu, t2 >> 16);
       if (t > static_cast<uint32_t>(best >> 32)) {
@@ -359,10 +350,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   best = warp_max(best);
   if (lane == 0) S.red[warp] = best;
   for (int k = tid; k < 257; k += kRowThreads) S.table[k] = kPow2.v[k];
-  if (tid == 0) {
-    S.x_cut = p.V;
-    S.n_cand = S.n_out = 0;
-  }
+  if (tid == 0) S.x_cut = p.V;
   __syncthreads();
   best = warp_max(S.red[lane]);
   __syncthreads();
@@ -390,261 +378,185 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   const uint32_t kmin = bf16_order_key(static_cast<uint16_t>(__float_as_uint(lmax - 32.f * p.temperature) >> 16));
   const uint32_t kcount = kmin > 0 ? kmin - 1 : 0;   // the smallest key counted (one to spare for the truncation)
 
-  uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
-  int xcut = p.V;
-  u64 z = 0;
-  bool done = false;
-  if (brief) {
-    // the largest bound that k of the maxima reach, bit by bit; then what reaches it
-    auto bound_of = [&](auto &&reach) {
-      uint32_t t = 0;
-#pragma unroll 1
-      for (uint32_t bit = 0x8000u; bit; bit >>= 1)
-        if (reach(t | bit) >= p.top_k) t |= bit;
-      return t;
-    };
-    const uint32_t least = bound_of([&](uint32_t t) { return __syncthreads_count(my_max >= t); });
-    for_chunks([&](int c, const uint4 &k) {
-      const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w));
-      if (max(t2 & 0xffffu, t2 >> 16) < least) return;
+  // ---- counts and masses of rows of 32 neighbouring values, the largest first
+  auto sum_rows = [&](int half, uint32_t from) {
+    const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
+    const int r_end = static_cast<int>((0x10000u - from + 31) >> 5);
+    for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
+      unsigned c[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int r = r0 + k * (kRowThreads / 32);
+        unsigned cs = 0;
+        u64 ms = 0;
+        if (r < r_end && __any_sync(0xffffffffu, c[k] != 0)) {
+          ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c[k];
+          cs = __reduce_add_sync(0xffffffffu, c[k]);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
+        }
+        if (lane == 0) {
+          S.row_count[half * kBinRows + r] = cs;
+          S.row_mass[half * kBinRows + r] = ms;
+        }
+      }
+    }
+    __syncthreads();
+  };
+  int resident = 0;
+  sum_rows(0, 0x8000u);
+  // the negative values: not where none of them counts, nor where the k largest are all >= 0
+  bool negative = kcount <= 0x7fffu;
+  if (use_k && negative) {
+    unsigned c = __reduce_add_sync(0xffffffffu, S.row_count[tid]);
+    if (lane == 0) S.red[warp] = c;
+    __syncthreads();
+    c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(S.red[lane]));
+    negative = c < static_cast<unsigned>(p.top_k);
+    __syncthreads();
+  }
+  if (negative) {
+    resident = 1;
+    count(1, kcount + 0x8000u);
+    __syncthreads();
+    sum_rows(1, kcount + 0x8000u);
+  } else {
+    S.row_count[kBinRows + tid] = 0;
+    S.row_mass[kBinRows + tid] = 0;
+  }
+  __syncthreads();
+  // prefix sums over the 2048 rows of values, two for each thread
+  u64 total_c, total_m;
+  const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
+  const u64 m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
+  const u64 pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
+  const u64 pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
+
+  // the counters of one row of 32 values, into S.bins
+  auto fetch_bins = [&](int r) {
+    const bool here = r / kBinRows == resident;
+    if (tid < 32) S.bins[tid] = here ? S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)] : 0u;
+    __syncthreads();
+    if (here) return;
+    const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
+    for_chunks([&](int, const uint4 &k) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int x = row.base + 8 * c + e;
-        if (chunk_half(k, e) < least || x < 0 || x >= p.V) continue;
-        const unsigned at = atomicAdd(&S.n_cand, 1u);
-        if (at < kCand) {
-          S.cand_key[at] = chunk_half(k, e);
-          S.cand_x[at] = x;
-        }
+        const uint32_t d = top - chunk_half(k, e);
+        if (d < 32u) atomicAdd(&S.bins[d], 1u);
       }
     }, nothing);
     __syncthreads();
-    const int n = static_cast<int>(S.n_cand);
-    done = n >= p.top_k && n <= kCand;            // else: fewer maxima than k, or many equal values
-    if (done) {
-      const bool mine = tid < n;
-      const uint32_t key = mine ? S.cand_key[tid] : 0;
-      const int mx = mine ? S.cand_x[tid] : 0;
-      vcut = bound_of([&](uint32_t t) { return __syncthreads_count(mine && key >= t); });   // the k-th largest
-      const u64 mass = mine && key >= vcut ? mass_of(mc, key_value(key)) : 0;
-      if (mine) S.cand_mass[tid] = mass;
-      block_scan<kRowThreads>(mass, S.red, &z);
-      bool stays = mass != 0;
-      if (use_p) {
-        // a token stays while what comes before it in descending order (equal values
-        // in index order) does not exceed top_p of the whole
-        if (tid == 0) S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
-        __syncthreads();
-        if (stays) {
-          u64 before = 0;
-          for (int i = 0; i < n; ++i) {
-            const uint32_t k = S.cand_key[i];
-            if (k > key || (k == key && S.cand_x[i] < mx)) before += S.cand_mass[i];
-          }
-          stays = before <= S.t_cut;
-        }
-        if (tid == 0) S.found = 0x10000;
-        __syncthreads();
-        block_scan<kRowThreads>(stays ? mass : 0, S.red, &z);
-        if (stays) atomicMin(&S.found, static_cast<int>(key));
-        if (tid == 0) S.x_cut = -1;
-        __syncthreads();
-        vcut = static_cast<uint32_t>(S.found);
-        if (stays && key == vcut) atomicMax(&S.x_cut, mx);
-        __syncthreads();
-        xcut = S.x_cut;
-      }
-      VerifyToken *list = p.lists + static_cast<long long>(blockIdx.x) * kVerifyList;
-      if (stays) {
-        const unsigned at = atomicAdd(&S.n_out, 1u);
-        if (at < kVerifyList) list[at] = VerifyToken{mass, mx, 0};
-      }
-      __syncthreads();
-      if (S.n_out <= kVerifyList) out.listed = static_cast<int>(S.n_out);
-    } else {
-      count(0, 0x8000u);                          // the long way after all
-      __syncthreads();
-    }
-  }
-  if (!done) {
-    // ---- counts and masses of rows of 32 neighbouring values, the largest first
-    auto sum_rows = [&](int half, uint32_t from) {
-      const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
-      const int r_end = static_cast<int>((0x10000u - from + 31) >> 5);
-      for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
-        unsigned c[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = r0 + k * (kRowThreads / 32);
-          unsigned cs = 0;
-          u64 ms = 0;
-          if (r < r_end && __any_sync(0xffffffffu, c[k] != 0)) {
-            ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c[k];
-            cs = __reduce_add_sync(0xffffffffu, c[k]);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
-          }
-          if (lane == 0) {
-            S.row_count[half * kBinRows + r] = cs;
-            S.row_mass[half * kBinRows + r] = ms;
-          }
-        }
-      }
-      __syncthreads();
-    };
-    int resident = 0;
-    sum_rows(0, 0x8000u);
-    // the negative values: not where none of them counts, nor where the k largest are all >= 0
-    bool negative = kcount <= 0x7fffu;
-    if (use_k && negative) {
-      unsigned c = __reduce_add_sync(0xffffffffu, S.row_count[tid]);
-      if (lane == 0) S.red[warp] = c;
-      __syncthreads();
-      c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(S.red[lane]));
-      negative = c < static_cast<unsigned>(p.top_k);
-      __syncthreads();
-    }
-    if (negative) {
-      resident = 1;
-      count(1, kcount + 0x8000u);
-      __syncthreads();
-      sum_rows(1, kcount + 0x8000u);
-    } else {
-      S.row_count[kBinRows + tid] = 0;
-      S.row_mass[kBinRows + tid] = 0;
+  };
+  auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
+
+  // ---- top-k: the k-th largest value; where fewer than k have a mass, all stay
+  uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
+  int xcut = p.V;
+  u64 z = total_m;
+  const u64 k_th = static_cast<u64>(max(p.top_k, 0));
+  if (use_k && total_c >= k_th) {
+    if (pc < k_th && k_th <= pc + c0 + c1) {
+      const bool second = k_th > pc + c0;
+      S.found = 2 * tid + second;
+      S.before_count = static_cast<unsigned>(pc + (second ? c0 : 0));
+      S.before_mass = pm + (second ? m0 : 0);
     }
     __syncthreads();
-    // prefix sums over the 2048 rows of values, two for each thread
-    u64 total_c, total_m;
-    const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
-    const u64 m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
-    const u64 pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
-    const u64 pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
-
-    // the counters of one row of 32 values, into S.bins
-    auto fetch_bins = [&](int r) {
-      const bool here = r / kBinRows == resident;
-      if (tid < 32) S.bins[tid] = here ? S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)] : 0u;
-      __syncthreads();
-      if (here) return;
-      const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
-      for_chunks([&](int, const uint4 &k) {
+    const int r = S.found;
+    fetch_bins(r);
+    if (warp == 0) {
+      const unsigned c = S.bins[lane];
+      unsigned ci = c;
+      const u64 m = c ? mass_of(mc, key_value(key_of(r, lane))) * c : 0;
+      u64 mi = m;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t d = top - chunk_half(k, e);
-          if (d < 32u) atomicAdd(&S.bins[d], 1u);
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned tc = __shfl_up_sync(0xffffffffu, ci, o);
+        const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
+        if (lane >= o) {
+          ci += tc;
+          mi += tm;
         }
-      }, nothing);
-      __syncthreads();
-    };
-    auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
-
-    // ---- top-k: the k-th largest value; where fewer than k have a mass, all stay
-    z = total_m;
-    const u64 k_th = static_cast<u64>(max(p.top_k, 0));
-    if (use_k && total_c >= k_th) {
-      if (pc < k_th && k_th <= pc + c0 + c1) {
-        const bool second = k_th > pc + c0;
-        S.found = 2 * tid + second;
-        S.before_count = static_cast<unsigned>(pc + (second ? c0 : 0));
-        S.before_mass = pm + (second ? m0 : 0);
       }
-      __syncthreads();
-      const int r = S.found;
+      const int bin = __ffs(__ballot_sync(0xffffffffu, S.before_count + ci >= k_th)) - 1;
+      if (lane == bin) {
+        S.bin = bin;
+        S.z = S.before_mass + mi;
+      }
+    }
+    __syncthreads();
+    vcut = key_of(r, S.bin);
+    z = S.z;
+    __syncthreads();
+  }
+  // ---- top-p: the value at which the running mass first exceeds top_p of the whole
+  if (use_p) {
+    if (tid == 0) {
+      S.found = -1;
+      S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
+    }
+    __syncthreads();
+    const u64 goal = S.t_cut;                     // a whole sum exceeds top_p z iff it exceeds its floor
+    auto over = [&](u64 v) { return v > goal; };
+    if (!over(pm) && over(pm + m0 + m1)) {
+      const bool second = !over(pm + m0);
+      S.found = 2 * tid + second;
+      S.before_mass = pm + (second ? m0 : 0);
+    }
+    __syncthreads();
+    const int r = S.found;                        // found: z > goal
+    if (r >= 0) {
       fetch_bins(r);
       if (warp == 0) {
         const unsigned c = S.bins[lane];
-        unsigned ci = c;
-        const u64 m = c ? mass_of(mc, key_value(key_of(r, lane))) * c : 0;
+        const u64 one = c ? mass_of(mc, key_value(key_of(r, lane))) : 0, m = one * c;
         u64 mi = m;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const unsigned tc = __shfl_up_sync(0xffffffffu, ci, o);
           const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
-          if (lane >= o) {
-            ci += tc;
-            mi += tm;
-          }
+          if (lane >= o) mi += tm;
         }
-        const int bin = __ffs(__ballot_sync(0xffffffffu, S.before_count + ci >= k_th)) - 1;
+        const int bin = __ffs(__ballot_sync(0xffffffffu, over(S.before_mass + mi))) - 1;
         if (lane == bin) {
+          // equal values have equal masses: the first t + 1 of them in index order stay
+          const u64 above = S.before_mass + mi - m;
+          const u64 tc = min((goal - above) / one, static_cast<u64>(c - 1));
           S.bin = bin;
-          S.z = S.before_mass + mi;
+          S.t_cut = tc + 1 < c ? tc : ~0ull;      // ~0: all of them
+          S.z = above + (tc + 1) * one;
         }
       }
       __syncthreads();
-      vcut = key_of(r, S.bin);
+      const uint32_t v = key_of(r, S.bin);
+      const u64 tc = S.t_cut;
       z = S.z;
-      __syncthreads();
-    }
-    // ---- top-p: the value at which the running mass first exceeds top_p of the whole
-    if (use_p) {
-      if (tid == 0) {
-        S.found = -1;
-        S.t_cut = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
-      }
-      __syncthreads();
-      const u64 goal = S.t_cut;                     // a whole sum exceeds top_p z iff it exceeds its floor
-      auto over = [&](u64 v) { return v > goal; };
-      if (!over(pm) && over(pm + m0 + m1)) {
-        const bool second = !over(pm + m0);
-        S.found = 2 * tid + second;
-        S.before_mass = pm + (second ? m0 : 0);
-      }
-      __syncthreads();
-      const int r = S.found;                        // found: z > goal
-      if (r >= 0) {
-        fetch_bins(r);
-        if (warp == 0) {
-          const unsigned c = S.bins[lane];
-          const u64 one = c ? mass_of(mc, key_value(key_of(r, lane))) : 0, m = one * c;
-          u64 mi = m;
+      vcut = v;
+      if (tc != ~0ull) {
+        // the index of the (t + 1)-th token of this value: counts in vocabulary
+        // order, a round of 1024 chunks at a time
+        u64 seen = 0;
+        for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
+          const int c = c_first + tid;
+          uint4 k = make_uint4(0, 0, 0, 0);       // key 0 is a NaN, never the cut
+          if (c < row.chunks) k = chunk_keys(load_chunk(row, c));
+          unsigned mine = 0;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const u64 tm = __shfl_up_sync(0xffffffffu, mi, o);
-            if (lane >= o) mi += tm;
+          for (int e = 0; e < 8; ++e) mine += chunk_half(k, e) == v;
+          u64 all;
+          u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
+          if (rank <= tc && tc < rank + mine) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (chunk_half(k, e) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
           }
-          const int bin = __ffs(__ballot_sync(0xffffffffu, over(S.before_mass + mi))) - 1;
-          if (lane == bin) {
-            // equal values have equal masses: the first t + 1 of them in index order stay
-            const u64 above = S.before_mass + mi - m;
-            const u64 tc = min((goal - above) / one, static_cast<u64>(c - 1));
-            S.bin = bin;
-            S.t_cut = tc + 1 < c ? tc : ~0ull;      // ~0: all of them
-            S.z = above + (tc + 1) * one;
-          }
+          seen += all;
+          if (seen > tc) break;                   // the same for every thread
         }
         __syncthreads();
-        const uint32_t v = key_of(r, S.bin);
-        const u64 tc = S.t_cut;
-        z = S.z;
-        vcut = v;
-        if (tc != ~0ull) {
-          // the index of the (t + 1)-th token of this value: counts in vocabulary
-          // order, a round of 1024 chunks at a time
-          u64 seen = 0;
-          for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
-            const int c = c_first + tid;
-            uint4 k = make_uint4(0, 0, 0, 0);       // key 0 is a NaN, never the cut
-            if (c < row.chunks) k = chunk_keys(load_chunk(row, c));
-            unsigned mine = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mine += chunk_half(k, e) == v;
-            u64 all;
-            u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
-            if (rank <= tc && tc < rank + mine) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (chunk_half(k, e) == v && rank++ == tc) S.x_cut = row.base + 8 * c + e;
-            }
-            seen += all;
-            if (seen > tc) break;                   // the same for every thread
-          }
-          __syncthreads();
-          xcut = S.x_cut;
-        }
+        xcut = S.x_cut;
       }
     }
   }
@@ -658,6 +570,229 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     }
     p.rows[blockIdx.x] = out;
     if (i < n && p.p_draft) p.p_draft[at] = static_cast<float>(static_cast<double>(out.mx) / static_cast<double>(z));
+  }
+}
+
+// ---------------------------------------------------------------- rows, small top-k
+struct TopSmem {
+  float2 table[257];
+  u64 red[33];
+  u64 mass[kTopThreads];
+  uint32_t key[kTopThreads];
+  int x[kTopThreads];
+  unsigned n, n_out, best;
+  int found, x_cut;
+};
+
+// Sum over the block (exact), for every thread.
+template <int THREADS>
+__device__ __forceinline__ u64 block_sum(u64 v, u64 *sh) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  u64 t = (threadIdx.x & 31) < THREADS / 32 ? sh[threadIdx.x & 31] : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  __syncthreads();                                // sh may be reused
+  return t;
+}
+
+__global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const VerifyParams p) {
+  __shared__ TopSmem S;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int b = blockIdx.x / (p.T + 1), i = blockIdx.x - b * (p.T + 1);
+  griddep_launch_dependents();
+  int n_draft = p.T;
+  if (p.n_draft) {
+    const int v = p.n_draft[b];
+    n_draft = min(max(v, 0), p.T);
+    if (n_draft != v && i == 0 && tid == 0) set_status(p.status, kDevBadInput);
+  }
+  const long long at = static_cast<long long>(b) * p.T + i;
+  if (i >= n_draft && i < p.T && p.p_draft && tid == 0) p.p_draft[at] = 0.f;   // no draft in this row
+  if (i > n_draft) return;
+  const Row row = make_row(p.logits + static_cast<long long>(blockIdx.x) * p.ld, p.V);
+  const int x_in = i < n_draft ? p.drafts[at] : -1;
+  const bool x_ok = x_in >= 0 && x_in < p.V;
+  auto for_chunks = [&](auto &&fn) {              // fn(chunk, its eight order keys in pairs), some loads at a time
+    for (int c0 = tid; c0 < row.chunks; c0 += kBatch * kTopThreads) {
+      uint4 w[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (c0 + k * kTopThreads < row.chunks) w[k] = load_chunk(row, c0 + k * kTopThreads);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (c0 + k * kTopThreads < row.chunks) fn(c0 + k * kTopThreads, chunk_keys(w[k]));
+    }
+  };
+  for (int k = tid; k < 257; k += kTopThreads) S.table[k] = kPow2.v[k];
+  if (tid == 0) {
+    S.n = S.n_out = S.best = 0;
+    S.x_cut = -1;
+    S.found = 0x10000;
+  }
+  uint32_t top2 = 0;                              // two maxima side by side
+  for_chunks([&](int, const uint4 &k) { top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(k.x, k.y)), __vmaxu2(k.z, k.w)); });
+  const uint32_t my_max = max(top2 & 0xffffu, top2 >> 16);
+  __syncthreads();
+  const uint32_t warp_best = __reduce_max_sync(0xffffffffu, my_max);
+  if (lane == 0) atomicMax(&S.best, warp_best);
+  // the largest bound that k of the maxima reach, bit by bit (0: fewer than k threads have a chunk)
+  auto bound_of = [&](auto &&reach) {
+    uint32_t t = 0;
+#pragma unroll 1
+    for (uint32_t bit = 0x8000u; bit; bit >>= 1)
+      if (reach(t | bit)) t |= bit;
+    return t;
+  };
+  const uint32_t least = bound_of([&](uint32_t t) { return __syncthreads_count(my_max >= t) >= p.top_k; });
+  const float lmax = key_value(S.best);
+  const bool fine = lmax > -INFINITY && lmax < INFINITY;              // NaN and infinities: no distribution
+  if (tid == 0 && (!fine || (i < n_draft && !x_ok))) set_status(p.status, kDevBadInput);
+  VerifyRow out{};
+  out.argmax = out.listed = -1;
+  out.lmax = lmax;
+  if (!fine) {
+    if (tid == 0) {
+      p.rows[blockIdx.x] = out;
+      if (i < n_draft && p.p_draft) p.p_draft[at] = 0.f;
+    }
+    return;
+  }
+  const MassCtx mc{lmax, p.c_hi, p.c_lo, S.table};
+  const bool use_p = p.top_p < 1.f;
+  uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
+  int xcut = p.V;
+  u64 z = 0;
+  // ---- what reaches the bound
+  for_chunks([&](int c, const uint4 &k) {
+    const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w));
+    if (max(t2 & 0xffffu, t2 >> 16) < least) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int x = row.base + 8 * c + e;
+      if (chunk_half(k, e) < least || x < 0 || x >= p.V) continue;
+      const unsigned to = atomicAdd(&S.n, 1u);
+      if (to < kTopThreads) {
+        S.key[to] = chunk_half(k, e);
+        S.x[to] = x;
+      }
+    }
+  });
+  __syncthreads();
+  const int n = static_cast<int>(S.n);
+  if (n >= p.top_k && n <= kTopThreads) {
+    const bool mine = tid < n;
+    const uint32_t key = mine ? S.key[tid] : 0;
+    const int x = mine ? S.x[tid] : 0;
+    int larger = 0, no_less = 0;
+    if (mine) {
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        larger += S.key[k] > key;
+        no_less += S.key[k] >= key;
+      }
+      if (larger < p.top_k && p.top_k <= no_less) S.found = static_cast<int>(key);   // the k-th largest
+    }
+    __syncthreads();
+    vcut = static_cast<uint32_t>(S.found);
+    const u64 mass = mine && key >= vcut ? mass_of(mc, key_value(key)) : 0;
+    S.mass[tid] = mass;
+    bool stays = mass != 0;
+    z = block_sum<kTopThreads>(mass, S.red);
+    if (use_p) {
+      // a token stays while what comes before it in descending order (equal values in
+      // index order) does not exceed top_p of the whole
+      const u64 goal = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
+      if (stays) {
+        u64 before = 0;
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) {
+          const uint32_t o = S.key[k];
+          before += o > key || (o == key && S.x[k] < x) ? S.mass[k] : 0;
+        }
+        stays = before <= goal;
+      }
+      if (tid == 0) S.found = 0x10000;
+      __syncthreads();
+      if (stays) atomicMin(&S.found, static_cast<int>(key));
+      z = block_sum<kTopThreads>(stays ? mass : 0, S.red);
+      vcut = static_cast<uint32_t>(S.found);
+      if (stays && key == vcut) atomicMax(&S.x_cut, x);
+      __syncthreads();
+      xcut = S.x_cut;
+    }
+    VerifyToken *list = p.lists + static_cast<long long>(blockIdx.x) * kVerifyList;
+    if (stays) {
+      const unsigned to = atomicAdd(&S.n_out, 1u);
+      if (to < kVerifyList) list[to] = VerifyToken{mass, x, 0};
+    }
+    __syncthreads();
+    if (S.n_out <= kVerifyList) out.listed = static_cast<int>(S.n_out);
+  } else {
+    // ---- fewer chunks than k, or many equal values: by passes over the row
+    auto mass_from = [&](uint32_t t) {
+      u64 m = 0;
+      for_chunks([&](int, const uint4 &k) {
+#pragma unroll 1
+        for (int e = 0; e < 8; ++e)
+          if (chunk_half(k, e) >= t) m += mass_of(mc, key_value(chunk_half(k, e)));
+      });
+      return block_sum<kTopThreads>(m, S.red);
+    };
+    auto count_from_key = [&](uint32_t t) {
+      u64 m = 0;
+      for_chunks([&](int c, const uint4 &k) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int x = row.base + 8 * c + e;
+          m += chunk_half(k, e) >= t && x >= 0 && x < p.V;
+        }
+      });
+      return block_sum<kTopThreads>(m, S.red);
+    };
+    vcut = bound_of([&](uint32_t t) { return count_from_key(t) >= static_cast<u64>(p.top_k); });
+    z = mass_from(vcut);
+    if (use_p) {
+      const u64 goal = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
+      const uint32_t v = bound_of([&](uint32_t t) { return mass_from(t) > goal; });   // at least the k-th largest: z > goal
+      const u64 above = mass_from(v + 1), one = mass_of(mc, key_value(v));
+      const u64 c = count_from_key(v) - count_from_key(v + 1), tc = min((goal - above) / one, c - 1);
+      z = above + (tc + 1) * one;
+      vcut = v;
+      // the index of the (tc + 1)-th token of this value, a round of chunks at a time
+      u64 seen = 0;
+      for (int c_first = 0; c_first < row.chunks && seen <= tc; c_first += kTopThreads) {
+        const int cc = c_first + tid;
+        uint4 k = make_uint4(0, 0, 0, 0);         // key 0 is a NaN, never the cut
+        if (cc < row.chunks) k = chunk_keys(load_chunk(row, cc));
+        unsigned many = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) many += chunk_half(k, e) == v;
+        u64 all;
+        u64 rank = seen + block_scan<kTopThreads>(many, S.red, &all);
+        if (rank <= tc && tc < rank + many) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (chunk_half(k, e) == v && rank++ == tc) S.x_cut = row.base + 8 * cc + e;
+        }
+        seen += all;
+      }
+      __syncthreads();
+      xcut = S.x_cut;
+    }
+  }
+  if (tid == 0) {
+    out.z = z;
+    out.vcut = vcut;
+    out.xcut = xcut;
+    if (x_ok) {
+      const uint32_t key = bf16_order_key(row.p[x_in]);
+      if (key > vcut || (key == vcut && x_in <= xcut)) out.mx = mass_of(mc, key_value(key));
+    }
+    p.rows[blockIdx.x] = out;
+    if (i < n_draft && p.p_draft) p.p_draft[at] = static_cast<float>(static_cast<double>(out.mx) / static_cast<double>(z));
   }
 }
 
@@ -816,8 +951,12 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st, int *launches) {
   cudaError_t e = ensure_smem_attr<verify_rows_kernel>(sizeof(RowSmem));
   if (e != cudaSuccess) return e;
+  const unsigned rows = static_cast<unsigned>(p.B) * (p.T + 1);
   prof_before(SMOL_K_SAMPLE, st);
-  verify_rows_kernel<<<static_cast<unsigned>(p.B) * (p.T + 1), kRowThreads, sizeof(RowSmem), st>>>(p);
+  if (!p.greedy && p.top_k > 0 && p.top_k <= kTopMaxK && p.top_k < p.V)
+    verify_top_kernel<<<rows, kTopThreads, 0, st>>>(p);
+  else
+    verify_rows_kernel<<<rows, kRowThreads, sizeof(RowSmem), st>>>(p);
   prof_after(SMOL_K_SAMPLE, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches = 1;
