@@ -121,6 +121,13 @@ __global__ void __launch_bounds__(512, 1)
     }
     return;
   }
+  if (tid == 0) {
+    tma_prefetch_desc(&tmQ);
+    if (!FP8) {
+      tma_prefetch_desc(&tmK);
+      tma_prefetch_desc(&tmV);
+    }
+  }
   // the schedule's scratch lies where Q will
   PagedIter it = paged_locate<C::THREADS>(p, cta, p.ctas, *reinterpret_cast<PagedSchedSmem *>(sQ));
   if (it.left == 0) {                             // the same for the whole CTA

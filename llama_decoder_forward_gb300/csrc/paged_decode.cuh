@@ -125,6 +125,11 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(q_full + 2);
   volatile int *s_parts = abort_flag + 1;         // [2] a unit to combine: its first CTA, and how many
 
+  if (tid == 0) {
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
   PagedSchedSmem &sched = *reinterpret_cast<PagedSchedSmem *>(merge);
   PagedIter ld = paged_locate<C::THREADS>(p, cta, p.ctas, sched);
   if (ld.left == 0) return;                       // the same for the whole CTA
@@ -526,38 +531,38 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
       for (int step = 0; step < 4; ++step) {
         const int from = step == 0 ? 4 : step == 1 ? 6 : step == 2 ? 2 : 1, to = step == 1 ? 2 : 0, n = step == 3 ? 1 : 2;
         if (warp >= from && warp < from + n) {
-          float *dst = merge + (warp - from) * 32 * C::MERGE_WORDS + lane;
+          float4 *dst = reinterpret_cast<float4 *>(merge + (warp - from) * 32 * C::MERGE_WORDS) + lane;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
             for (int d = 0; d < ND8; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) dst[(rt * (ND8 * 4 + 4) + d * 4 + e) * 32] = o[rt][d][e];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              dst[(rt * (ND8 * 4 + 4) + ND8 * 4 + i) * 32] = m[rt][i];
-              dst[(rt * (ND8 * 4 + 4) + ND8 * 4 + 2 + i) * 32] = l[rt][i];
-            }
+              dst[(rt * (ND8 + 1) + d) * 32] = make_float4(o[rt][d][0], o[rt][d][1], o[rt][d][2], o[rt][d][3]);
+            dst[(rt * (ND8 + 1) + ND8) * 32] = make_float4(m[rt][0], m[rt][1], l[rt][0], l[rt][1]);
           }
         }
         __syncthreads();
         if (warp >= to && warp < to + n) {
-          const float *src = merge + (warp - to) * 32 * C::MERGE_WORDS + lane;
+          const float4 *src = reinterpret_cast<const float4 *>(merge + (warp - to) * 32 * C::MERGE_WORDS) + lane;
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) {
-            const float *sr = src + rt * (ND8 * 4 + 4) * 32;
+            const float4 other = src[(rt * (ND8 + 1) + ND8) * 32];
+            const float m2[2] = {other.x, other.y}, l2[2] = {other.z, other.w};
+            float a[2], a2[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float m2 = sr[(ND8 * 4 + i) * 32], l2 = sr[(ND8 * 4 + 2 + i) * 32];
-              const float mn = fmaxf(m[rt][i], m2);
-              const float a = mn == -INFINITY ? 1.f : ex2_approx(m[rt][i] - mn), a2 = mn == -INFINITY ? 1.f : ex2_approx(m2 - mn);
+              const float mn = fmaxf(m[rt][i], m2[i]);
+              a[i] = mn == -INFINITY ? 1.f : ex2_approx(m[rt][i] - mn);
+              a2[i] = mn == -INFINITY ? 1.f : ex2_approx(m2[i] - mn);
               m[rt][i] = mn;
-              l[rt][i] = l[rt][i] * a + l2 * a2;
+              l[rt][i] = l[rt][i] * a[i] + l2[i] * a2[i];
+            }
 #pragma unroll
-              for (int d = 0; d < ND8; ++d)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  o[rt][d][2 * i + e] = o[rt][d][2 * i + e] * a + sr[(d * 4 + 2 * i + e) * 32] * a2;
+            for (int d = 0; d < ND8; ++d) {
+              const float4 v = src[(rt * (ND8 + 1) + d) * 32];
+              o[rt][d][0] = o[rt][d][0] * a[0] + v.x * a2[0];
+              o[rt][d][1] = o[rt][d][1] * a[0] + v.y * a2[0];
+              o[rt][d][2] = o[rt][d][2] * a[1] + v.z * a2[1];
+              o[rt][d][3] = o[rt][d][3] * a[1] + v.w * a2[1];
             }
           }
         }

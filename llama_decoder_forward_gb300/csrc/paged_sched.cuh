@@ -72,6 +72,12 @@ __device__ __forceinline__ long long paged_seq_tiles(const PagedAttnParams &p, c
   return sum * p.kv.KV;
 }
 
+// a / b of whole numbers, b > 0; in 32 bits where they hold both (a division of 64 bits
+// takes hundreds of cycles, and every CTA's start waits for it)
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<unsigned>(a) / static_cast<unsigned>(b) : a / b;
+}
+
 struct PagedSchedSmem {
   long long warp_sum[32], total;
   int workers;
@@ -80,7 +86,7 @@ struct PagedSchedSmem {
 
 // The worker that has tile x of the line.
 __device__ __forceinline__ int paged_worker_of(long long x, long long total, int workers) {
-  return static_cast<int>(((x + 1) * workers - 1) / total);
+  return static_cast<int>(paged_div((x + 1) * workers - 1, total));
 }
 
 // Worker `w` of `workers`: its first tile and how many it has (left == 0: none; the
@@ -115,7 +121,7 @@ __device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int 
     sm.workers = workers;
   }
   if (w >= workers) return it;                    // the same for the whole CTA
-  const long long from = total * w / workers, to = total * (w + 1) / workers;
+  const long long from = paged_div(total * w, workers), to = paged_div(total * (w + 1), workers);
   // the sequence that holds tile `from`, THREADS sequences at a time
   long long before = 0;
   for (int base = 0; base < p.c.B; base += THREADS) {
@@ -151,7 +157,7 @@ __device__ __forceinline__ PagedIter paged_locate(const PagedAttnParams &p, int 
         paged_set_unit(p, it);
         const long long unit = it.j1 - it.j0, all = unit * p.kv.KV;
         if (off < all) {
-          it.kvh = static_cast<int>(off / unit);
+          it.kvh = static_cast<int>(paged_div(off, unit));
           it.j = it.j0 + static_cast<int>(off - it.kvh * unit);
           it.u0 = from - (it.j - it.j0);
           break;
@@ -194,15 +200,25 @@ template <int HD>
 __device__ __forceinline__ void paged_combine_row(const PagedAttnParams &p, int rows, int c0, int n, int r, float *weight,
                                                   long long out) {
   const int lane = threadIdx.x & 31;
+  constexpr int kHeld = (kPagedMaxCtas + 31) / 32;
+  float2 ml[kHeld];                               // this lane's parts' maxima and sums
   float mx = -INFINITY, sum = 0.f;
-  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, __ldcg(paged_part(p.ws, c0 + i, i == 0, rows, HD) + rows * HD + 2 * r));
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = lane + 32 * k;
+    ml[k] = make_float2(-INFINITY, 0.f);
+    if (i < n) ml[k] = __ldcg(reinterpret_cast<const float2 *>(paged_part(p.ws, c0 + i, i == 0, rows, HD) + rows * HD + 2 * r));
+  }
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) mx = fmaxf(mx, ml[k].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  for (int i = lane; i < n; i += 32) {
-    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(paged_part(p.ws, c0 + i, i == 0, rows, HD) + rows * HD + 2 * r));
-    const float a = mx == -INFINITY ? 0.f : ex2_approx(ml.x - mx);
-    weight[i] = a;
-    sum += a * ml.y;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = lane + 32 * k;
+    const float a = mx == -INFINITY ? 0.f : ex2_approx(ml[k].x - mx);
+    if (i < n) weight[i] = a;
+    sum += a * ml[k].y;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -211,7 +227,7 @@ __device__ __forceinline__ void paged_combine_row(const PagedAttnParams &p, int 
   float acc[HD / 32];
 #pragma unroll
   for (int e = 0; e < HD / 32; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < n; ++i) {
     const float *row = paged_part(p.ws, c0 + i, i == 0, rows, HD) + r * HD + lane * (HD / 32);
     const float a = weight[i];
