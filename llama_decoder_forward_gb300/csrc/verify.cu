@@ -19,12 +19,12 @@
 //   rows    one CTA of 1024 threads for each target row, which it reads one to
 //           three times (from L2 after the first; in registers it would take half
 //           of them, and the spills cost more).  bf16 logits take few distinct
-//           values, so the row becomes a histogram over the values (32,768
-//           counters: the values >= 0, or those < 0) and the exponential is taken
-//           once for each value that occurs: a tenth of the row and less.  The
-//           sum, the k-th largest value and the top-p cut are prefix sums over
-//           the histogram.  Where the k largest are all >= 0, the rest is not
-//           looked at.
+//           values, so the row becomes a histogram over the values, and the
+//           exponential is taken once for each value that occurs: a tenth of the row
+//           and less.  The 65,536 counters have 16 bits, two in a word; where one ran
+//           over, which the sum shows, the row is read again for a histogram of the
+//           values >= 0 and one of those < 0.  The sum, the k-th largest value and the
+//           top-p cut are prefix sums over the histogram.
 //           With top-k up to 256 another kernel does this without a histogram, two
 //           CTAs on an SM: the k-th largest of the threads' own maxima is a bound
 //           below which none of the k largest lies, and what reaches it, a little
@@ -217,6 +217,9 @@ __device__ __forceinline__ uint4 chunk_keys(const uint4 &c) {
   return make_uint4(order_key2(c.x), order_key2(c.y), order_key2(c.z), order_key2(c.w));
 }
 
+// The larger of the upper keys and of the lower ones, side by side.
+__device__ __forceinline__ uint32_t chunk_max2(const uint4 &k) { return __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w)); }
+
 __device__ __forceinline__ float key_value(uint32_t key) {
   const uint32_t bits = (key & 0x8000u) ? key & 0x7fffu : ~key & 0xffffu;
   return __uint_as_float(bits << 16);
@@ -226,6 +229,15 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 __device__ __forceinline__ void count_from(uint32_t base, uint32_t k, uint32_t from) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(base + 4 * k),
                "r"(k), "r"(from)
+               : "memory");
+}
+// The same for two counters of 16 bits in a word, the value >= 0 in the lower one and
+// the one < 0 of the same low 15 key bits in the upper; `n` counts along.
+__device__ __forceinline__ void count_packed(uint32_t base, uint32_t k, uint32_t from, uint32_t &n) {
+  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 v;\n\tsetp.ge.u32 p, %2, %3;\n\tsetp.ge.u32 q, %2, 0x8000;\n\t"
+               "selp.b32 v, 1, 0x10000, q;\n\t@p red.shared.add.u32 [%1], v;\n\t@p add.u32 %0, %0, 1;\n\t}"
+               : "+r"(n)
+               : "r"(base + 4 * (k & 0x7fffu)), "r"(k), "r"(from)
                : "memory");
 }
 
@@ -258,6 +270,20 @@ __device__ __forceinline__ u64 block_scan(u64 v, u64 *sh, u64 *total) {   // exc
   *total = sh[32];
   __syncthreads();
   return before + inc - v;
+}
+
+// Sum over the block (exact), for every thread.
+template <int THREADS>
+__device__ __forceinline__ u64 block_sum(u64 v, u64 *sh) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  __syncthreads();
+  u64 t = (threadIdx.x & 31) < THREADS / 32 ? sh[threadIdx.x & 31] : 0;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  __syncthreads();                                // sh may be reused
+  return t;
 }
 
 __device__ __forceinline__ u64 warp_max(u64 v) {
@@ -297,7 +323,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   const Row row = make_row(p.logits + static_cast<long long>(blockIdx.x) * p.ld, p.V);
 
   // fn(chunk, its eight order keys in pairs), over this thread's chunks, a batch of
-  // loads at a time; `between` runs with the first batch under way
+  // loads at a time; `between` runs with the first batch under way and is given the
+  // largest of its keys by a call
   auto for_chunks = [&](auto &&fn, auto &&between) {
     bool start = true;
     for (int c0 = tid; start || c0 < row.chunks; c0 += kBatch * kRowThreads) {
@@ -305,37 +332,76 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (c0 + k * kRowThreads < row.chunks) w[k] = load_chunk(row, c0 + k * kRowThreads);
-      if (start) between();
+      if (start)
+        between([&] {
+          uint32_t top2 = 0;
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            if (c0 + k * kRowThreads < row.chunks) top2 = __vmaxu2(top2, chunk_max2(chunk_keys(w[k])));
+          return max(top2 & 0xffffu, top2 >> 16);
+        });
       start = false;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (c0 + k * kRowThreads < row.chunks) fn(c0 + k * kRowThreads, chunk_keys(w[k]));
     }
   };
-  auto nothing = [] {};
+  auto nothing = [](auto &&) {};
+  auto block_max = [&](uint32_t v) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0) S.red[warp] = v;
+    __syncthreads();
+    v = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(S.red[lane]));
+    __syncthreads();
+    return v;
+  };
+  auto clear = [&] {
+    for (int k = tid; k < kBins / 4; k += kRowThreads) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
+  };
+  // a value below l_max - 32 temperature has mass 0 (45 ln 2 = 31.2): the smallest key
+  // that counts (one to spare for the truncation)
+  auto least_key = [&](uint32_t kmax) {
+    const float least = key_value(kmax) - 32.f * p.temperature;
+    if (!(least > -INFINITY)) return 0u;
+    const uint32_t k = bf16_order_key(static_cast<uint16_t>(__float_as_uint(least) >> 16));
+    return k > 0 ? k - 1 : 0u;
+  };
+  // one pass for both signs, the counters packed: the keys' maximum, and how many of this
+  // thread's were counted.  The largest of the first batch bounds what is counted.
+  uint32_t counted = 0;
+  auto count_both = [&] {
+    uint32_t top2 = 0, from = 0;
+    const uint32_t base = smem_u32(S.hist);
+    for_chunks([&](int, const uint4 &k) {
+      top2 = __vmaxu2(top2, chunk_max2(k));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) count_packed(base, chunk_half(k, e), from, counted);
+    }, [&](auto &&first_max) {
+      clear();
+      from = least_key(block_max(first_max()));
+    });
+    return max(top2 & 0xffffu, top2 >> 16);
+  };
   // adds the values of one sign with keys >= from to the histogram; in the pass over
   // the negative ones the keys' top bit is flipped, so that they are the upper half
   auto count = [&](int half, uint32_t from) {
     const uint32_t flip = half ? 0x80008000u : 0u, base = smem_u32(S.hist) - 4 * kBins;
-    uint32_t top2 = 0;                            // two maxima side by side
     for_chunks([&](int, const uint4 &k) {
-      top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(k.x, k.y)), __vmaxu2(k.z, k.w));
       const uint4 q = make_uint4(k.x ^ flip, k.y ^ flip, k.z ^ flip, k.w ^ flip);
 #pragma unroll
       for (int e = 0; e < 8; ++e) count_from(base, chunk_half(q, e), from);
-    }, [&] {
-      for (int k = tid; k < kBins / 4; k += kRowThreads) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
+    }, [&](auto &&) {
+      clear();
       __syncthreads();
     });
-    return max(top2 & 0xffffu, top2 >> 16);
   };
 
-  // ---- the largest value, with the histogram of the values >= 0 on the way
+  // ---- the largest value, with the histogram on the way
   const bool use_k = p.top_k > 0 && p.top_k < p.V, use_p = p.top_p < 1.f;
   u64 best = 0;
   if (p.greedy) {
     for_chunks([&](int c, const uint4 &k) {       // chunks ascend: the first of equal values stays
-      const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w)), t = max(t2 & 0xffffu, t2 >> 16);
+      const uint32_t t2 = chunk_max2(k), t = max(t2 & 0xffffu, t2 >> 16);
       if (t > static_cast<uint32_t>(best >> 32)) {
         int x = 0;
 #pragma unroll
@@ -345,7 +411,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       }
     }, nothing);
   } else {
-    best = argmax_pack(count(0, 0x8000u), 0);
+    best = argmax_pack(count_both(), 0);
   }
   best = warp_max(best);
   if (lane == 0) S.red[warp] = best;
@@ -374,59 +440,67 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     return;
   }
   const MassCtx mc = MassCtx{lmax, p.c_hi, p.c_lo, S.table};
-  // a value below l_max - 32 temperature has mass 0 (45 ln 2 = 31.2); it is not counted
-  const uint32_t kmin = bf16_order_key(static_cast<uint16_t>(__float_as_uint(lmax - 32.f * p.temperature) >> 16));
-  const uint32_t kcount = kmin > 0 ? kmin - 1 : 0;   // the smallest key counted (one to spare for the truncation)
-
-  // ---- counts and masses of rows of 32 neighbouring values, the largest first
-  auto sum_rows = [&](int half, uint32_t from) {
-    const uint32_t top = half == 0 ? 0xffffu : 0x7fffu;
-    const int r_end = static_cast<int>((0x10000u - from + 31) >> 5);
+  // ---- counts and masses of rows of 32 neighbouring values, the largest first: of one
+  // sign (rows 0 .. 1023 or 1024 .. 2047), or of both where the counters are packed
+  auto sum_row = [&](int r, unsigned c) {
+    unsigned cs = 0;
+    u64 ms = 0;
+    if (__any_sync(0xffffffffu, c != 0)) {
+      ms = mass_of(mc, key_value((r < kBinRows ? 0xffffu : 0x7fffu) - ((r & (kBinRows - 1)) * 32 + lane))) * c;
+      cs = __reduce_add_sync(0xffffffffu, c);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
+    }
+    if (lane == 0) {
+      S.row_count[r] = cs;
+      S.row_mass[r] = ms;
+    }
+  };
+  auto sum_rows = [&](int half, bool packed) {
     for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
       unsigned c[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 8; ++k) {
         const int r = r0 + k * (kRowThreads / 32);
-        unsigned cs = 0;
-        u64 ms = 0;
-        if (r < r_end && __any_sync(0xffffffffu, c[k] != 0)) {
-          ms = mass_of(mc, key_value(top - (r * 32 + lane))) * c[k];
-          cs = __reduce_add_sync(0xffffffffu, c[k]);
+        if (packed) {
+          sum_row(r, c[0] & 0xffffu);
+          sum_row(kBinRows + r, c[0] >> 16);
+        } else {
+          sum_row(half * kBinRows + r, c[0]);
+        }
 #pragma unroll
-          for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
-        }
-        if (lane == 0) {
-          S.row_count[half * kBinRows + r] = cs;
-          S.row_mass[half * kBinRows + r] = ms;
-        }
+        for (int i = 0; i < 7; ++i) c[i] = c[i + 1];
       }
     }
     __syncthreads();
   };
-  int resident = 0;
-  sum_rows(0, 0x8000u);
-  // the negative values: not where none of them counts, nor where the k largest are all >= 0
-  bool negative = kcount <= 0x7fffu;
-  if (use_k && negative) {
-    unsigned c = __reduce_add_sync(0xffffffffu, S.row_count[tid]);
-    if (lane == 0) S.red[warp] = c;
+  enum { kPositive, kNegative, kBoth };
+  int resident = kBoth;                           // the values that the histogram holds
+  sum_rows(0, true);
+  if (block_sum<kRowThreads>(static_cast<int>(S.row_count[tid] + S.row_count[kBinRows + tid] - counted), S.red) != 0) {
+    // a counter of 16 bits ran over, which takes 65,535 or 65,536 from the sum: again,
+    // a sign at a time, with 32 bits
+    resident = kPositive;
+    count(0, 0x8000u);
     __syncthreads();
-    c = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(S.red[lane]));
-    negative = c < static_cast<unsigned>(p.top_k);
+    sum_rows(0, false);
+    // the negative values: not where none of them counts, nor where the k largest are all >= 0
+    const uint32_t from = least_key(kmax);
+    bool negative = from <= 0x7fffu;
+    if (use_k && negative) negative = block_sum<kRowThreads>(S.row_count[tid], S.red) < static_cast<u64>(p.top_k);
+    if (negative) {
+      resident = kNegative;
+      count(1, from + 0x8000u);
+      __syncthreads();
+      sum_rows(1, false);
+    } else {
+      S.row_count[kBinRows + tid] = 0;
+      S.row_mass[kBinRows + tid] = 0;
+    }
     __syncthreads();
   }
-  if (negative) {
-    resident = 1;
-    count(1, kcount + 0x8000u);
-    __syncthreads();
-    sum_rows(1, kcount + 0x8000u);
-  } else {
-    S.row_count[kBinRows + tid] = 0;
-    S.row_mass[kBinRows + tid] = 0;
-  }
-  __syncthreads();
   // prefix sums over the 2048 rows of values, two for each thread
   u64 total_c, total_m;
   const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
@@ -436,8 +510,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
 
   // the counters of one row of 32 values, into S.bins
   auto fetch_bins = [&](int r) {
-    const bool here = r / kBinRows == resident;
-    if (tid < 32) S.bins[tid] = here ? S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)] : 0u;
+    const bool here = resident == kBoth || r / kBinRows == resident;
+    if (tid < 32) {
+      const unsigned c = S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)];
+      S.bins[tid] = !here ? 0u : resident != kBoth ? c : r < kBinRows ? c & 0xffffu : c >> 16;
+    }
     __syncthreads();
     if (here) return;
     const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
@@ -584,20 +661,6 @@ struct TopSmem {
   int found, x_cut;
 };
 
-// Sum over the block (exact), for every thread.
-template <int THREADS>
-__device__ __forceinline__ u64 block_sum(u64 v, u64 *sh) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 t = (threadIdx.x & 31) < THREADS / 32 ? sh[threadIdx.x & 31] : 0;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  __syncthreads();                                // sh may be reused
-  return t;
-}
-
 __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const VerifyParams p) {
   __shared__ TopSmem S;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -633,7 +696,7 @@ __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const Verify
     S.found = 0x10000;
   }
   uint32_t top2 = 0;                              // two maxima side by side
-  for_chunks([&](int, const uint4 &k) { top2 = __vmaxu2(__vmaxu2(top2, __vmaxu2(k.x, k.y)), __vmaxu2(k.z, k.w)); });
+  for_chunks([&](int, const uint4 &k) { top2 = __vmaxu2(top2, chunk_max2(k)); });
   const uint32_t my_max = max(top2 & 0xffffu, top2 >> 16);
   __syncthreads();
   const uint32_t warp_best = __reduce_max_sync(0xffffffffu, my_max);
@@ -667,7 +730,7 @@ __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const Verify
   u64 z = 0;
   // ---- what reaches the bound
   for_chunks([&](int c, const uint4 &k) {
-    const uint32_t t2 = __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w));
+    const uint32_t t2 = chunk_max2(k);
     if (max(t2 & 0xffffu, t2 >> 16) < least) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -887,7 +950,7 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   const uint32_t vcut2 = r.vcut | (r.vcut << 16);
   auto weights = [&](int c, u64 (&w)[8]) -> u64 {
     const uint4 keys = chunk_keys(load_chunk(row, c));
-    const uint32_t t2 = __vmaxu2(__vmaxu2(keys.x, keys.y), __vmaxu2(keys.z, keys.w));
+    const uint32_t t2 = chunk_max2(keys);
     u64 sum = 0;
     if (__vmaxu2(t2, vcut2) == vcut2 && (t2 & 0xffffu) != r.vcut && (t2 >> 16) != r.vcut) {
       // none of the eight stays

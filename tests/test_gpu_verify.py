@@ -143,6 +143,33 @@ def test_filters_on_both_ways(S, V, top_k):
             check(S, lg, drafts, u, None, top_k=top_k, **kw)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=300), dict(top_k=100000, top_p=0.9), dict(top_p=0.5)])
+def test_values_that_fill_a_counter(S, kw):
+    """65,536 tokens and more of one value, of either sign, among 150,000."""
+    V, T = 150000, 6
+    logits, drafts, u, probs = case(2, T, V, seed=3)
+    at = torch.randperm(V, generator=torch.Generator("cuda").manual_seed(4), device="cuda")
+    for i, (many, value, other) in enumerate([(65535, 1.5, None), (65536, 1.5, None), (131072, -0.75, None), (70000, -0.75, 1.5),
+                                              (65536, 0.0, -0.75), (65537, -9.0, 9.0), (150000, -3.0, None)]):
+        logits[:, i, at[:many]] = value
+        if other is not None:
+            logits[:, i, at[many:many + 65536]] = other   # 65,536 of these too, where they fit
+    check(S, logits, drafts, u, probs, **kw)
+    check(S, logits, drafts, u, None, **kw)
+
+
+@pytest.mark.parametrize("hidden", [-math.inf, torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=300, top_p=0.9)])
+def test_a_masked_vocabulary(S, hidden, kw):
+    V, T = 128257, 3
+    logits, drafts, u, probs = case(2, T, V, seed=5)
+    logits[0, :, :100000] = hidden                         # all that is looked at first
+    logits[1, :, 70:] = hidden
+    drafts[1] = torch.tensor([69, 3, 128256])
+    check(S, logits, drafts, u, probs, **kw)
+    check(S, logits, drafts, u, None, **kw)
+
+
 def test_zeros_of_both_signs_are_equal(S):
     B, T, V = 12, 2, 3000
     g = torch.Generator("cuda").manual_seed(21)
