@@ -456,36 +456,61 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       S.row_mass[r] = ms;
     }
   };
-  auto sum_rows = [&](int half, bool packed) {
+  // fn(word row, its word in this lane), rows without tokens left out
+  auto for_words = [&](auto &&fn) {
     for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
       unsigned c[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
 #pragma unroll 1
       for (int k = 0; k < 8; ++k) {
-        const int r = r0 + k * (kRowThreads / 32);
-        if (packed) {
-          sum_row(r, c[0] & 0xffffu);
-          sum_row(kBinRows + r, c[0] >> 16);
-        } else {
-          sum_row(half * kBinRows + r, c[0]);
-        }
+        if (__any_sync(0xffffffffu, c[0] != 0)) fn(r0 + k * (kRowThreads / 32), c[0]);
 #pragma unroll
         for (int i = 0; i < 7; ++i) c[i] = c[i + 1];
       }
     }
+  };
+  auto clear_rows = [&](int half) {
+    S.row_count[half * kBinRows + tid] = 0;
+    S.row_mass[half * kBinRows + tid] = 0;
+  };
+  auto sum_rows = [&](int half) {
+    clear_rows(half);
+    __syncthreads();
+    for_words([&](int r, unsigned c) { sum_row(half * kBinRows + r, c); });
     __syncthreads();
   };
   enum { kPositive, kNegative, kBoth };
   int resident = kBoth;                           // the values that the histogram holds
-  sum_rows(0, true);
-  if (block_sum<kRowThreads>(static_cast<int>(S.row_count[tid] + S.row_count[kBinRows + tid] - counted), S.red) != 0) {
+  u64 total_m = 0;
+  unsigned held = 0;
+  if (use_k || use_p) {
+    clear_rows(0);
+    clear_rows(1);
+    __syncthreads();
+    for_words([&](int r, unsigned c) {
+      sum_row(r, c & 0xffffu);
+      sum_row(kBinRows + r, c >> 16);
+    });
+    __syncthreads();
+    held = S.row_count[tid] + S.row_count[kBinRows + tid];
+  } else {
+    // only the whole sum is wanted
+    for_words([&](int r, unsigned c) {
+      const unsigned plus = c & 0xffffu, minus = c >> 16;
+      held += plus + minus;
+      if (plus) total_m += mass_of(mc, key_value(0xffffu - (r * 32 + lane))) * plus;
+      if (minus) total_m += mass_of(mc, key_value(0x7fffu - (r * 32 + lane))) * minus;
+    });
+    total_m = block_sum<kRowThreads>(total_m, S.red);
+  }
+  if (block_sum<kRowThreads>(static_cast<int>(held - counted), S.red) != 0) {
     // a counter of 16 bits ran over, which takes 65,535 or 65,536 from the sum: again,
     // a sign at a time, with 32 bits
     resident = kPositive;
     count(0, 0x8000u);
     __syncthreads();
-    sum_rows(0, false);
+    sum_rows(0);
     // the negative values: not where none of them counts, nor where the k largest are all >= 0
     const uint32_t from = least_key(kmax);
     bool negative = from <= 0x7fffu;
@@ -494,19 +519,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       resident = kNegative;
       count(1, from + 0x8000u);
       __syncthreads();
-      sum_rows(1, false);
+      sum_rows(1);
     } else {
-      S.row_count[kBinRows + tid] = 0;
-      S.row_mass[kBinRows + tid] = 0;
+      clear_rows(1);
     }
     __syncthreads();
   }
   // prefix sums over the 2048 rows of values, two for each thread
-  u64 total_c, total_m;
-  const unsigned c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
-  const u64 m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
-  const u64 pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
-  const u64 pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
+  u64 total_c = 0, m0 = 0, m1 = 0, pc = 0, pm = 0;
+  unsigned c0 = 0, c1 = 0;
+  if (use_k || use_p || resident != kBoth) {
+    c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
+    m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
+    pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
+    pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
+  }
 
   // the counters of one row of 32 values, into S.bins
   auto fetch_bins = [&](int r) {
@@ -942,27 +969,33 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   const bool refused = kept < n;
   const float *q = refused && p.probs ? p.probs + at * p.ldq : nullptr;
   const int gone = refused && !p.probs ? p.drafts[at] : -1;           // q is 1 there: nothing is left of p
-  // this thread's chunks, in vocabulary order across the cluster
-  const int per = (row.chunks + kChoiceCtas * kChoiceThreads - 1) / (kChoiceCtas * kChoiceThreads);
-  const int first = min(row.chunks, (static_cast<int>(rank) * kChoiceThreads + tid) * per), last = min(row.chunks, first + per);
+  // this warp's chunks, in vocabulary order across the cluster: rounds of 32
+  const int lane = tid & 31, warp = static_cast<int>(rank) * (kChoiceThreads / 32) + (tid >> 5);
+  const int rounds = (row.chunks + kChoiceCtas * kChoiceThreads - 1) / (kChoiceCtas * kChoiceThreads);
+  const int first = warp * rounds * 32 + lane;
   bool rest = refused;                            // weights max(p - q, 0), else p
   const float zh = __ull2float_rn(r.z), zl = rest_of(r.z, zh);
-  const uint32_t vcut2 = r.vcut | (r.vcut << 16);
   auto weights = [&](int c, u64 (&w)[8]) -> u64 {
-    const uint4 keys = chunk_keys(load_chunk(row, c));
-    const uint32_t t2 = chunk_max2(keys);
-    u64 sum = 0;
-    if (__vmaxu2(t2, vcut2) == vcut2 && (t2 & 0xffffu) != r.vcut && (t2 >> 16) != r.vcut) {
-      // none of the eight stays
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 0;
-      return 0;
+    for (int e = 0; e < 8; ++e) w[e] = 0;
+    if (c >= row.chunks) return 0;
+    const uint4 keys = chunk_keys(load_chunk(row, c));
+    u64 sum = 0;
+    if (r.vcut) {
+      const uint32_t t2 = chunk_max2(keys);
+      if (max(t2 & 0xffffu, t2 >> 16) < r.vcut) return 0;             // none of the eight stays
     }
     const int x0 = row.base + 8 * c;
     float qv[8];
     if (rest && q) {
+      const float *from = q + x0;
+      if (x0 >= 0 && x0 + 8 <= p.V) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qv[e] = x0 + e >= 0 && x0 + e < p.V ? q[x0 + e] : 0.f;
+        for (int e = 0; e < 8; ++e) qv[e] = from[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qv[e] = x0 + e >= 0 && x0 + e < p.V ? from[e] : 0.f;
+      }
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -976,12 +1009,12 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
     }
     return sum;
   };
-  u64 w[8], mine, before, whole;                  // this thread's mass, that of all before it, and the whole
+  u64 w[8], mine, before, whole;                  // this thread's mass, that of all threads before it, and the whole
   while (true) {
     u64 all;
     mine = 0;
 #pragma unroll 2
-    for (int c = first; c < last; ++c) mine += weights(c, w);
+    for (int i = 0; i < rounds; ++i) mine += weights(first + 32 * i, w);
     before = block_scan<kChoiceThreads>(mine, red, &all);
     if (tid == 0) my_total = all;
     cluster_sync_all();
@@ -998,14 +1031,28 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
   }
   // the first token whose running sum exceeds u * whole, i.e. floor(u * whole)
   const u64 goal = min(scaled_floor(p.uniform[static_cast<long long>(b) * (p.T + 1) + p.T], whole), whole - 1);
-  if (goal < before || goal >= before + mine) return;
-  for (int c = first; c < last; ++c) {
-    weights(c, w);
+  // the warp that has it (the sum before its first lane is that before all its chunks)
+  const u64 end = __shfl_sync(0xffffffffu, before + mine, 31);
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (goal < before || goal >= end) return;
+  for (int i = 0; i < rounds; ++i) {
+    const u64 sum = weights(first + 32 * i, w);
+    u64 inc = sum;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (before <= goal && goal < before + w[e]) p.next[b] = row.base + 8 * c + e;
-      before += w[e];
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
     }
+    u64 run = before + inc - sum;
+    if (run <= goal && goal < run + sum) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (run <= goal && goal < run + w[e]) p.next[b] = row.base + 8 * (first + 32 * i) + e;
+        run += w[e];
+      }
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+    if (goal < before) return;                    // the same for the whole warp
   }
 }
 
