@@ -217,8 +217,13 @@ __device__ __forceinline__ uint4 chunk_keys(const uint4 &c) {
   return make_uint4(order_key2(c.x), order_key2(c.y), order_key2(c.z), order_key2(c.w));
 }
 
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {   // of two pairs of 16 bits
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 // The larger of the upper keys and of the lower ones, side by side.
-__device__ __forceinline__ uint32_t chunk_max2(const uint4 &k) { return __vmaxu2(__vmaxu2(k.x, k.y), __vmaxu2(k.z, k.w)); }
+__device__ __forceinline__ uint32_t chunk_max2(const uint4 &k) { return max2(max2(k.x, k.y), max2(k.z, k.w)); }
 
 __device__ __forceinline__ float key_value(uint32_t key) {
   const uint32_t bits = (key & 0x8000u) ? key & 0x7fffu : ~key & 0xffffu;
@@ -293,6 +298,7 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
 }
 
 // ---------------------------------------------------------------- rows
+static_assert(kRowThreads == 1024 && kBinRows == 1024, "a warp for every 32nd row of values");
 struct RowSmem {
   unsigned hist[kBins];
   unsigned row_count[2 * kBinRows];  // tokens, and masses, of 32 neighbouring values, the largest first
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
           uint32_t top2 = 0;
 #pragma unroll
           for (int k = 0; k < kBatch; ++k)
-            if (c0 + k * kRowThreads < row.chunks) top2 = __vmaxu2(top2, chunk_max2(chunk_keys(w[k])));
+            if (c0 + k * kRowThreads < row.chunks) top2 = max2(top2, chunk_max2(chunk_keys(w[k])));
           return max(top2 & 0xffffu, top2 >> 16);
         });
       start = false;
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     uint32_t top2 = 0, from = 0;
     const uint32_t base = smem_u32(S.hist);
     for_chunks([&](int, const uint4 &k) {
-      top2 = __vmaxu2(top2, chunk_max2(k));
+      top2 = max2(top2, chunk_max2(k));
 #pragma unroll
       for (int e = 0; e < 8; ++e) count_packed(base, chunk_half(k, e), from, counted);
     }, [&](auto &&first_max) {
@@ -456,18 +462,17 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       S.row_mass[r] = ms;
     }
   };
-  // fn(word row, its word in this lane), rows without tokens left out
+  // fn(word row, its word in this lane), rows without tokens left out: a warp looks
+  // through its 32 rows first
   auto for_words = [&](auto &&fn) {
-    for (int r0 = warp; r0 < kBinRows; r0 += 8 * (kRowThreads / 32)) {
-      unsigned c[8];
+    const unsigned *mine = S.hist + kBins - 1 - (warp * 32 + lane);
+    uint32_t some = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) c[k] = S.hist[kBins - 1 - ((r0 + k * (kRowThreads / 32)) * 32 + lane)];
+    for (int k = 0; k < kBinRows / 32; ++k) some |= (__any_sync(0xffffffffu, mine[-k * kRowThreads] != 0) ? 1u : 0u) << k;
 #pragma unroll 1
-      for (int k = 0; k < 8; ++k) {
-        if (__any_sync(0xffffffffu, c[0] != 0)) fn(r0 + k * (kRowThreads / 32), c[0]);
-#pragma unroll
-        for (int i = 0; i < 7; ++i) c[i] = c[i + 1];
-      }
+    for (; some; some &= some - 1) {
+      const int k = __ffs(some) - 1;
+      fn(warp + 32 * k, mine[-k * kRowThreads]);
     }
   };
   auto clear_rows = [&](int half) {
@@ -723,7 +728,7 @@ __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const Verify
     S.found = 0x10000;
   }
   uint32_t top2 = 0;                              // two maxima side by side
-  for_chunks([&](int, const uint4 &k) { top2 = __vmaxu2(top2, chunk_max2(k)); });
+  for_chunks([&](int, const uint4 &k) { top2 = max2(top2, chunk_max2(k)); });
   const uint32_t my_max = max(top2 & 0xffffu, top2 >> 16);
   __syncthreads();
   const uint32_t warp_best = __reduce_max_sync(0xffffffffu, my_max);
