@@ -40,18 +40,26 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const Paged
     paged_combine_row<HD>(p, rows, c, n, r, weight[warp], paged_unit_row(p.o, p, s, mine.b, t0, mine.kvh, r));
 }
 
-template <int HD, bool FP8, int RT>
+template <int HD, bool FP8, int NR>
 cudaError_t launch_few(const PagedAttnParams &p, cudaStream_t st) {
-  using C = PdCfg<HD, FP8, RT>;
-  const cudaError_t e = ensure_smem_attr<paged_few_rows_kernel<HD, FP8, RT>>(C::SMEM);
+  using C = PdCfg<HD, FP8, NR>;
+  const cudaError_t e = ensure_smem_attr<paged_few_rows_kernel<HD, FP8, NR>>(C::SMEM);
   if (e != cudaSuccess) return e;
   PagedAttnParams q = p;
   q.bk_shift = C::BK_SHIFT;
   CUtensorMap tq, tk, tv;
   if (!paged_map_q(&tq, p) || !paged_map_pages(&tk, p.kv, p.kv.k, C::KC) || !paged_map_pages(&tv, p.kv, p.kv.v, C::KC))
     return cudaErrorInvalidValue;
-  paged_few_rows_kernel<HD, FP8, RT><<<p.ctas, C::THREADS, C::SMEM, st>>>(tq, tk, tv, q);
+  paged_few_rows_kernel<HD, FP8, NR><<<p.ctas, C::THREADS, C::SMEM, st>>>(tq, tk, tv, q);
   return cudaGetLastError();
+}
+
+template <int HD, bool FP8>
+cudaError_t launch_few(int rows, const PagedAttnParams &p, cudaStream_t st) {
+  return rows == 8    ? launch_few<HD, FP8, 1>(p, st)
+         : rows == 16 ? launch_few<HD, FP8, 2>(p, st)
+         : rows == 24 ? launch_few<HD, FP8, 3>(p, st)
+                      : launch_few<HD, FP8, 4>(p, st);
 }
 
 template <int HD>
@@ -91,7 +99,7 @@ bool paged_map_pages(CUtensorMap *map, const PagedKv &kv, const void *base, int 
 // Rows of a unit: the tile of the kernel that takes the call.
 static int unit_rows(int G, int T) {
   const long long r = (long long)T * G;
-  return r <= 16 ? 16 : r <= 32 ? 32 : r <= 128 ? 128 : 256;
+  return r <= 32 ? static_cast<int>((r + 7) / 8 * 8) : r <= 128 ? 128 : 256;
 }
 
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {
@@ -103,18 +111,16 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   p.ctas = min(sms, kPagedMaxCtas);
   const int rows = unit_rows(p.G, p.c.T);
   p.tt = rows / p.G;
-  const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64, one = rows == 16;
+  const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64;
   p.bk_shift = rows >= 128 || !(h64 || f8) ? 7 : 8;
   cudaError_t e;
   prof_before(SMOL_K_DEC_ATTN, st);
   if (rows >= 128) {
     e = launch_paged_tiles(p, st);
   } else if (h64) {
-    if (f8) e = one ? launch_few<64, true, 1>(p, st) : launch_few<64, true, 2>(p, st);
-    else e = one ? launch_few<64, false, 1>(p, st) : launch_few<64, false, 2>(p, st);
+    e = f8 ? launch_few<64, true>(rows, p, st) : launch_few<64, false>(rows, p, st);
   } else {
-    if (f8) e = one ? launch_few<128, true, 1>(p, st) : launch_few<128, true, 2>(p, st);
-    else e = one ? launch_few<128, false, 1>(p, st) : launch_few<128, false, 2>(p, st);
+    e = f8 ? launch_few<128, true>(rows, p, st) : launch_few<128, false>(rows, p, st);
   }
   prof_after(SMOL_K_DEC_ATTN, st);
   if (e != cudaSuccess) return e;

@@ -1,4 +1,4 @@
-// paged_decode.cuh - paged attention of few rows: up to 16 or 32 query rows
+// paged_decode.cuh - paged attention of few rows: up to 8, 16, 24 or 32 query rows
 // (tokens times heads of a kv head) share a sequence's keys.  Included by
 // paged_attention.cu.
 //
@@ -13,8 +13,14 @@
 //
 // mma.sync m16n8k16 (bf16, fp32 sums): a tcgen05 tile has 128 rows, of which 3 to
 // 32 would be used, and its score tile's trip through tensor memory is longer than
-// the whole step here.  The fragments of a step stay in registers; with 32 rows the
-// queries' are read from shared memory each time (they would spill).
+// the whole step here.  An instruction takes some 15 cycles of its quarter of the SM,
+// and with 32 query rows that is the time of a step, so the products are taken as
+// S^T = K Q^T and O^T = V^T P^T: keys and dims are the 16 rows, the queries the 8
+// columns, and 3 of them cost half of what they would as rows.  A lane then has two
+// query columns of eight, its own rows' maxima and sums, and P^T is turned by
+// movmatrix between the products.  The fragments of a step stay in registers; with
+// more than 16 rows the queries' are read from shared memory each time (they would
+// spill).
 //
 // e4m3 codes become bf16 exactly, by way of f16 and fp32: four cycles of the integer
 // pipe for a pair (shifting the bits into place took eight).
@@ -53,13 +59,14 @@ __device__ __forceinline__ uint4 pd_lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 pd_lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
-  return v;
+// The transpose of an 8x8 tile of 16-bit values.
+__device__ __forceinline__ uint32_t pd_turn(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
-template <int HD, bool FP8, int RT>
+template <int HD, bool FP8, int NR>
 struct PdCfg {
   static constexpr int NW = 8, THREADS = 32 * NW;
   static constexpr int KC = (HD == 128 && !FP8) ? 16 : 32;     // keys of a warp's step: 4 or 8 KB of K and V
@@ -68,23 +75,29 @@ struct PdCfg {
   static constexpr int SUB_BYTES = KC * ROWB;
   static constexpr int KV_BYTES = NSUB * SUB_BYTES;
   static constexpr int STAGE = 2 * KV_BYTES;
-  static constexpr int NS = STAGE == 4096 ? 5 : RT == 2 && HD == 128 ? 2 : 3;
+  static constexpr int NS = STAGE == 4096 ? 5 : NR > 2 && HD == 128 ? 2 : 3;
   static constexpr int BK_SHIFT = KC == 32 ? 8 : 7;            // keys of a tile: NW * KC
-  static constexpr int NT8 = KC / 8;                           // key columns of the score fragments
-  static constexpr int ND8 = HD / 8;
-  static constexpr bool Q_REGS = RT == 1;                      // the queries' fragments stay in registers
-  static constexpr int Q_BYTES = RT * 16 * HD * 2;             // [HD / 64][RT * 16 rows][64]
-  static constexpr int MERGE_WORDS = RT * (ND8 * 4 + 4);       // a thread's state
+  static constexpr int KT = KC / 16, DT = HD / 16;             // 16-row tiles of S^T and of O^T
+  static constexpr int ROWS = 8 * NR;
+  static constexpr bool Q_REGS = NR <= 2;                      // the queries' fragments stay in registers
+  static constexpr int Q_BYTES = ROWS * HD * 2;                // [HD / 64][ROWS][64]
+  static constexpr int STATE_BYTES = 32 * NR * (DT + 1) * 16;  // a warp's sums, maxima and row sums
   static constexpr int OFF_SC = NW * NS * STAGE;               // of each stage: scales of the keys, and of the values
   static constexpr int OFF_NOTE = OFF_SC + (FP8 ? NW * NS * 2 * KC * 4 : 0);
   static constexpr int OFF_Q = (OFF_NOTE + NW * NS * 64 + 1023) / 1024 * 1024;   // [2] this unit's and the next one's
-  static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;        // two warps' states at a time
-  static constexpr int MERGE_BYTES = 2 * 32 * MERGE_WORDS * 4;
-  static constexpr int OFF_BAR = OFF_MERGE + MERGE_BYTES;      // [NW][NS] stages, [2] Q
-  static constexpr int USED = OFF_BAR + (NW * NS + 2) * 8 + 16;
+  static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;        // some warps' states; then the unit's rows
+  static constexpr int BAR_BYTES = (NW * NS + 2) * 8 + 16;     // [NW][NS] stages, [2] Q
+  static constexpr int MERGE_WARPS = OFF_MERGE + 4 * STATE_BYTES + BAR_BYTES <= 232448 ? 4 : 2;
+  static constexpr int TILE_LD = HD + 4;                       // words of a row of the merged unit
+  static constexpr int TILE_BYTES = ROWS * (TILE_LD + 2) * 4;
+  static constexpr int SCHED_BYTES = 8 * kPagedMaxCtas * 4 + (int)sizeof(PagedSchedSmem);   // the parts' weights, and the schedule
+  static constexpr int MERGE_BYTES =
+      (MERGE_WARPS * STATE_BYTES > SCHED_BYTES ? MERGE_WARPS * STATE_BYTES : SCHED_BYTES) / 16 * 16 + 16;
+  static constexpr int OFF_BAR = OFF_MERGE + MERGE_BYTES;
+  static constexpr int USED = OFF_BAR + BAR_BYTES;
   static constexpr int SMEM = USED + 1008 <= 232448 ? USED + 1008 : 232448;
   static_assert(USED <= 232448, "shared memory per CTA");
-  static_assert(MERGE_BYTES >= 8 * kPagedMaxCtas * 4 + (int)sizeof(PagedSchedSmem), "room for the parts' weights, and the schedule");
+  static_assert(MERGE_BYTES >= TILE_BYTES, "room for the merged unit");
 };
 
 // A warp's note of a step, beside its keys.
@@ -102,12 +115,12 @@ static_assert(sizeof(PdNote) == 64, "note");
 enum : int { kPdFirst = 1, kPdEnds = 2, kPdLast = 4 };       // the unit's first tile here, its last tile, this CTA's last
 enum : int { kPdTimeout = 0x209 };
 
-template <int HD, bool FP8, int RT>
-__global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
+template <int HD, bool FP8, int NR>
+__global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
     paged_few_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                           const __grid_constant__ CUtensorMap tmV, const PagedAttnParams p) {
-  using C = PdCfg<HD, FP8, RT>;
-  constexpr int KC = C::KC, NS = C::NS, ND8 = C::ND8, NT8 = C::NT8, NSUB = C::NSUB;
+  using C = PdCfg<HD, FP8, NR>;
+  constexpr int KC = C::KC, KT = C::KT, DT = C::DT, NS = C::NS, NSUB = C::NSUB;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), cta = blockIdx.x;
@@ -157,7 +170,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
         mbar_arrive_expect_tx(bar, (HD / 64) * 128 * p.tt * p.G);
 #pragma unroll
         for (int sub = 0; sub < HD / 64; ++sub)
-          tma_load_4d(smem + C::OFF_Q + (nq & 1) * C::Q_BYTES + sub * (RT * 16 * 128), &tmQ, bar, sub * 64, qn.kvh * p.G,
+          tma_load_4d(smem + C::OFF_Q + (nq & 1) * C::Q_BYTES + sub * (C::ROWS * 128), &tmQ, bar, sub * 64, qn.kvh * p.G,
                       qn.s.row0 + qn.t0, p.c.row_start ? 0 : qn.b);
       }
       ++nq;
@@ -239,32 +252,41 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
 #pragma unroll
   for (int i = 0; i < NS - 1; ++i) produce();
 
-  // ---- state of the rows: row g8 + 8 i of m-tile rt
-  float o[RT][ND8][4], m[RT][2], l[RT][2];
-  [[maybe_unused]] uint32_t qf[RT][HD / 16][4];
+  // ---- state of the rows: this lane's are 8 nt + 2 c4 + i
+  float o[DT][NR][4], m[NR][2], l[NR][2];
+  [[maybe_unused]] uint32_t qf[NR][DT][2];
   uint32_t units = 0, phase = 0;
   int stage = 0;
-  // A fragments of k-step ks.  Codes: a lane's B fragments of four k-steps are 16
-  // neighbouring bytes of the key, so step s of group g takes the dims
+  // the queries' fragments of k-steps 2 k2 and 2 k2 + 1.  Codes: a lane's pieces of four
+  // k-steps are 16 neighbouring bytes of the key, so step s of group g takes the dims
   // 64 g + 16 c4 + 4 s .. + 3 there, and the queries' fragments the same.
-  auto load_a = [&](uint32_t q_s, int rt, int ks, uint32_t (&a)[4]) {
-    const uint32_t sub = q_s + (ks >> 2) * (RT * 16 * 128) + rt * (16 * 128);
+  auto load_q = [&](uint32_t q_s, int nt, int k2, uint32_t (&b)[4]) {
+    const uint32_t sub = q_s + (k2 >> 1) * (C::ROWS * 128) + nt * 1024;
     if constexpr (FP8) {
-      const int ch = 2 * c4 + ((ks & 3) >> 1);
-      const uint2 u = pd_lds64(sub + g8 * 128 + ((ch ^ g8) << 4) + (ks & 1) * 8);
-      const uint2 v = pd_lds64(sub + (g8 + 8) * 128 + ((ch ^ g8) << 4) + (ks & 1) * 8);
-      a[0] = u.x;
-      a[1] = v.x;
-      a[2] = u.y;
-      a[3] = v.y;
+      const uint4 v = pd_lds128(sub + g8 * 128 + (((2 * c4 + (k2 & 1)) ^ g8) << 4));
+      b[0] = v.x;
+      b[1] = v.y;
+      b[2] = v.z;
+      b[3] = v.w;
     } else {
-      pd_ldsm4(a, sub + (lane & 15) * 128 + ((((ks & 3) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
+      pd_ldsm4(b, sub + (lane & 7) * 128 + ((((k2 & 1) * 4 + (lane >> 3)) ^ (lane & 7)) << 4));
+    }
+  };
+  auto take_q = [&](uint32_t q_s, int k2, uint32_t (&b)[NR][4]) {
+#pragma unroll
+    for (int nt = 0; nt < NR; ++nt) {
+      if constexpr (C::Q_REGS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b[nt][e] = qf[nt][2 * k2 + (e >> 1)][e & 1];
+      } else {
+        load_q(q_s, nt, k2, b[nt]);
+      }
     }
   };
   // where this lane's pieces of the keys and values lie in a box (the boxes' swizzle:
   // 128-byte rows by the row's last three bits, 64-byte rows by its bits 1 and 2)
-  // codes of hd 128: fragment column n reads key (n >> 1) + 4 (n & 1) of eight, so that
-  // two rows' pieces meet different banks; the weights' columns follow
+  // codes of hd 128: fragment row n reads key (n >> 1) + 4 (n & 1) of eight, so that
+  // two rows' pieces meet different banks; the values' columns follow
   constexpr bool PERM = FP8 && HD == 128;
   auto key_of = [](int n) { return PERM ? (n & ~7) | ((n & 7) >> 1) | ((n & 1) << 2) : n; };
   while (true) {
@@ -289,21 +311,26 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
       }
       if constexpr (C::Q_REGS) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-          for (int ks = 0; ks < HD / 16; ++ks) load_a(q_s, rt, ks, qf[rt][ks]);
+          for (int k2 = 0; k2 < DT / 2; ++k2) {
+            uint32_t b[4];
+            load_q(q_s, nt, k2, b);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qf[nt][2 * k2 + (e >> 1)][e & 1] = b[e];
+          }
       }
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
+      for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          m[rt][i] = -INFINITY;
-          l[rt][i] = 0.f;
+          m[nt][i] = -INFINITY;
+          l[nt][i] = 0.f;
         }
 #pragma unroll
-        for (int d = 0; d < ND8; ++d)
+        for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[rt][d][e] = 0.f;
+          for (int e = 0; e < 4; ++e) o[d][nt][e] = 0.f;
       }
     }
     if (x0 < hi && x0 + KC > lo) {
@@ -320,290 +347,282 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
         fence_proxy_async_smem();                 // before the stage's next boxes
         __syncwarp();
       }
-      // ---- S = Q K^T
-      float s[RT][NT8][4];
+      // ---- S^T = K Q^T: key 16 t + g8 (+ 8 from element 2 on), row 8 nt + 2 c4 + (e & 1)
+      float s[KT][NR][4];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int t = 0; t < KT; ++t)
 #pragma unroll
-        for (int n = 0; n < NT8; ++n)
+        for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s[rt][n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) s[t][nt][e] = 0.f;
       if constexpr (FP8) {
 #pragma unroll
         for (int gr = 0; gr < HD / 64; ++gr) {
-          uint4 w[NT8];
+          uint4 w[2 * KT];
 #pragma unroll
-          for (int n = 0; n < NT8; ++n) {
+          for (int n = 0; n < 2 * KT; ++n) {
             const int key = n * 8 + key_of(g8);
             const uint32_t ch = gr * 4 + c4;
             w[n] = pd_lds128(k_s + key * C::ROWB + ((HD == 64 ? ch ^ ((key >> 1) & 3) : ch ^ (key & 7)) << 4));
           }
 #pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            uint32_t a[RT][4];
+          for (int k2 = 0; k2 < 2; ++k2) {
+            uint32_t b[NR][4];
+            take_q(q_s, gr * 2 + k2, b);
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              if constexpr (C::Q_REGS) {
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a[rt][e] = qf[rt][gr * 4 + q4][e];
-              } else {
-                load_a(q_s, rt, gr * 4 + q4, a[rt]);
+              for (int t = 0; t < KT; ++t) {
+                const int q4 = 2 * k2 + h;
+                uint32_t a[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  const uint4 &v = w[2 * t + n];
+                  const uint32_t u = q4 == 0 ? v.x : q4 == 1 ? v.y : q4 == 2 ? v.z : v.w;
+                  const float2 f0 = unpack_e4m3x2(u), f1 = unpack_e4m3x2(u >> 16);
+                  a[n] = pack_bf16x2(f0.x, f0.y);
+                  a[2 + n] = pack_bf16x2(f1.x, f1.y);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt) pd_mma(s[t][nt], a, b[nt][2 * h], b[nt][2 * h + 1]);
               }
-            }
-#pragma unroll
-            for (int n = 0; n < NT8; ++n) {
-              const uint32_t u = q4 == 0 ? w[n].x : q4 == 1 ? w[n].y : q4 == 2 ? w[n].z : w[n].w;
-              const float2 f0 = unpack_e4m3x2(u), f1 = unpack_e4m3x2(u >> 16);
-              const uint32_t b0 = pack_bf16x2(f0.x, f0.y), b1 = pack_bf16x2(f1.x, f1.y);
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) pd_mma(s[rt][n], a[rt], b0, b1);
-            }
           }
         }
       } else {
-        const uint32_t k_lane = k_s + (lane & 7) * 128 + (((lane >> 3) ^ (lane & 7)) << 4);
+        const uint32_t k_lane = k_s + (lane & 15) * 128;
 #pragma unroll
-        for (int k2 = 0; k2 < HD / 32; ++k2) {
-          uint32_t a[RT][2][4];
+        for (int k2 = 0; k2 < DT / 2; ++k2) {
+          uint32_t b[NR][4];
+          take_q(q_s, k2, b);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if constexpr (C::Q_REGS) {
+            for (int t = 0; t < KT; ++t) {
+              uint32_t a[4];
+              pd_ldsm4(a, k_lane + (k2 >> 1) * C::SUB_BYTES + t * 2048 + (((((k2 & 1) * 2 + h) * 2 + (lane >> 4)) ^ (lane & 7)) << 4));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) a[rt][h][e] = qf[rt][2 * k2 + h][e];
-              } else {
-                load_a(q_s, rt, 2 * k2 + h, a[rt][h]);
-              }
+              for (int nt = 0; nt < NR; ++nt) pd_mma(s[t][nt], a, b[nt][2 * h], b[nt][2 * h + 1]);
             }
-#pragma unroll
-          for (int n = 0; n < NT8; ++n) {
-            uint32_t b[4];
-            pd_ldsm4(b, (k_lane ^ ((k2 & 1) * 64)) + (k2 >> 1) * C::SUB_BYTES + n * 1024);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              pd_mma(s[rt][n], a[rt][0], b[0], b[1]);
-              pd_mma(s[rt][n], a[rt][1], b[2], b[3]);
-            }
-          }
         }
       }
       // ---- scores in the exp2 domain, replaced where a row does not see the key
       const bool edge = x0 + KC - 1 > first_at || x0 < lo || (p.window > 0 && x0 <= first_at + (rows - 1) / p.G - p.window);
+      if constexpr (FP8) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if constexpr (FP8) {
+        for (int t = 0; t < KT; ++t) {
+          const float k0 = scales[t * 16 + key_of(g8)] * p.scale_log2, k1 = scales[t * 16 + 8 + key_of(g8)] * p.scale_log2;
 #pragma unroll
-          for (int n = 0; n < NT8; ++n) {
-            const float k0 = scales[n * 8 + key_of(2 * c4)] * p.scale_log2, k1 = scales[n * 8 + key_of(2 * c4 + 1)] * p.scale_log2;
-            s[rt][n][0] *= k0;
-            s[rt][n][1] *= k1;
-            s[rt][n][2] *= k0;
-            s[rt][n][3] *= k1;
+          for (int nt = 0; nt < NR; ++nt) {
+            s[t][nt][0] *= k0;
+            s[t][nt][1] *= k0;
+            s[t][nt][2] *= k1;
+            s[t][nt][3] *= k1;
           }
         }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt) {
         if (edge) {
           int own[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) own[i] = first_at + (rt * 16 + g8 + 8 * i) / p.G;   // past the unit's rows: not written
+          for (int i = 0; i < 2; ++i) own[i] = first_at + (nt * 8 + 2 * c4 + i) / p.G;   // past the unit's rows: not written
 #pragma unroll
-          for (int n = 0; n < NT8; ++n)
+          for (int t = 0; t < KT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int x = x0 + n * 8 + key_of(2 * c4 + (e & 1));
-              if (x > own[e >> 1] || (p.window > 0 && x <= own[e >> 1] - p.window)) s[rt][n][e] = -INFINITY;
+              const int x = x0 + t * 16 + (e >> 1) * 8 + key_of(g8);
+              if (x > own[e & 1] || (p.window > 0 && x <= own[e & 1] - p.window)) s[t][nt][e] = -INFINITY;
             }
         }
         float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int n = 0; n < NT8; ++n) {
-          mx[0] = fmax3(mx[0], s[rt][n][0], s[rt][n][1]);
-          mx[1] = fmax3(mx[1], s[rt][n][2], s[rt][n][3]);
+        for (int t = 0; t < KT; ++t) {
+          mx[0] = fmax3(mx[0], s[t][nt][0], s[t][nt][2]);
+          mx[1] = fmax3(mx[1], s[t][nt][1], s[t][nt][3]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-          mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], x));
           if (!FP8) mx[i] *= p.scale_log2;        // scale > 0; -inf stays -inf
         }
-        if (__any_sync(0xffffffffu, mx[0] > m[rt][0] || mx[1] > m[rt][1])) {
+        if (__any_sync(0xffffffffu, mx[0] > m[nt][0] || mx[1] > m[nt][1])) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float mn = fmaxf(m[rt][i], mx[i]);
-            const float a = mn == -INFINITY ? 1.f : ex2_approx(m[rt][i] - mn);
-            m[rt][i] = mn;
-            l[rt][i] *= a;
+            const float mn = fmaxf(m[nt][i], mx[i]);
+            const float a = mn == -INFINITY ? 1.f : ex2_approx(m[nt][i] - mn);
+            m[nt][i] = mn;
+            l[nt][i] *= a;
 #pragma unroll
-            for (int d = 0; d < ND8; ++d) {
-              o[rt][d][2 * i] *= a;
-              o[rt][d][2 * i + 1] *= a;
+            for (int d = 0; d < DT; ++d) {
+              o[d][nt][i] *= a;
+              o[d][nt][2 + i] *= a;
             }
           }
         }
+        const float mu0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0], mu1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        float2 sum = make_float2(l[nt][0], l[nt][1]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float mu = m[rt][i] == -INFINITY ? 0.f : m[rt][i];
-          float2 sum = make_float2(0.f, 0.f);
+        for (int t = 0; t < KT; ++t)
 #pragma unroll
-          for (int n = 0; n < NT8; ++n) {
+          for (int h = 0; h < 2; ++h) {
+            float &f0 = s[t][nt][2 * h], &f1 = s[t][nt][2 * h + 1];
             float2 x;
-            if constexpr (FP8) x = fadd2(s[rt][n][2 * i], s[rt][n][2 * i + 1], -mu, -mu);
-            else x = ffma2(s[rt][n][2 * i], s[rt][n][2 * i + 1], p.scale_log2, -mu);
-            x.x = ex2_approx(x.x);
-            x.y = ex2_approx(x.y);
-            sum = fadd2(sum.x, sum.y, x.x, x.y);
-            s[rt][n][2 * i] = x.x;
-            s[rt][n][2 * i + 1] = x.y;
+            if constexpr (FP8) x = fadd2(f0, f1, -mu0, -mu1);
+            else x = make_float2(fmaf(f0, p.scale_log2, -mu0), fmaf(f1, p.scale_log2, -mu1));
+            f0 = ex2_approx(x.x);
+            f1 = ex2_approx(x.y);
+            sum = fadd2(sum.x, sum.y, f0, f1);
           }
-          l[rt][i] += sum.x + sum.y;
-        }
+        l[nt][0] = sum.x;
+        l[nt][1] = sum.y;
       }
-      // ---- O += P V; P rounded to bf16, the tensor core's operand type
+      // ---- O^T += V^T P^T; P rounded to bf16, the tensor core's operand type
 #pragma unroll
-      for (int k16 = 0; k16 < KC / 16; ++k16) {
-        uint32_t a[RT][4];
-        float2 vs0 = make_float2(1.f, 1.f), vs1 = vs0;
+      for (int t = 0; t < KT; ++t) {
+        uint32_t b[NR][2];
+        float v0 = 1.f, v1 = 1.f;
         if constexpr (FP8) {
-          vs0 = make_float2(scales[KC + k16 * 16 + key_of(2 * c4)], scales[KC + k16 * 16 + key_of(2 * c4 + 1)]);
-          vs1 = make_float2(scales[KC + k16 * 16 + 8 + key_of(2 * c4)], scales[KC + k16 * 16 + 8 + key_of(2 * c4 + 1)]);
+          v0 = scales[KC + t * 16 + key_of(g8)];
+          v1 = scales[KC + t * 16 + 8 + key_of(g8)];
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const float(&f)[4] = s[rt][2 * k16], (&g)[4] = s[rt][2 * k16 + 1];
-          a[rt][0] = pack_bf16x2(f[0] * vs0.x, f[1] * vs0.y);
-          a[rt][1] = pack_bf16x2(f[2] * vs0.x, f[3] * vs0.y);
-          a[rt][2] = pack_bf16x2(g[0] * vs1.x, g[1] * vs1.y);
-          a[rt][3] = pack_bf16x2(g[2] * vs1.x, g[3] * vs1.y);
+        for (int nt = 0; nt < NR; ++nt) {
+          b[nt][0] = pd_turn(pack_bf16x2(s[t][nt][0] * v0, s[t][nt][1] * v0));
+          b[nt][1] = pd_turn(pack_bf16x2(s[t][nt][2] * v1, s[t][nt][3] * v1));
         }
         if constexpr (FP8) {
-          // a transposed load gives pairs of neighbouring dims: the even dims of 16 go
-          // to one accumulator column block, the odd ones to the next
-          const int key = k16 * 16 + key_of(lane & 15);
+          // a transposed load gives pairs of neighbouring dims: the even dims of 16 are a
+          // tile's rows 0 .. 7, the odd ones its rows 8 .. 15
+          const int key = t * 16 + key_of(lane & 15);
           const uint32_t row = v_s + key * C::ROWB;
 #pragma unroll
-          for (int c2 = 0; c2 < HD / 32; ++c2) {
-            uint32_t b[4];
+          for (int c2 = 0; c2 < DT / 2; ++c2) {
+            uint32_t u[4];
             const uint32_t ch = 2 * c2 + (lane >> 4);
-            pd_ldsm4_t(b, row + ((HD == 64 ? ch ^ ((key >> 1) & 3) : ch ^ (key & 7)) << 4));
+            pd_ldsm4_t(u, row + ((HD == 64 ? ch ^ ((key >> 1) & 3) : ch ^ (key & 7)) << 4));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float2 p0 = unpack_e4m3x2(b[2 * h]), p1 = unpack_e4m3x2(b[2 * h] >> 16);
-              const float2 p2 = unpack_e4m3x2(b[2 * h + 1]), p3 = unpack_e4m3x2(b[2 * h + 1] >> 16);
-              const uint32_t e0 = pack_bf16x2(p0.x, p1.x), e1 = pack_bf16x2(p2.x, p3.x);
-              const uint32_t d0 = pack_bf16x2(p0.y, p1.y), d1 = pack_bf16x2(p2.y, p3.y);
+              const float2 p0 = unpack_e4m3x2(u[2 * h]), p1 = unpack_e4m3x2(u[2 * h] >> 16);
+              const float2 p2 = unpack_e4m3x2(u[2 * h + 1]), p3 = unpack_e4m3x2(u[2 * h + 1] >> 16);
+              const uint32_t a[4] = {pack_bf16x2(p0.x, p1.x), pack_bf16x2(p0.y, p1.y), pack_bf16x2(p2.x, p3.x),
+                                     pack_bf16x2(p2.y, p3.y)};
 #pragma unroll
-              for (int rt = 0; rt < RT; ++rt) {
-                pd_mma(o[rt][4 * c2 + 2 * h], a[rt], e0, e1);
-                pd_mma(o[rt][4 * c2 + 2 * h + 1], a[rt], d0, d1);
-              }
+              for (int nt = 0; nt < NR; ++nt) pd_mma(o[2 * c2 + h][nt], a, b[nt][0], b[nt][1]);
             }
           }
         } else {
-          const uint32_t v_lane = v_s + k16 * 2048 + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
+          const uint32_t v_lane = v_s + t * 2048 + (lane & 15) * 128 + (((lane >> 4) ^ (lane & 7)) << 4);
 #pragma unroll
-          for (int c2 = 0; c2 < HD / 16; ++c2) {
-            uint32_t b[4];
-            pd_ldsm4_t(b, (v_lane ^ ((c2 & 3) * 32)) + (c2 >> 2) * C::SUB_BYTES);
+          for (int d = 0; d < DT; ++d) {
+            uint32_t u[4];
+            pd_ldsm4_t(u, (v_lane ^ ((d & 3) * 32)) + (d >> 2) * C::SUB_BYTES);
+            const uint32_t a[4] = {u[0], u[2], u[1], u[3]};
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-              pd_mma(o[rt][2 * c2], a[rt], b[0], b[1]);
-              pd_mma(o[rt][2 * c2 + 1], a[rt], b[2], b[3]);
-            }
+            for (int nt = 0; nt < NR; ++nt) pd_mma(o[d][nt], a, b[nt][0], b[nt][1]);
           }
         }
       }
     }
     if (flags & (kPdEnds | kPdLast)) {
-      // ---- the unit, or this CTA's part of it, is done: merge the warps' states: 4, 5
-      // into 0, 1; 6, 7 into 2, 3; 2, 3 into 0, 1; 1 into 0
+      // ---- the unit, or this CTA's part of it, is done: merge the warps' states, those of
+      // MERGE_WARPS warps at a time: 4 .. 7 into 0 .. 3, 2 and 3 into 0 and 1, 1 into 0
       const PdNote u = *note;
       const bool in_unit = units == 0 && started_inside, whole = (flags & kPdEnds) && !in_unit;
       PagedSeq us{};
       us.row0 = u.row0;
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
+      for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          l[rt][i] += __shfl_xor_sync(0xffffffffu, l[rt][i], 1);
-          l[rt][i] += __shfl_xor_sync(0xffffffffu, l[rt][i], 2);
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], x);
 #pragma unroll 1
-      for (int step = 0; step < 4; ++step) {
-        const int from = step == 0 ? 4 : step == 1 ? 6 : step == 2 ? 2 : 1, to = step == 1 ? 2 : 0, n = step == 3 ? 1 : 2;
-        if (warp >= from && warp < from + n) {
-          float4 *dst = reinterpret_cast<float4 *>(merge + (warp - from) * 32 * C::MERGE_WORDS) + lane;
+      for (int half = 4; half; half >>= 1) {
+#pragma unroll 1
+        for (int to = 0; to < half; to += C::MERGE_WARPS) {
+          const int from = half + to, n = min(half, C::MERGE_WARPS);
+          if (warp >= from && warp < from + n) {
+            float4 *dst = reinterpret_cast<float4 *>(smem + C::OFF_MERGE + (warp - from) * C::STATE_BYTES) + lane;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
+            for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
-            for (int d = 0; d < ND8; ++d)
-              dst[(rt * (ND8 + 1) + d) * 32] = make_float4(o[rt][d][0], o[rt][d][1], o[rt][d][2], o[rt][d][3]);
-            dst[(rt * (ND8 + 1) + ND8) * 32] = make_float4(m[rt][0], m[rt][1], l[rt][0], l[rt][1]);
-          }
-        }
-        __syncthreads();
-        if (warp >= to && warp < to + n) {
-          const float4 *src = reinterpret_cast<const float4 *>(merge + (warp - to) * 32 * C::MERGE_WORDS) + lane;
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const float4 other = src[(rt * (ND8 + 1) + ND8) * 32];
-            const float m2[2] = {other.x, other.y}, l2[2] = {other.z, other.w};
-            float a[2], a2[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float mn = fmaxf(m[rt][i], m2[i]);
-              a[i] = mn == -INFINITY ? 1.f : ex2_approx(m[rt][i] - mn);
-              a2[i] = mn == -INFINITY ? 1.f : ex2_approx(m2[i] - mn);
-              m[rt][i] = mn;
-              l[rt][i] = l[rt][i] * a[i] + l2[i] * a2[i];
-            }
-#pragma unroll
-            for (int d = 0; d < ND8; ++d) {
-              const float4 v = src[(rt * (ND8 + 1) + d) * 32];
-              o[rt][d][0] = o[rt][d][0] * a[0] + v.x * a2[0];
-              o[rt][d][1] = o[rt][d][1] * a[0] + v.y * a2[0];
-              o[rt][d][2] = o[rt][d][2] * a[1] + v.z * a2[1];
-              o[rt][d][3] = o[rt][d][3] * a[1] + v.w * a2[1];
+              for (int d = 0; d < DT; ++d)
+                dst[(nt * (DT + 1) + d) * 32] = make_float4(o[d][nt][0], o[d][nt][1], o[d][nt][2], o[d][nt][3]);
+              dst[(nt * (DT + 1) + DT) * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
             }
           }
-        }
-        __syncthreads();
-      }
-      if (warp == 0) {
-        float *part = paged_part(p.ws, cta, in_unit ? 0 : 1, RT * 16, HD);
+          __syncthreads();
+          if (warp >= to && warp < to + n) {
+            const float4 *src = reinterpret_cast<const float4 *>(smem + C::OFF_MERGE + (warp - to) * C::STATE_BYTES) + lane;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+            for (int nt = 0; nt < NR; ++nt) {
+              const float4 other = src[(nt * (DT + 1) + DT) * 32];
+              const float m2[2] = {other.x, other.y}, l2[2] = {other.z, other.w};
+              float a[2], a2[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = rt * 16 + g8 + 8 * i;
-            if (r >= rows) continue;
-            const float inv = l[rt][i] > 0.f ? 1.f / l[rt][i] : 0.f;
-            const long long out = whole ? paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r) : 0;
-            float *row = part + r * HD;
+              for (int i = 0; i < 2; ++i) {
+                const float mn = fmaxf(m[nt][i], m2[i]);
+                a[i] = mn == -INFINITY ? 1.f : ex2_approx(m[nt][i] - mn);
+                a2[i] = mn == -INFINITY ? 1.f : ex2_approx(m2[i] - mn);
+                m[nt][i] = mn;
+                l[nt][i] = l[nt][i] * a[i] + l2[i] * a2[i];
+              }
 #pragma unroll
-            for (int d = 0; d < ND8; ++d) {
-              const float x = o[rt][d][2 * i], y = o[rt][d][2 * i + 1];
-              if constexpr (FP8) {
-                if (d & 1) continue;
-                const float x1 = o[rt][d + 1][2 * i], y1 = o[rt][d + 1][2 * i + 1];   // the odd dims
-                const int dim = d * 8 + 4 * c4;
-                if (whole)
-                  *reinterpret_cast<uint2 *>(p.o.data + (out + dim) * 2) =
-                      p.o_f16 ? make_uint2(pack_f16x2(x * inv, x1 * inv), pack_f16x2(y * inv, y1 * inv))
-                              : make_uint2(pack_bf16x2(x * inv, x1 * inv), pack_bf16x2(y * inv, y1 * inv));
-                else
-                  __stcg(reinterpret_cast<float4 *>(row + dim), make_float4(x, x1, y, y1));
-              } else {
-                const int dim = d * 8 + 2 * c4;
-                if (whole)
-                  *reinterpret_cast<uint32_t *>(p.o.data + (out + dim) * 2) =
-                      p.o_f16 ? pack_f16x2(x * inv, y * inv) : pack_bf16x2(x * inv, y * inv);
-                else
-                  __stcg(reinterpret_cast<float2 *>(row + dim), make_float2(x, y));
+              for (int d = 0; d < DT; ++d) {
+                const float4 v = src[(nt * (DT + 1) + d) * 32];
+                o[d][nt][0] = o[d][nt][0] * a[0] + v.x * a2[0];
+                o[d][nt][1] = o[d][nt][1] * a[1] + v.y * a2[1];
+                o[d][nt][2] = o[d][nt][2] * a[0] + v.z * a2[0];
+                o[d][nt][3] = o[d][nt][3] * a[1] + v.w * a2[1];
               }
             }
-            if (!whole && c4 == 0) __stcg(reinterpret_cast<float2 *>(part + RT * 16 * HD + 2 * r), make_float2(m[rt][i], l[rt][i]));
+          }
+          __syncthreads();
+        }
+      }
+      // ---- the rows through shared memory, then a warp for each
+      float2 *ml = reinterpret_cast<float2 *>(merge + C::ROWS * C::TILE_LD);
+      if (warp == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = nt * 8 + 2 * c4 + i;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              float *to = merge + r * C::TILE_LD + d * 16 + (FP8 ? 2 * g8 : g8);
+              to[0] = o[d][nt][i];
+              to[FP8 ? 1 : 8] = o[d][nt][2 + i];
+            }
+            if (g8 == 0) ml[r] = make_float2(m[nt][i], l[nt][i]);
           }
       }
+      __syncthreads();
+      float *part = paged_part(p.ws, cta, in_unit ? 0 : 1, C::ROWS, HD);
+      for (int r = warp; r < rows; r += C::NW) {
+        const float *row = merge + r * C::TILE_LD + lane * (HD / 32);
+        const float2 st = ml[r];
+        const float inv = st.y > 0.f ? 1.f / st.y : 0.f;
+        uint8_t *to = p.o.data + 2 * (whole ? paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r) + lane * (HD / 32) : 0);
+        if constexpr (HD == 64) {
+          const float2 v = *reinterpret_cast<const float2 *>(row);
+          if (whole)
+            *reinterpret_cast<uint32_t *>(to) = p.o_f16 ? pack_f16x2(v.x * inv, v.y * inv) : pack_bf16x2(v.x * inv, v.y * inv);
+          else
+            __stcg(reinterpret_cast<float2 *>(part + r * HD) + lane, v);
+        } else {
+          const float4 v = *reinterpret_cast<const float4 *>(row);
+          if (whole)
+            *reinterpret_cast<uint2 *>(to) =
+                p.o_f16 ? make_uint2(pack_f16x2(v.x * inv, v.y * inv), pack_f16x2(v.z * inv, v.w * inv))
+                        : make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
+          else
+            __stcg(reinterpret_cast<float4 *>(part + r * HD) + lane, v);
+        }
+        if (!whole && lane == 0) __stcg(reinterpret_cast<float2 *>(part + C::ROWS * HD + 2 * r), st);
+      }
+      if (whole) __syncthreads();                 // before the next unit's states
       if (!whole) {
         // ---- the CTA that brings a unit's last part combines them all
         __threadfence();
@@ -622,7 +641,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, RT>::THREADS, 1)
           __threadfence();
           float *weight = merge + warp * kPagedMaxCtas;
           for (int r = warp; r < rows; r += C::NW)
-            paged_combine_row<HD>(p, RT * 16, c0, n, r, weight, paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r));
+            paged_combine_row<HD>(p, C::ROWS, c0, n, r, weight, paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r));
           __syncthreads();
         }
       }
