@@ -6,6 +6,8 @@
 // j <= p, j > p - window, p = L + t.
 #include <math.h>
 
+#include <algorithm>
+
 #include "paged_decode.cuh"
 #include "profile.cuh"
 
@@ -54,12 +56,20 @@ cudaError_t launch_few(const PagedAttnParams &p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// The most rows that the few-rows kernel takes as one unit (32 sequences of 2000 to 8191
+// cached tokens, by it and by the many-rows kernel): bf16 of hd 64 24 rows 43 and 48 us,
+// 30 rows 50 and 48; of hd 128 16 rows 68 and 71, 20 rows 84 and 71; e4m3 of hd 128 20
+// rows 75 and 157, of hd 64 27 rows 51 and 90.
+constexpr int few_rows_most(int hd, bool e4m3) { return e4m3 ? 32 : hd == 64 ? 24 : 16; }
+
 template <int HD, bool FP8>
 cudaError_t launch_few(int rows, const PagedAttnParams &p, cudaStream_t st) {
-  return rows == 8    ? launch_few<HD, FP8, 1>(p, st)
-         : rows == 16 ? launch_few<HD, FP8, 2>(p, st)
-         : rows == 24 ? launch_few<HD, FP8, 3>(p, st)
-                      : launch_few<HD, FP8, 4>(p, st);
+  constexpr int most = few_rows_most(HD, FP8);
+  if constexpr (most >= 32)
+    if (rows > 24) return launch_few<HD, FP8, 4>(p, st);
+  if constexpr (most >= 24)
+    if (rows > 16) return launch_few<HD, FP8, 3>(p, st);
+  return rows > 8 ? launch_few<HD, FP8, 2>(p, st) : launch_few<HD, FP8, 1>(p, st);
 }
 
 template <int HD>
@@ -96,20 +106,25 @@ bool paged_map_pages(CUtensorMap *map, const PagedKv &kv, const void *base, int 
   return make_tmap_nd(map, base, kv.e4m3 ? 1 : 2, 3, d, s, b, kv.e4m3 && kv.hd == 64 ? 64 : 128);
 }
 
-// Rows of a unit: the tile of the kernel that takes the call.
-static int unit_rows(int G, int T) {
+// Rows of a unit: the tile of the kernel that takes the call.  e4m3 chunks of up to 48
+// rows go to the few-rows kernel in two halves, which read the same keys (4 heads, 9
+// tokens: 129 us, by the many-rows kernel 157; 3 heads, 16 tokens 72 and 91; of 64 rows
+// 192 and 162).
+static int unit_rows(int G, int T, int hd, bool e4m3) {
   const long long r = (long long)T * G;
-  return r <= 32 ? static_cast<int>((r + 7) / 8 * 8) : r <= 128 ? 128 : 256;
+  if (r <= few_rows_most(hd, e4m3)) return static_cast<int>((r + 7) / 8 * 8);
+  if (e4m3 && r <= 48 && (T + 1) / 2 * G <= 24) return unit_rows(G, (T + 1) / 2, hd, true);
+  return r <= 128 ? 128 : 256;
 }
 
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T) {
-  return kPagedPartOff + (size_t)kPagedMaxCtas * 2 * unit_rows(H / KV, T) * (hd + 2) * sizeof(float);
+  return kPagedPartOff + (size_t)kPagedMaxCtas * 2 * std::max(unit_rows(H / KV, T, hd, false), unit_rows(H / KV, T, hd, true)) * (hd + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStream_t st, int *launches) {
   PagedAttnParams p = p0;
   p.ctas = min(sms, kPagedMaxCtas);
-  const int rows = unit_rows(p.G, p.c.T);
+  const int rows = unit_rows(p.G, p.c.T, p.kv.hd, p.kv.e4m3);
   p.tt = rows / p.G;
   const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64;
   p.bk_shift = rows >= 128 || !(h64 || f8) ? 7 : 8;

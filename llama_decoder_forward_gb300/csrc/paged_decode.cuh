@@ -75,7 +75,7 @@ struct PdCfg {
   static constexpr int SUB_BYTES = KC * ROWB;
   static constexpr int KV_BYTES = NSUB * SUB_BYTES;
   static constexpr int STAGE = 2 * KV_BYTES;
-  static constexpr int NS = STAGE == 4096 ? 5 : NR > 2 && HD == 128 ? 2 : 3;
+  static constexpr int NS = STAGE == 4096 ? 5 : NR > 2 && HD == 128 ? 2 : 3;   // by shared memory
   static constexpr int BK_SHIFT = KC == 32 ? 8 : 7;            // keys of a tile: NW * KC
   static constexpr int KT = KC / 16, DT = HD / 16;             // 16-row tiles of S^T and of O^T
   static constexpr int ROWS = 8 * NR;
