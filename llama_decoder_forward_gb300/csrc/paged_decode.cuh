@@ -624,21 +624,24 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
       }
       if (whole) __syncthreads();                 // before the next unit's states
       if (!whole) {
-        // ---- the CTA that brings a unit's last part combines them all
-        __threadfence();
+        // ---- the CTA that brings a unit's last part combines them all.  The barriers
+        // around make thread 0's fences stand for the whole CTA's parts.
         __syncthreads();
         if (tid == 0) {
           const int c0 = paged_worker_of(u.u0, total, workers), n = paged_worker_of(u.u0 + u.j01 - 1, total, workers) - c0 + 1;
           int *count = reinterpret_cast<int *>(p.ws + kPagedCountOff) + c0;
+          __threadfence();
           const bool mine = atomicAdd(count, 1) == n - 1;
-          if (mine) atomicExch(count, 0);         // for the next call
+          if (mine) {
+            __threadfence();
+            atomicExch(count, 0);                 // for the next call
+          }
           s_parts[0] = c0;
           s_parts[1] = mine ? n : 0;
         }
         __syncthreads();
         const int c0 = s_parts[0], n = s_parts[1];
         if (n > 0) {
-          __threadfence();
           float *weight = merge + warp * kPagedMaxCtas;
           for (int r = warp; r < rows; r += C::NW)
             paged_combine_row<HD>(p, C::ROWS, c0, n, r, weight, paged_unit_row(p.o, p, us, u.b, u.t0, u.kvh, r));
