@@ -277,11 +277,6 @@ __device__ __forceinline__ void cp_async16(void *smem, const void *gmem, bool va
                "r"(sz)
                : "memory");
 }
-// The same for 4 bytes.
-__device__ __forceinline__ void cp_async4(void *smem, const void *gmem, bool valid) {
-  const int sz = valid ? 4 : 0;
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(smem)), "l"(gmem), "r"(sz) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
