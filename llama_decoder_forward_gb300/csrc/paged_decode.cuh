@@ -2,25 +2,32 @@
 // (tokens times heads of a kv head) share a sequence's keys.  Included by
 // paged_attention.cu.
 //
-// Bound by memory: every key and value is read once for at most 32 rows.  What
-// counts is bytes in flight, so each of the CTA's eight warps runs by itself: its
-// own ring of stages in shared memory, filled by TMA boxes that one lane asks for
-// (a box for each page), and its own running maximum, sum and accumulator over an
-// eighth of each key tile.  No barrier of the CTA is met until a unit ends; then the
-// eight states are merged through shared memory, two at a time.  A unit that
-// several CTAs share is finished by the one that comes last: it combines all their
-// parts, in the CTAs' order (the same bits every time).
+// Every key and value is read once for at most 32 rows, so bytes in flight count:
+// each of the CTA's eight warps runs by itself, with its own ring of stages in shared
+// memory, filled by TMA boxes that one lane asks for (a box for each page), and its own
+// running maximum, sum and accumulator over an eighth of each key tile.  No barrier of
+// the CTA is met until a unit ends; then the eight states are merged through shared
+// memory, two or four at a time.  A unit that several CTAs share is finished by the one
+// that comes last: it combines all their parts, in the CTAs' order (the same bits every
+// time).
+//
+// 64 sequences of one token on 1024 to 4096 cached ones, hd 64, 3 heads each (126 MB):
+// 29.4 us, 4.3 TB/s.  Of a CTA's 48,000 cycles 6,500 pass before its first key, 28,000
+// in 13 steps, 14,000 at the ends of two units.  e4m3, hd 128, 20 rows, 32 sequences
+// (171 MB): 74 us, bound by the steps (4,700 cycles for 32 keys of each warp).
 //
 // mma.sync m16n8k16 (bf16, fp32 sums): a tcgen05 tile has 128 rows, of which 3 to
 // 32 would be used, and its score tile's trip through tensor memory is longer than
-// the whole step here.  An instruction takes some 15 cycles of its quarter of the SM,
-// and with 32 query rows that is the time of a step, so the products are taken as
-// S^T = K Q^T and O^T = V^T P^T: keys and dims are the 16 rows, the queries the 8
-// columns, and 3 of them cost half of what they would as rows.  A lane then has two
-// query columns of eight, its own rows' maxima and sums, and P^T is turned by
-// movmatrix between the products.  The fragments of a step stay in registers; with
-// more than 16 rows the queries' are read from shared memory each time (they would
-// spill).
+// the whole step here.  The products are taken as S^T = K Q^T and O^T = V^T P^T: keys
+// and dims are the 16 rows of an instruction, the queries its 8 columns, and 3 of them
+// cost half of what they would as rows.  With two warps in a quarter of the SM a step
+// is a chain of waits for results (the tensor pipe is busy 5 to 20 % of the time), so
+// fewer instructions count, and large steps: half the keys in each of 16 warps took
+// longer (e4m3, 32 sequences of 2000 to 8191 tokens, hd 64: 36 us, 64 keys in each of
+// eight 30, 32 keys 33).  A lane has two query columns of eight, its own rows' maxima
+// and sums, and P^T is turned by movmatrix between the products.  The fragments of a
+// step stay in registers; with more than 16 rows the queries' are read from shared
+// memory each time (they would spill).
 //
 // e4m3 codes become bf16 exactly, by way of f16 and fp32: four cycles of the integer
 // pipe for a pair (shifting the bits into place took eight).
@@ -69,14 +76,14 @@ __device__ __forceinline__ uint32_t pd_turn(uint32_t v) {
 template <int HD, bool FP8, int NR>
 struct PdCfg {
   static constexpr int NW = 8, THREADS = 32 * NW;
-  static constexpr int KC = (HD == 128 && !FP8) ? 16 : 32;     // keys of a warp's step: 4 or 8 KB of K and V
+  static constexpr int KC = HD == 128 ? (FP8 ? 32 : 16) : FP8 && NR <= 2 ? 64 : 32;   // keys of a warp's step: 4 or 8 KB of K and V
   static constexpr int NSUB = FP8 ? 1 : HD / 64;               // boxes across a key (128 bytes each, or 64)
   static constexpr int ROWB = FP8 ? HD : 128;                  // bytes of a key in a box
   static constexpr int SUB_BYTES = KC * ROWB;
   static constexpr int KV_BYTES = NSUB * SUB_BYTES;
   static constexpr int STAGE = 2 * KV_BYTES;
   static constexpr int NS = STAGE == 4096 ? 5 : NR > 2 && HD == 128 ? 2 : 3;   // by shared memory
-  static constexpr int BK_SHIFT = KC == 32 ? 8 : 7;            // keys of a tile: NW * KC
+  static constexpr int BK_SHIFT = KC == 64 ? 9 : KC == 32 ? 8 : 7;   // keys of a tile: NW * KC
   static constexpr int KT = KC / 16, DT = HD / 16;             // 16-row tiles of S^T and of O^T
   static constexpr int ROWS = 8 * NR;
   static constexpr bool Q_REGS = NR <= 2;                      // the queries' fragments stay in registers
@@ -338,7 +345,9 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
       float *scales = ring_sc + stage * 2 * KC;
       if (x0 < lo || x0 + KC > hi) {
         // keys out of sight: their values (and the values' scales) become zeros
-        if (FP8 && lane < KC && (x0 + lane < lo || x0 + lane >= hi)) scales[KC + lane] = 0.f;
+        if (FP8)
+          for (int i = lane; i < KC; i += 32)
+            if (x0 + i < lo || x0 + i >= hi) scales[KC + i] = 0.f;
         for (int i = lane; i < C::KV_BYTES / 16; i += 32) {
           const int key = i / (C::ROWB / 16) % KC;
           if (x0 + key < lo || x0 + key >= hi)
