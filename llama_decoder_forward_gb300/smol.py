@@ -505,6 +505,14 @@ def _same_place(cache: PagedCache, chunk: Chunk) -> None:
         raise ValueError(f"{chunk.B} sequences, and {cache.n_seqs} rows of the page table")
 
 
+def _here(*tensors) -> None:
+    """All on the current device, where the call is going to run."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("every tensor must be on the current device")
+
+
 def _paged_copy(fn, where, cache, chunk, k, v, names, stream):
     _same_place(cache, chunk)
     kr = _rows(k, names[0], cache, chunk, cache.n_kv_heads, 1)
@@ -566,6 +574,7 @@ def prefill_paged(cfg: Config, packed: torch.Tensor, ids: torch.Tensor, cache: P
     _dev(logits, torch.bfloat16, "logits")
     if pos.shape != (B,) or logits.shape != (B, T, cfg.vocab) or B > cache.n_seqs:
         raise ValueError("pos must be [B], logits [B, T, V], and the page table have B rows")
+    _here(packed, ids, cache.tensors[0], pos, logits, ws)
     _check(_lib.smol_prefill_paged(ctypes.byref(cfg), packed.data_ptr(), ids.data_ptr(), B, T, cache.ref, pos.data_ptr(),
                                    logits.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream)), "smol_prefill_paged")
 
@@ -606,6 +615,7 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, n_accepted: torch.
     V = logits.shape[-1]
     ld = _row_pitch(logits, "logits", torch.bfloat16, B, T + 1, V)
     ldq = 0 if draft_probs is None else _row_pitch(draft_probs, "draft_probs", torch.float32, B, T, V)
+    _here(logits, drafts, n_accepted, next_ids, ws, uniform, draft_probs, n_draft, p_draft)
     i32, f32 = torch.int32, torch.float32
     _check(_lib.smol_verify_drafts(
         logits.data_ptr(), ld, _table(drafts, "drafts", i32, (B, T)),

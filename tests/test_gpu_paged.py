@@ -232,3 +232,33 @@ def test_scale_and_large_scores(S):
 def test_layers_of_one_pool(S):
     for layer in (0, 2):
         check_attention(S, "e4m3", 8, 2, 64, 32, [50, 333], [4, 80], L=3, layer=layer)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,KV,hd,T", [(8, 1, 64, 1), (8, 1, 64, 3), (8, 1, 64, 4), (8, 1, 64, 6), (7, 1, 64, 7), (6, 1, 64, 8),
+                                       (8, 1, 128, 1), (8, 1, 128, 2), (8, 1, 128, 3), (8, 1, 128, 4), (5, 1, 128, 9),
+                                       (1, 1, 128, 9), (1, 1, 64, 33), (3, 1, 128, 16), (7, 1, 128, 18)])
+def test_rows_next_to_the_kernels_borders(S, kind, H, KV, hd, T):
+    check_attention(S, kind, H, KV, hd, 16, [0, 31, 500, 1200, 2], [T, T, max(T - 2, 0), T, 1], packed=False)
+
+
+def test_strides_of_axes_of_one_entry_say_nothing(S):
+    import ctypes
+    cache = U.make_cache(S, "bf16", 1, 1, 64, 16, 1, 4)
+    fill(S, cache, [40])
+    q, out, ws = randn(1, 1, 1, 64, seed=8), torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda"), S.alloc_paged_workspace(cache, 1, 1, 64)
+    chunk = S.Chunk(1, 1, i32([39]))
+    S.paged_attention(cache, 0, chunk, q, out, ws)
+    bare = torch.zeros_like(out)
+    rows = [ctypes.byref(S._Rows(t.data_ptr(), 0, 0, 0, 0)) for t in (q, bare)]
+    S._check(S._lib.smol_paged_attention(cache.ref, 0, chunk.ref(1), 1, *rows, 0.0, 0, ws.data_ptr(), ws.numel(), S._stream()), "attention")
+    assert S.workspace_status(ws) == S.OK
+    assert torch.equal(out, bare)
+    # the many-rows kernel: one head, one sequence
+    q, out = randn(1, 40, 1, 64, seed=9), torch.zeros(1, 40, 1, 64, dtype=torch.bfloat16, device="cuda")
+    chunk = S.Chunk(1, 40, i32([0]))
+    S.paged_attention(cache, 0, chunk, q, out, ws)
+    bare = torch.zeros_like(out)
+    rows = [ctypes.byref(S._Rows(t.data_ptr(), 0, 0, 64, 0)) for t in (q, bare)]
+    S._check(S._lib.smol_paged_attention(cache.ref, 0, chunk.ref(1), 1, *rows, 0.0, 0, ws.data_ptr(), ws.numel(), S._stream()), "attention")
+    assert torch.equal(out, bare)

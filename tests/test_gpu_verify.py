@@ -158,6 +158,19 @@ def test_values_that_fill_a_counter(S, kw):
     check(S, logits, drafts, u, None, **kw)
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(top_k=700, top_p=0.3), dict(top_k=3)])
+def test_the_largest_vocabulary(S, kw):
+    V, T = 2 ** 19, 2
+    logits, drafts, u, probs = case(1, T, V, seed=6)
+    logits[0, 0] = 1.0                                     # all equal: the largest sum, 2^63 units
+    check(S, logits, drafts, u, probs, **kw)
+    u[0, :2] = 1.0
+    check(S, logits, drafts, u, None, **kw)
+    logits[0, 2] = -2.5
+    u[0, :2] = 0.0                                         # everything stays: the draw from the last row
+    check(S, logits, drafts, u, probs, **kw)
+
+
 @pytest.mark.parametrize("hidden", [-math.inf, torch.finfo(torch.bfloat16).min])
 @pytest.mark.parametrize("kw", [dict(), dict(top_k=300, top_p=0.9)])
 def test_a_masked_vocabulary(S, hidden, kw):
@@ -259,3 +272,15 @@ def test_frequencies_follow_the_target(S):
     p = torch.softmax(row[0].double(), -1)
     count = torch.bincount(first.long(), minlength=V).double()
     assert bool(((count - B * p).abs() <= 5 * (B * p * (1 - p)).sqrt()).all())
+
+
+def test_tensors_of_another_device_are_refused(S, monkeypatch):
+    logits, drafts, u, probs = case(1, 2, 100, seed=7)
+    acc, nxt = (torch.full((1,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    ws = S.alloc_verify_workspace(1, 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: logits.device.index + 1)
+    with pytest.raises(ValueError, match="current device"):
+        S.verify_drafts(logits, drafts, acc, nxt, ws, uniform=u, draft_probs=probs)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert int(acc) == -9 and int(nxt) == -9
