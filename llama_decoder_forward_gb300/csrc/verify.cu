@@ -29,8 +29,8 @@
 //           CTAs on an SM: the k-th largest of the threads' own maxima is a bound
 //           below which none of the k largest lies, and what reaches it, a little
 //           more than k tokens, goes to a list in shared memory on which the filters
-//           work token by token (64 sequences of up to 5 drafts, V = 49152, top-k 50:
-//           the whole call takes 26 us, with the histogram 54).
+//           work token by token, in descending order (64 sequences of up to 5 drafts, V =
+//           49152, top-k 50: the whole call takes 19 us, with the histogram 54).
 //   choice  one cluster of eight CTAs for each sequence: the acceptances, then
 //           the draw over one row, an eighth of the vocabulary for each CTA (or from
 //           the row's list, one token for each thread of one CTA).
@@ -686,11 +686,10 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
 struct TopSmem {
   float2 table[257];
   u64 red[33];
-  u64 mass[kTopThreads];
-  uint32_t key[kTopThreads];
-  int x[kTopThreads];
-  unsigned n, n_out, best;
-  int found, x_cut;
+  alignas(16) u64 token[kTopThreads];    // order key, and the index's complement: larger goes before
+  u64 z;
+  unsigned n, best, vcut;
+  int x_cut;
 };
 
 __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const VerifyParams p) {
@@ -723,9 +722,8 @@ __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const Verify
   };
   for (int k = tid; k < 257; k += kTopThreads) S.table[k] = kPow2.v[k];
   if (tid == 0) {
-    S.n = S.n_out = S.best = 0;
+    S.n = S.best = 0;
     S.x_cut = -1;
-    S.found = 0x10000;
   }
   uint32_t top2 = 0;                              // two maxima side by side
   for_chunks([&](int, const uint4 &k) { top2 = max2(top2, chunk_max2(k)); });
@@ -769,62 +767,54 @@ __global__ void __launch_bounds__(kTopThreads, 2) verify_top_kernel(const Verify
       const int x = row.base + 8 * c + e;
       if (chunk_half(k, e) < least || x < 0 || x >= p.V) continue;
       const unsigned to = atomicAdd(&S.n, 1u);
-      if (to < kTopThreads) {
-        S.key[to] = chunk_half(k, e);
-        S.x[to] = x;
-      }
+      if (to < kTopThreads) S.token[to] = argmax_pack(chunk_half(k, e), x);
     }
   });
   __syncthreads();
   const int n = static_cast<int>(S.n);
   if (n >= p.top_k && n <= kTopThreads) {
-    const bool mine = tid < n;
-    const uint32_t key = mine ? S.key[tid] : 0;
-    const int x = mine ? S.x[tid] : 0;
-    int larger = 0, no_less = 0;
-    if (mine) {
+    // in descending order, equal values in index order: a token's place is the number before it
+    const u64 token = tid < n ? S.token[tid] : 0;
+    int place = tid;
+    if (tid < n) {
+      place = 0;
+      int i = 0;
 #pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        larger += S.key[k] > key;
-        no_less += S.key[k] >= key;
+      for (; i + 1 < n; i += 2) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&S.token[i]);
+        place += (two.x > token) + (two.y > token);
       }
-      if (larger < p.top_k && p.top_k <= no_less) S.found = static_cast<int>(key);   // the k-th largest
+      if (i < n) place += S.token[i] > token;
     }
     __syncthreads();
-    vcut = static_cast<uint32_t>(S.found);
-    const u64 mass = mine && key >= vcut ? mass_of(mc, key_value(key)) : 0;
-    S.mass[tid] = mass;
+    S.token[place] = token;
+    __syncthreads();
+    const u64 own = S.token[tid];
+    const uint32_t key = static_cast<uint32_t>(own >> 32);
+    const int x = argmax_index(own);
+    vcut = static_cast<uint32_t>(S.token[p.top_k - 1] >> 32);         // the k-th largest value
+    const u64 mass = tid < n && key >= vcut ? mass_of(mc, key_value(key)) : 0;
+    const u64 before = block_scan<kTopThreads>(mass, S.red, &z);
     bool stays = mass != 0;
-    z = block_sum<kTopThreads>(mass, S.red);
     if (use_p) {
-      // a token stays while what comes before it in descending order (equal values in
-      // index order) does not exceed top_p of the whole
+      // a token stays while what comes before it does not exceed top_p of the whole
       const u64 goal = static_cast<u64>(static_cast<double>(p.top_p) * static_cast<double>(z));
-      if (stays) {
-        u64 before = 0;
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-          const uint32_t o = S.key[k];
-          before += o > key || (o == key && S.x[k] < x) ? S.mass[k] : 0;
-        }
-        stays = before <= goal;
+      stays = stays && before <= goal;
+    }
+    const int many = __syncthreads_count(stays);  // the first ones: masses descend, sums grow
+    if (use_p) {
+      if (tid == many - 1) {
+        S.z = before + mass;
+        S.vcut = key;
+        S.x_cut = x;
       }
-      if (tid == 0) S.found = 0x10000;
       __syncthreads();
-      if (stays) atomicMin(&S.found, static_cast<int>(key));
-      z = block_sum<kTopThreads>(stays ? mass : 0, S.red);
-      vcut = static_cast<uint32_t>(S.found);
-      if (stays && key == vcut) atomicMax(&S.x_cut, x);
-      __syncthreads();
+      z = S.z;
+      vcut = S.vcut;
       xcut = S.x_cut;
     }
-    VerifyToken *list = p.lists + static_cast<long long>(blockIdx.x) * kVerifyList;
-    if (stays) {
-      const unsigned to = atomicAdd(&S.n_out, 1u);
-      if (to < kVerifyList) list[to] = VerifyToken{mass, x, 0};
-    }
-    __syncthreads();
-    if (S.n_out <= kVerifyList) out.listed = static_cast<int>(S.n_out);
+    if (stays && tid < kVerifyList) p.lists[static_cast<long long>(blockIdx.x) * kVerifyList + tid] = VerifyToken{mass, x, 0};
+    if (many <= kVerifyList) out.listed = many;
   } else {
     // ---- fewer chunks than k, or many equal values: by passes over the row
     auto mass_from = [&](uint32_t t) {
