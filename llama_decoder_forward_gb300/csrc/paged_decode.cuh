@@ -94,14 +94,15 @@ struct PdCfg {
   static constexpr int OFF_Q = (OFF_NOTE + NW * NS * 64 + 1023) / 1024 * 1024;   // [2] this unit's and the next one's
   static constexpr int OFF_MERGE = OFF_Q + 2 * Q_BYTES;        // some warps' states; then the unit's rows
   static constexpr int BAR_BYTES = (NW * NS + 2) * 8 + 16;     // [NW][NS] stages, [2] Q
-  static constexpr int MERGE_WARPS = OFF_MERGE + 4 * STATE_BYTES + BAR_BYTES <= 232448 ? 4 : 2;
+  static constexpr int MERGE_WARPS = OFF_MERGE + 4 * STATE_BYTES + BAR_BYTES + 128 <= 232448 ? 4 : 2;
   static constexpr int TILE_LD = HD + 4;                       // words of a row of the merged unit
   static constexpr int TILE_BYTES = ROWS * (TILE_LD + 2) * 4;
   static constexpr int SCHED_BYTES = 8 * kPagedMaxCtas * 4 + (int)sizeof(PagedSchedSmem);   // the parts' weights, and the schedule
   static constexpr int MERGE_BYTES =
       (MERGE_WARPS * STATE_BYTES > SCHED_BYTES ? MERGE_WARPS * STATE_BYTES : SCHED_BYTES) / 16 * 16 + 16;
   static constexpr int OFF_BAR = OFF_MERGE + MERGE_BYTES;
-  static constexpr int USED = OFF_BAR + BAR_BYTES;
+  static constexpr int OFF_WALK = OFF_BAR + (BAR_BYTES + 15) / 16 * 16;
+  static constexpr int USED = OFF_WALK + (NR > 3 ? (int)sizeof(PagedIter) : 0);   // warp 0's walk over the queries
   static constexpr int SMEM = USED + 1008 <= 232448 ? USED + 1008 : 232448;
   static_assert(USED <= 232448, "shared memory per CTA");
   static_assert(MERGE_BYTES >= TILE_BYTES, "room for the merged unit");
@@ -168,9 +169,15 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
   bool alive = true;                              // false: a wait gave up, nothing more is asked for
   // ---- Q of a unit by TMA: its tokens' heads are the rows (rows past its last are
   // whatever follows, or zeros: they reach no other row)
-  PagedIter qn = ld;                              // the unit whose Q is asked for next (warp 0)
+  // (with 32 rows the walk lies in shared memory: in registers, where every warp would
+  // hold it, it makes the accumulators spill; e4m3, hd 128: 95 us, in registers 107)
+  PagedIter q_own;
+  PagedIter &next_q = NR > 3 ? *reinterpret_cast<PagedIter *>(smem + C::OFF_WALK) : q_own;
+  if (NR <= 3 || tid == 0) next_q = ld;
   uint32_t nq = 0;
   auto ask_q = [&]() {
+    PagedIter qn = next_q;                        // the unit whose Q is asked for next
+    __syncwarp();
     if (qn.left > 0 && alive) {
       if (lane == 0) {
         uint64_t *bar = &q_full[nq & 1];
@@ -184,6 +191,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
       qn.left -= qn.j1 - qn.j - 1;                // to the unit's last tile, and over it
       qn.j = qn.j1 - 1;
       paged_next(p, qn);
+      if (NR <= 3 || lane == 0) next_q = qn;
     }
     __syncwarp();
   };
@@ -253,6 +261,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
     ld_stage = ld_stage + 1 == NS ? 0 : ld_stage + 1;
   };
   if (warp == 0) {
+    __syncwarp();
     ask_q();
     ask_q();
   }

@@ -34,11 +34,14 @@ def starts(news):
     return s
 
 
-def fill(S, cache, lens, seed=1):
-    """Appends random keys and values at positions 0 .. lens[b] - 1."""
+def fill(S, cache, lens, seed=1, spread=0):
+    """Appends random keys and values at positions 0 .. lens[b] - 1, the values' rows times 2^-spread .. 2^spread."""
     B, T = len(lens), max(max(lens), 1)
     shape = (cache.n_layers, B, T, cache.n_kv_heads, cache.head_dim)
-    S.paged_append(cache, S.Chunk(B, T, i32([0] * B), n_new=i32(lens)), randn(*shape, seed=seed), randn(*shape, seed=seed + 1))
+    g = torch.Generator("cuda").manual_seed(seed + 2)
+    by = torch.exp2(torch.randint(-spread, spread + 1, (*shape[:-1], 1), generator=g, device="cuda").float())
+    S.paged_append(cache, S.Chunk(B, T, i32([0] * B), n_new=i32(lens)), randn(*shape, seed=seed),
+                   (randn(*shape, seed=seed + 1).float() * by).to(torch.bfloat16))
 
 
 # ---------------------------------------------------------------- append and read
@@ -131,11 +134,12 @@ def test_rows_out_of_range_are_not_written(S):
 
 
 # ---------------------------------------------------------------- attention
-def check_attention(S, kind, H, KV, hd, page, lens, news, window=0, packed=True, scale=None, qscale=2.0, T=None, L=1, layer=0):
+def check_attention(S, kind, H, KV, hd, page, lens, news, window=0, packed=True, scale=None, qscale=2.0, T=None, L=1, layer=0,
+                    spread=0):
     B, T = len(lens), T or max(max(news), 1)
     cols = -(-(max(a + n for a, n in zip(lens, news)) + 1) // page)
     cache = U.make_cache(S, kind, L, KV, hd, page, B, cols, seed=len(lens) + H)
-    fill(S, cache, [a + n for a, n in zip(lens, news)])
+    fill(S, cache, [a + n for a, n in zip(lens, news)], spread=spread)
     if packed:
         rs = starts(news)
         rows = rs[-1] + 2
@@ -262,3 +266,13 @@ def test_strides_of_axes_of_one_entry_say_nothing(S):
     rows = [ctypes.byref(S._Rows(t.data_ptr(), 0, 0, 64, 0)) for t in (q, bare)]
     S._check(S._lib.smol_paged_attention(cache.ref, 0, chunk.ref(1), 1, *rows, 0.0, 0, ws.data_ptr(), ws.numel(), S._stream()), "attention")
     assert torch.equal(out, bare)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,KV,hd", [(9, 3, 64), (16, 4, 128)])
+def test_values_of_very_different_size(S, kind, H, KV, hd):
+    # the first row sees neither the last positions nor, with a window, the first ones
+    for T in (1, 4, 5, 9, 100):
+        check_attention(S, kind, H, KV, hd, 16, [0, 40, 700], [T, T, T], packed=False, spread=40, window=0 if T % 2 else 50)
+    # peaked: the large values have weights of next to nothing
+    check_attention(S, kind, H, KV, hd, 16, [300, 90], [3, 70], spread=30, qscale=8.0)
