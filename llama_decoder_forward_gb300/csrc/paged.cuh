@@ -29,6 +29,12 @@ struct PagedRows {
   long long layer, seq, row, head;
 };
 
+// a / b of whole numbers, b > 0; in 32 bits where they hold both (a division of 64 bits
+// takes hundreds of cycles, and the kernels' starts wait for it)
+__device__ __forceinline__ long long paged_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<unsigned>(a) / static_cast<unsigned>(b) : a / b;
+}
+
 // One sequence of a chunk as the kernels use it: clamped so that no index built
 // from it leaves the tables or the row tensors.
 struct PagedSeq {

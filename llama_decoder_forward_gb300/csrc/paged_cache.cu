@@ -18,7 +18,9 @@
 // loads in flight, the row's maximum needs two or three shuffles, and the search
 // for the row's sequence and page is done once.  Consecutive groups take
 // consecutive kv heads of a row: contiguous in packed rows, whole 128- or 256-byte
-// lines otherwise.
+// lines otherwise.  In tensors whose rows of a head lie one behind the other (the dense
+// cache's layout) they take consecutive rows of a head: 16 sequences of up to 4096
+// tokens, e4m3 to bf16, 77 us, by kv heads 80.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -44,7 +46,7 @@ __device__ __forceinline__ bool chunk_row(const PagedChunk &c, long long r, int 
     const long long d = r - s.row0;
     t = d < 0 || d > 0x7fffffff ? -1 : static_cast<int>(d);
   } else {
-    b = static_cast<int>(r / c.T);
+    b = static_cast<int>(paged_div(r, c.T));
     t = static_cast<int>(r - static_cast<long long>(b) * c.T);
     s = paged_seq(c, b, cap);
   }
@@ -102,12 +104,20 @@ __device__ __forceinline__ uint4 quantise16(const uint4 (&w)[2], float &scale) {
 template <int HD, bool FP8, bool APPEND>
 __global__ void __launch_bounds__(kPcThreads) paged_copy_kernel(const PagedKv kv, const PagedChunk c,
                                                                 const PagedRows kr, const PagedRows vr,
-                                                                long long n_rows, int layers, int per) {
+                                                                long long n_rows, int layers, int per, int by_row) {
   constexpr int LANES = HD / 16;                 // lanes of one row
   const long long g = (static_cast<long long>(blockIdx.x) * kPcThreads + threadIdx.x) / LANES;
   const int part = threadIdx.x % LANES;          // values part * 16 .. + 15
-  const long long r = g / kv.KV;
-  const int h = static_cast<int>(g - r * kv.KV);
+  long long r;
+  int h;
+  if (by_row) {                                  // g = (b * KV + h) * T + t
+    const long long bh = paged_div(g, c.T), b = paged_div(bh, kv.KV);
+    h = static_cast<int>(bh - b * kv.KV);
+    r = b * c.T + (g - bh * c.T);
+  } else {                                       // g = row * KV + h
+    r = paged_div(g, kv.KV);
+    h = static_cast<int>(g - r * kv.KV);
+  }
   const int cap = kv.max_pages << kv.page_shift;
   int b = 0, t = 0, page = -1, x = 0;
   PagedSeq s{};
@@ -196,13 +206,14 @@ cudaError_t launch_copy(const PagedKv &kv, int layers, const PagedChunk &c, cons
   if (blocks > 0x7fffffffll || layers > 65535) return cudaErrorInvalidConfiguration;
   // layers of a thread: as many as leave some 2000 blocks, eight at most
   const int per = static_cast<int>(max(1ll, min(8ll, blocks * layers / 2000)));
+  const int by_row = !c.row_start && c.T > 1 && k.row == kv.hd && v.row == kv.hd;
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(cdiv(layers, per)));
   if (kv.hd == 64) {
-    if (kv.e4m3) paged_copy_kernel<64, true, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per);
-    else paged_copy_kernel<64, false, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per);
+    if (kv.e4m3) paged_copy_kernel<64, true, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per, by_row);
+    else paged_copy_kernel<64, false, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per, by_row);
   } else {
-    if (kv.e4m3) paged_copy_kernel<128, true, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per);
-    else paged_copy_kernel<128, false, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per);
+    if (kv.e4m3) paged_copy_kernel<128, true, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per, by_row);
+    else paged_copy_kernel<128, false, APPEND><<<grid, kPcThreads, 0, st>>>(kv, c, k, v, n_rows, layers, per, by_row);
   }
   return cudaGetLastError();
 }

@@ -72,12 +72,6 @@ __device__ __forceinline__ long long paged_seq_tiles(const PagedAttnParams &p, c
   return sum * p.kv.KV;
 }
 
-// a / b of whole numbers, b > 0; in 32 bits where they hold both (a division of 64 bits
-// takes hundreds of cycles, and every CTA's start waits for it)
-__device__ __forceinline__ long long paged_div(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? static_cast<unsigned>(a) / static_cast<unsigned>(b) : a / b;
-}
-
 struct PagedSchedSmem {
   long long warp_sum[32], total;
   int workers;
