@@ -586,9 +586,9 @@ def alloc_verify_workspace(B: int, T: int, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _table(t: torch.Tensor, name: str, dtype, shape) -> int:
-    if not (t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
+def _table(t: torch.Tensor, name: str, dtype, shape, device: int) -> int:
+    if not (t.get_device() == device and t.dtype == dtype and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on the current device")
     return t.data_ptr()
 
 
@@ -615,15 +615,15 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, n_accepted: torch.
     V = logits.shape[-1]
     ld = _row_pitch(logits, "logits", torch.bfloat16, B, T + 1, V)
     ldq = 0 if draft_probs is None else _row_pitch(draft_probs, "draft_probs", torch.float32, B, T, V)
-    _here(logits, drafts, n_accepted, next_ids, ws, uniform, draft_probs, n_draft, p_draft)
-    i32, f32 = torch.int32, torch.float32
+    _here(logits, draft_probs, ws)
+    i32, f32, dev = torch.int32, torch.float32, logits.get_device()
     _check(_lib.smol_verify_drafts(
-        logits.data_ptr(), ld, _table(drafts, "drafts", i32, (B, T)),
-        None if n_draft is None else _table(n_draft, "n_draft", i32, (B,)),
+        logits.data_ptr(), ld, _table(drafts, "drafts", i32, (B, T), dev),
+        None if n_draft is None else _table(n_draft, "n_draft", i32, (B,), dev),
         None if draft_probs is None else draft_probs.data_ptr(), ldq, B, T, V, temperature, top_k, top_p,
-        int(bool(do_sample)), None if uniform is None else _table(uniform, "uniform", f32, (B, T + 1)),
-        _table(n_accepted, "n_accepted", i32, (B,)), _table(next_ids, "next_ids", i32, (B,)),
-        None if p_draft is None else _table(p_draft, "p_draft", f32, (B, T)), ws.data_ptr(), ws.numel(),
+        int(bool(do_sample)), None if uniform is None else _table(uniform, "uniform", f32, (B, T + 1), dev),
+        _table(n_accepted, "n_accepted", i32, (B,), dev), _table(next_ids, "next_ids", i32, (B,), dev),
+        None if p_draft is None else _table(p_draft, "p_draft", f32, (B, T), dev), ws.data_ptr(), ws.numel(),
         _stream(stream)), "smol_verify_drafts")
 
 
