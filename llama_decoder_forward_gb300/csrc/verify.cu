@@ -997,7 +997,7 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
       const int x = x0 + e;
       const uint32_t key = chunk_half(keys, e);
       u64 m = mass_of(mc, key_value(key));        // 0 outside the row: -infinity
-      if (key < r.vcut || (key == r.vcut && x > r.xcut)) m = 0;
+      if (r.vcut && (key < r.vcut || (key == r.vcut && x > r.xcut))) m = 0;
       if (rest) m = q ? mass_less(m, qv[e], zh, zl) : x == gone ? 0 : m;
       w[e] = m;
       sum += m;
