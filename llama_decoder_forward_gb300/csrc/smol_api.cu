@@ -1049,7 +1049,7 @@ SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t 
   p.lists = reinterpret_cast<VerifyToken *>(static_cast<uint8_t *>(ws) + 1024);
   p.rows = reinterpret_cast<VerifyRow *>(p.lists + (size_t)B * (T + 1) * kVerifyList);
   int n = 0;
-  const cudaError_t e = launch_verify(p, static_cast<cudaStream_t>(stream), &n);
+  const cudaError_t e = launch_verify(p, sms, static_cast<cudaStream_t>(stream), &n);
   g_launches = n;
   return e == cudaSuccess ? SMOL_OK : cuda_fail(e);
 }

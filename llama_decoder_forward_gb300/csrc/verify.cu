@@ -16,15 +16,16 @@
 // borders are then off by less than 1e-11 of the whole.
 //
 // Two launches.
-//   rows    one CTA of 1024 threads for each target row, which it reads one to
-//           three times (from L2 after the first; in registers it would take half
-//           of them, and the spills cost more).  bf16 logits take few distinct
-//           values, so the row becomes a histogram over the values, and the
-//           exponential is taken once for each value that occurs: a tenth of the row
-//           and less.  The 65,536 counters have 16 bits, two in a word; where one ran
-//           over, which the sum shows, the row is read again for a histogram of the
-//           values >= 0 and one of those < 0.  The sum, the k-th largest value and the
-//           top-p cut are prefix sums over the histogram.
+//   rows    one CTA for each target row, which it reads one to three times (from L2
+//           after the first; in registers it would take half of them, and the spills
+//           cost more).  bf16 logits take few distinct values, so the row becomes a
+//           histogram over the values, and the exponential is taken once for each value
+//           that occurs: a tenth of the row and less.  The counters of the values of
+//           magnitude below 512 have 16 bits, two in a word, so that two CTAs of 512
+//           threads share an SM (few rows: one of 1024 threads).  Where one ran over,
+//           which the sum shows, or larger values count, the row is read again for 16,384
+//           values at a time, with counters of 32 bits.  The sum, the k-th largest value
+//           and the top-p cut are prefix sums over the histogram.
 //           With top-k up to 256 another kernel does this without a histogram, two
 //           CTAs on an SM: the k-th largest of the threads' own maxima is a bound
 //           below which none of the k largest lies, and what reaches it, a little
@@ -46,12 +47,13 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kRowThreads = 1024;
 constexpr int kTopThreads = 512;     // of the kernel for a small top-k, and the tokens of its list
 constexpr int kTopMaxK = 256;        // the largest top-k it takes
 constexpr int kBatch = 6;            // 16-byte loads in flight in each thread
-constexpr int kBins = 32768;         // values of one sign
-constexpr int kBinRows = kBins / 32;
+constexpr int kLoKey = 0x3c00, kHiKey = 0xc400;   // order keys of the values of magnitude below 512
+constexpr int kPairs = (kHiKey - kLoKey) / 2;
+constexpr int kWindow = 16384;       // keys that are counted together in 32 bits
+constexpr int kRows = 0x10000 / 32;  // rows of 32 neighbouring values
 constexpr int kChoiceThreads = 512;  // the most drafts of a sequence, too
 constexpr int kChoiceCtas = 8;
 constexpr float kMinLog2 = -45.f;    // 2^x below half a unit of 2^-44 counts as 0
@@ -230,19 +232,11 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(bits << 16);
 }
 
-// Adds 1 to the counter of key k (at `base` + 4 k) if k >= from, without a branch.
-__device__ __forceinline__ void count_from(uint32_t base, uint32_t k, uint32_t from) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t@p red.shared.add.u32 [%0], 1;\n\t}" ::"r"(base + 4 * k),
-               "r"(k), "r"(from)
-               : "memory");
-}
-// The same for two counters of 16 bits in a word, the value >= 0 in the lower one and
-// the one < 0 of the same low 15 key bits in the upper; `n` counts along.
-__device__ __forceinline__ void count_packed(uint32_t base, uint32_t k, uint32_t from, uint32_t &n) {
-  asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b32 v;\n\tsetp.ge.u32 p, %2, %3;\n\tsetp.ge.u32 q, %2, 0x8000;\n\t"
-               "selp.b32 v, 1, 0x10000, q;\n\t@p red.shared.add.u32 [%1], v;\n\t@p add.u32 %0, %0, 1;\n\t}"
+// Adds `by` to the counter at `to`, and 1 to n, where d < span, without a branch.
+__device__ __forceinline__ void count_in(uint32_t to, uint32_t by, uint32_t d, uint32_t span, uint32_t &n) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.u32 p, %3, %4;\n\t@p red.shared.add.u32 [%1], %2;\n\t@p add.u32 %0, %0, 1;\n\t}"
                : "+r"(n)
-               : "r"(base + 4 * (k & 0x7fffu)), "r"(k), "r"(from)
+               : "r"(to), "r"(by), "r"(d), "r"(span)
                : "memory");
 }
 
@@ -298,11 +292,10 @@ __device__ __forceinline__ u64 warp_max(u64 v) {
 }
 
 // ---------------------------------------------------------------- rows
-static_assert(kRowThreads == 1024 && kBinRows == 1024, "a warp for every 32nd row of values");
 struct RowSmem {
-  unsigned hist[kBins];
-  unsigned row_count[2 * kBinRows];  // tokens, and masses, of 32 neighbouring values, the largest first
-  u64 row_mass[2 * kBinRows];
+  unsigned hist[kPairs];             // two counters of 16 bits in a word, or one of 32 bits for each of kWindow keys
+  unsigned row_count[kRows];  // tokens, and masses, of 32 neighbouring values, the largest first
+  u64 row_mass[kRows];
   float2 table[257];
   u64 red[33];
   unsigned bins[32];
@@ -311,7 +304,9 @@ struct RowSmem {
   int found, bin, x_cut;
 };
 
-__global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const VerifyParams p) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) verify_rows_kernel(const VerifyParams p) {
+  constexpr int WARPS = THREADS / 32, PER = kRows / THREADS;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   RowSmem &S = *reinterpret_cast<RowSmem *>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -333,23 +328,23 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   // largest of its keys by a call
   auto for_chunks = [&](auto &&fn, auto &&between) {
     bool start = true;
-    for (int c0 = tid; start || c0 < row.chunks; c0 += kBatch * kRowThreads) {
+    for (int c0 = tid; start || c0 < row.chunks; c0 += kBatch * THREADS) {
       uint4 w[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (c0 + k * kRowThreads < row.chunks) w[k] = load_chunk(row, c0 + k * kRowThreads);
+        if (c0 + k * THREADS < row.chunks) w[k] = load_chunk(row, c0 + k * THREADS);
       if (start)
         between([&] {
           uint32_t top2 = 0;
 #pragma unroll
           for (int k = 0; k < kBatch; ++k)
-            if (c0 + k * kRowThreads < row.chunks) top2 = max2(top2, chunk_max2(chunk_keys(w[k])));
+            if (c0 + k * THREADS < row.chunks) top2 = max2(top2, chunk_max2(chunk_keys(w[k])));
           return max(top2 & 0xffffu, top2 >> 16);
         });
       start = false;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (c0 + k * kRowThreads < row.chunks) fn(c0 + k * kRowThreads, chunk_keys(w[k]));
+        if (c0 + k * THREADS < row.chunks) fn(c0 + k * THREADS, chunk_keys(w[k]));
     }
   };
   auto nothing = [](auto &&) {};
@@ -357,12 +352,12 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     v = __reduce_max_sync(0xffffffffu, v);
     if (lane == 0) S.red[warp] = v;
     __syncthreads();
-    v = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(S.red[lane]));
+    v = __reduce_max_sync(0xffffffffu, lane < WARPS ? static_cast<uint32_t>(S.red[lane]) : 0u);
     __syncthreads();
     return v;
   };
   auto clear = [&] {
-    for (int k = tid; k < kBins / 4; k += kRowThreads) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
+    for (int k = tid; k < kPairs / 4; k += THREADS) reinterpret_cast<uint4 *>(S.hist)[k] = make_uint4(0, 0, 0, 0);
   };
   // a value below l_max - 32 temperature has mass 0 (45 ln 2 = 31.2): the smallest key
   // that counts (one to spare for the truncation)
@@ -372,34 +367,39 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     const uint32_t k = bf16_order_key(static_cast<uint16_t>(__float_as_uint(least) >> 16));
     return k > 0 ? k - 1 : 0u;
   };
-  // one pass for both signs, the counters packed: the keys' maximum, and how many of this
-  // thread's were counted.  The largest of the first batch bounds what is counted.
+  // one pass for the values of magnitude below 512: the keys' maximum, and how many of
+  // this thread's were counted.  The largest of the first batch bounds what is counted.
   uint32_t counted = 0;
-  auto count_both = [&] {
-    uint32_t top2 = 0, from = 0;
-    const uint32_t base = smem_u32(S.hist);
+  auto count_packed = [&] {
+    uint32_t top2 = 0, from = 0, span = 0;
+    const uint32_t base = smem_u32(S.hist) - 2 * kLoKey;
     for_chunks([&](int, const uint4 &k) {
       top2 = max2(top2, chunk_max2(k));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) count_packed(base, chunk_half(k, e), from, counted);
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t key = chunk_half(k, e);
+        count_in(base + 2 * (key & 0xfffeu), 1u + (key & 1u) * 0xffffu, key - from, span, counted);
+      }
     }, [&](auto &&first_max) {
       clear();
-      from = least_key(block_max(first_max()));
+      from = max(least_key(block_max(first_max())), static_cast<uint32_t>(kLoKey));
+      span = from < kHiKey ? kHiKey - from : 0u;
     });
     return max(top2 & 0xffffu, top2 >> 16);
   };
-  // adds the values of one sign with keys >= from to the histogram; in the pass over
-  // the negative ones the keys' top bit is flipped, so that they are the upper half
-  auto count = [&](int half, uint32_t from) {
-    const uint32_t flip = half ? 0x80008000u : 0u, base = smem_u32(S.hist) - 4 * kBins;
+  // the keys of one window of kWindow, those >= from
+  auto count_window = [&](int window, uint32_t from) {
+    const uint32_t low = 0x10000u - (window + 1) * kWindow, lo = max(low, from), span = low + kWindow - lo;
+    const uint32_t base = smem_u32(S.hist) - 4 * low;
+    uint32_t all = 0;
     for_chunks([&](int, const uint4 &k) {
-      const uint4 q = make_uint4(k.x ^ flip, k.y ^ flip, k.z ^ flip, k.w ^ flip);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) count_from(base, chunk_half(q, e), from);
+      for (int e = 0; e < 8; ++e) count_in(base + 4 * chunk_half(k, e), 1u, chunk_half(k, e) - lo, span, all);
     }, [&](auto &&) {
       clear();
       __syncthreads();
     });
+    __syncthreads();
   };
 
   // ---- the largest value, with the histogram on the way
@@ -417,14 +417,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       }
     }, nothing);
   } else {
-    best = argmax_pack(count_both(), 0);
+    best = argmax_pack(count_packed(), 0);
   }
   best = warp_max(best);
   if (lane == 0) S.red[warp] = best;
-  for (int k = tid; k < 257; k += kRowThreads) S.table[k] = kPow2.v[k];
+  for (int k = tid; k < 257; k += THREADS) S.table[k] = kPow2.v[k];
   if (tid == 0) S.x_cut = p.V;
   __syncthreads();
-  best = warp_max(S.red[lane]);
+  best = warp_max(lane < WARPS ? S.red[lane] : 0);
   __syncthreads();
   const uint32_t kmax = static_cast<uint32_t>(best >> 32);
   const float lmax = key_value(kmax);
@@ -446,120 +446,118 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     return;
   }
   const MassCtx mc = MassCtx{lmax, p.c_hi, p.c_lo, S.table};
-  // ---- counts and masses of rows of 32 neighbouring values, the largest first: of one
-  // sign (rows 0 .. 1023 or 1024 .. 2047), or of both where the counters are packed
-  auto sum_row = [&](int r, unsigned c) {
-    unsigned cs = 0;
-    u64 ms = 0;
-    if (__any_sync(0xffffffffu, c != 0)) {
-      ms = mass_of(mc, key_value((r < kBinRows ? 0xffffu : 0x7fffu) - ((r & (kBinRows - 1)) * 32 + lane))) * c;
-      cs = __reduce_add_sync(0xffffffffu, c);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
-    }
-    if (lane == 0) {
-      S.row_count[r] = cs;
-      S.row_mass[r] = ms;
-    }
-  };
-  // fn(word row, its word in this lane), rows without tokens left out: a warp looks
-  // through its 32 rows first
-  auto for_words = [&](auto &&fn) {
-    const unsigned *mine = S.hist + kBins - 1 - (warp * 32 + lane);
-    uint32_t some = 0;
-#pragma unroll
-    for (int k = 0; k < kBinRows / 32; ++k) some |= (__any_sync(0xffffffffu, mine[-k * kRowThreads] != 0) ? 1u : 0u) << k;
-#pragma unroll 1
-    for (; some; some &= some - 1) {
-      const int k = __ffs(some) - 1;
-      fn(warp + 32 * k, mine[-k * kRowThreads]);
-    }
-  };
-  auto clear_rows = [&](int half) {
-    S.row_count[half * kBinRows + tid] = 0;
-    S.row_mass[half * kBinRows + tid] = 0;
-  };
-  auto sum_rows = [&](int half) {
-    clear_rows(half);
-    __syncthreads();
-    for_words([&](int r, unsigned c) { sum_row(half * kBinRows + r, c); });
-    __syncthreads();
-  };
-  enum { kPositive, kNegative, kBoth };
-  int resident = kBoth;                           // the values that the histogram holds
+  // ---- counts and masses of rows of 32 neighbouring values, the largest first: row r has
+  // the keys 0xffff - 32 r - (0 .. 31)
+  for (int k = tid; k < kRows; k += THREADS) {
+    S.row_count[k] = 0;
+    S.row_mass[k] = 0;
+  }
+  __syncthreads();
+  constexpr int kPacked = -1;
+  int resident = kPacked;                         // what the histogram holds, or the window
   u64 total_m = 0;
   unsigned held = 0;
-  if (use_k || use_p) {
-    clear_rows(0);
-    clear_rows(1);
-    __syncthreads();
-    for_words([&](int r, unsigned c) {
-      sum_row(r, c & 0xffffu);
-      sum_row(kBinRows + r, c >> 16);
-    });
-    __syncthreads();
-    held = S.row_count[tid] + S.row_count[kBinRows + tid];
-  } else {
-    // only the whole sum is wanted
-    for_words([&](int r, unsigned c) {
-      const unsigned plus = c & 0xffffu, minus = c >> 16;
-      held += plus + minus;
-      if (plus) total_m += mass_of(mc, key_value(0xffffu - (r * 32 + lane))) * plus;
-      if (minus) total_m += mass_of(mc, key_value(0x7fffu - (r * 32 + lane))) * minus;
-    });
-    total_m = block_sum<kRowThreads>(total_m, S.red);
-  }
-  if (block_sum<kRowThreads>(static_cast<int>(held - counted), S.red) != 0) {
-    // a counter of 16 bits ran over, which takes 65,535 or 65,536 from the sum: again,
-    // a sign at a time, with 32 bits
-    resident = kPositive;
-    count(0, 0x8000u);
-    __syncthreads();
-    sum_rows(0);
-    // the negative values: not where none of them counts, nor where the k largest are all >= 0
-    const uint32_t from = least_key(kmax);
-    bool negative = from <= 0x7fffu;
-    if (use_k && negative) negative = block_sum<kRowThreads>(S.row_count[tid], S.red) < static_cast<u64>(p.top_k);
-    if (negative) {
-      resident = kNegative;
-      count(1, from + 0x8000u);
-      __syncthreads();
-      sum_rows(1);
-    } else {
-      clear_rows(1);
+  // a warp looks through its blocks of 64 keys first: two in each lane
+  {
+    constexpr int BLOCKS = kPairs / 32 / WARPS;
+    static_assert(BLOCKS * 32 * WARPS == kPairs && BLOCKS <= 64, "the same number of blocks for every warp");
+    const unsigned *mine = S.hist + warp * 32 + lane;
+    u64 some = 0;
+#pragma unroll
+    for (int k = 0; k < BLOCKS; ++k) some |= static_cast<u64>(__any_sync(0xffffffffu, mine[k * THREADS] != 0) ? 1 : 0) << k;
+#pragma unroll 1
+    for (; some; some &= some - 1) {
+      const int k = __ffsll(static_cast<long long>(some)) - 1, block = warp + k * WARPS;
+      const unsigned w = mine[k * THREADS], c0 = w & 0xffffu, c1 = w >> 16;
+      const uint32_t key = kLoKey + 64 * block + 2 * lane;
+      u64 ms = 0;
+      if (c0) ms = mass_of(mc, key_value(key)) * c0;
+      if (c1) ms += mass_of(mc, key_value(key + 1)) * c1;
+      held += c0 + c1;
+      if (!use_k && !use_p) {                     // only the whole sum is wanted
+        total_m += ms;
+      } else {
+        unsigned cs = c0 + c1;
+#pragma unroll
+        for (int o = 8; o; o >>= 1) {
+          cs += __shfl_xor_sync(0xffffffffu, cs, o);
+          ms += __shfl_xor_sync(0xffffffffu, ms, o);
+        }
+        if ((lane & 15) == 0) {
+          const int r = (0xffff - static_cast<int>(key)) >> 5;        // the lower 32 keys are the later row
+          S.row_count[r] = cs;
+          S.row_mass[r] = ms;
+        }
+      }
     }
-    __syncthreads();
   }
-  // prefix sums over the 2048 rows of values, two for each thread
-  u64 total_c = 0, m0 = 0, m1 = 0, pc = 0, pm = 0;
-  unsigned c0 = 0, c1 = 0;
-  if (use_k || use_p || resident != kBoth) {
-    c0 = S.row_count[2 * tid], c1 = S.row_count[2 * tid + 1];
-    m0 = S.row_mass[2 * tid], m1 = S.row_mass[2 * tid + 1];
-    pc = block_scan<kRowThreads>(c0 + c1, S.red, &total_c);
-    pm = block_scan<kRowThreads>(m0 + m1, S.red, &total_m);
+  const uint32_t least = least_key(kmax);
+  // a counter of 16 bits that ran over takes 65,535 or 65,536 from the sum
+  const bool spoilt = block_sum<THREADS>(static_cast<int>(held - counted), S.red) != 0;
+  if (!use_k && !use_p) total_m = block_sum<THREADS>(total_m, S.red);
+  if (spoilt || kmax >= kHiKey || least < kLoKey) {
+    // so did one, or values of 512 and more count: a window of the keys at a time, with
+    // counters of 32 bits, down to the smallest key that counts or the k-th largest
+    u64 have = 0;
+    for (int k = tid; k < kRows; k += THREADS) {
+      S.row_count[k] = 0;
+      S.row_mass[k] = 0;
+    }
+    for (int window = 0; window < 0x10000 / kWindow; ++window) {
+      if (0xffffu - window * kWindow < least || (use_k && have >= static_cast<u64>(p.top_k))) break;
+      resident = window;
+      count_window(window, least);
+      unsigned mine = 0;
+      for (int j = warp; j < kWindow / 32; j += WARPS) {
+        const unsigned c = S.hist[kWindow - 1 - 32 * j - lane];
+        if (!__any_sync(0xffffffffu, c != 0)) continue;
+        const int r = window * (kWindow / 32) + j;
+        u64 ms = c ? mass_of(mc, key_value(0xffffu - 32 * r - lane)) * c : 0;
+        const unsigned cs = __reduce_add_sync(0xffffffffu, c);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ms += __shfl_xor_sync(0xffffffffu, ms, o);
+        mine += c;
+        if (lane == 0) {
+          S.row_count[r] = cs;
+          S.row_mass[r] = ms;
+        }
+      }
+      have += block_sum<THREADS>(mine, S.red);
+    }
+  }
+  // prefix sums over the rows, PER for each thread
+  u64 total_c = 0, pc = 0, pm = 0, m_of[PER] = {}, mm = 0;
+  unsigned c_of[PER] = {}, cc = 0;
+  if (use_k || use_p || resident != kPacked) {
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      cc += c_of[q] = S.row_count[PER * tid + q];
+      mm += m_of[q] = S.row_mass[PER * tid + q];
+    }
+    pc = block_scan<THREADS>(cc, S.red, &total_c);
+    pm = block_scan<THREADS>(mm, S.red, &total_m);
   }
 
   // the counters of one row of 32 values, into S.bins
   auto fetch_bins = [&](int r) {
-    const bool here = resident == kBoth || r / kBinRows == resident;
-    if (tid < 32) {
-      const unsigned c = S.hist[kBins - 1 - ((r % kBinRows) * 32 + tid)];
-      S.bins[tid] = !here ? 0u : resident != kBoth ? c : r < kBinRows ? c & 0xffffu : c >> 16;
-    }
+    const int top = 0xffff - 32 * r;
+    const bool here = resident == kPacked || r / (kWindow / 32) == resident;
+    if (tid < 32)
+      S.bins[tid] = !here                 ? 0u
+                    : resident == kPacked ? reinterpret_cast<const uint16_t *>(S.hist)[top - tid - kLoKey]
+                                          : S.hist[kWindow - 1 - 32 * (r % (kWindow / 32)) - tid];
     __syncthreads();
     if (here) return;
-    const uint32_t top = (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32;
     for_chunks([&](int, const uint4 &k) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t d = top - chunk_half(k, e);
+        const uint32_t d = static_cast<uint32_t>(top) - chunk_half(k, e);
         if (d < 32u) atomicAdd(&S.bins[d], 1u);
       }
     }, nothing);
     __syncthreads();
   };
-  auto key_of = [&](int r, int bin) { return (r < kBinRows ? 0xffffu : 0x7fffu) - (r % kBinRows) * 32 - bin; };
+  auto key_of = [&](int r, int bin) { return static_cast<uint32_t>(0xffff - 32 * r - bin); };
 
   // ---- top-k: the k-th largest value; where fewer than k have a mass, all stay
   uint32_t vcut = 0;                              // values above stay, and of this one the tokens up to xcut
@@ -567,11 +565,16 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
   u64 z = total_m;
   const u64 k_th = static_cast<u64>(max(p.top_k, 0));
   if (use_k && total_c >= k_th) {
-    if (pc < k_th && k_th <= pc + c0 + c1) {
-      const bool second = k_th > pc + c0;
-      S.found = 2 * tid + second;
-      S.before_count = static_cast<unsigned>(pc + (second ? c0 : 0));
-      S.before_mass = pm + (second ? m0 : 0);
+    u64 c_before = pc, m_before = pm;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      if (c_before < k_th && k_th <= c_before + c_of[q]) {
+        S.found = PER * tid + q;
+        S.before_count = static_cast<unsigned>(c_before);
+        S.before_mass = m_before;
+      }
+      c_before += c_of[q];
+      m_before += m_of[q];
     }
     __syncthreads();
     const int r = S.found;
@@ -610,10 +613,14 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
     __syncthreads();
     const u64 goal = S.t_cut;                     // a whole sum exceeds top_p z iff it exceeds its floor
     auto over = [&](u64 v) { return v > goal; };
-    if (!over(pm) && over(pm + m0 + m1)) {
-      const bool second = !over(pm + m0);
-      S.found = 2 * tid + second;
-      S.before_mass = pm + (second ? m0 : 0);
+    u64 m_before = pm;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+      if (!over(m_before) && over(m_before + m_of[q])) {
+        S.found = PER * tid + q;
+        S.before_mass = m_before;
+      }
+      m_before += m_of[q];
     }
     __syncthreads();
     const int r = S.found;                        // found: z > goal
@@ -645,9 +652,9 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
       vcut = v;
       if (tc != ~0ull) {
         // the index of the (t + 1)-th token of this value: counts in vocabulary
-        // order, a round of 1024 chunks at a time
+        // order, a round of a chunk for each thread at a time
         u64 seen = 0;
-        for (int c_first = 0; c_first < row.chunks; c_first += kRowThreads) {
+        for (int c_first = 0; c_first < row.chunks; c_first += THREADS) {
           const int c = c_first + tid;
           uint4 k = make_uint4(0, 0, 0, 0);       // key 0 is a NaN, never the cut
           if (c < row.chunks) k = chunk_keys(load_chunk(row, c));
@@ -655,7 +662,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) verify_rows_kernel(const Verif
 #pragma unroll
           for (int e = 0; e < 8; ++e) mine += chunk_half(k, e) == v;
           u64 all;
-          u64 rank = seen + block_scan<kRowThreads>(mine, S.red, &all);
+          u64 rank = seen + block_scan<THREADS>(mine, S.red, &all);
           if (rank <= tc && tc < rank + mine) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -1053,15 +1060,18 @@ __global__ void __cluster_dims__(kChoiceCtas, 1, 1) __launch_bounds__(kChoiceThr
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st, int *launches) {
-  cudaError_t e = ensure_smem_attr<verify_rows_kernel>(sizeof(RowSmem));
+cudaError_t launch_verify(const VerifyParams &p, int sms, cudaStream_t st, int *launches) {
+  cudaError_t e = ensure_smem_attr<verify_rows_kernel<512>>(sizeof(RowSmem));
+  if (e == cudaSuccess) e = ensure_smem_attr<verify_rows_kernel<1024>>(sizeof(RowSmem));
   if (e != cudaSuccess) return e;
   const unsigned rows = static_cast<unsigned>(p.B) * (p.T + 1);
   prof_before(SMOL_K_SAMPLE, st);
   if (!p.greedy && p.top_k > 0 && p.top_k <= kTopMaxK && p.top_k < p.V)
     verify_top_kernel<<<rows, kTopThreads, 0, st>>>(p);
+  else if (rows <= 3u * sms / 2)                  // 192 rows of V = 128257: 71 us, by 512 threads 76; 256 rows 75 and 66
+    verify_rows_kernel<1024><<<rows, 1024, sizeof(RowSmem), st>>>(p);
   else
-    verify_rows_kernel<<<rows, kRowThreads, sizeof(RowSmem), st>>>(p);
+    verify_rows_kernel<512><<<rows, 512, sizeof(RowSmem), st>>>(p);
   prof_after(SMOL_K_SAMPLE, st);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   *launches = 1;

@@ -42,6 +42,6 @@ struct VerifyParams {
   VerifyToken *lists;          // [B, T + 1][kVerifyList], workspace
   int *status;
 };
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t st, int *launches);
+cudaError_t launch_verify(const VerifyParams &p, int sms, cudaStream_t st, int *launches);
 
 }  // namespace smol

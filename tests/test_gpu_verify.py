@@ -158,6 +158,16 @@ def test_values_that_fill_a_counter(S, kw):
     check(S, logits, drafts, u, None, **kw)
 
 
+@pytest.mark.parametrize("B", [2, 80])
+@pytest.mark.parametrize("spread,peak,kw", [(400.0, 0.0, dict(temperature=60.0)), (2.0, 900.0, dict()), (300.0, 700.0, dict(top_p=0.9)),
+                                            (5.0, 0.0, dict(temperature=50.0, top_k=300)), (0.5, 6.0, dict(top_p=0.7)),
+                                            (400.0, 0.0, dict(temperature=90.0, top_k=700, top_p=0.8))])
+def test_large_logits_and_temperatures(S, B, spread, peak, kw):
+    logits, drafts, u, probs = case(B, 3, 3001, seed=8, spread=spread, peak=peak)
+    check(S, logits, drafts, u, probs, **kw)
+    check(S, logits, drafts, u, None, **kw)
+
+
 @pytest.mark.parametrize("kw", [dict(), dict(top_k=700, top_p=0.3), dict(top_k=3)])
 def test_the_largest_vocabulary(S, kw):
     V, T = 2 ** 19, 2
