@@ -31,7 +31,7 @@
 //           below which none of the k largest lies, and what reaches it, a little
 //           more than k tokens, goes to a list in shared memory on which the filters
 //           work token by token, in descending order (64 sequences of up to 5 drafts, V =
-//           49152, top-k 50: the whole call takes 19 us, with the histogram 54).
+//           49152, top-k 50: the whole call takes 19 us, with the histogram 50).
 //   choice  one cluster of eight CTAs for each sequence: the acceptances, then
 //           the draw over one row, an eighth of the vocabulary for each CTA (or from
 //           the row's list, one token for each thread of one CTA).
