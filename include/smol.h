@@ -492,7 +492,8 @@ int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_ch
  *            status word otherwise); new token t stands at position pos[b] + t.
  *   logits   device [B, T, V] bf16.
  *   ws       >= smol_prefill_paged_workspace_bytes(cfg, cache, B, T) bytes, zeroed
- *            once.
+ *            once; one of the largest call's size serves prompts, drafts and
+ *            single tokens of any batch in turn.
  * B up to 4096; T < max_pos and T <= max_pages * page_size (SMOL_ERR_TOO_LONG).
  * ------------------------------------------------------------------------- */
 size_t smol_prefill_paged_workspace_bytes(const smol_config *cfg, const smol_paged_cache *cache, int B, int T);

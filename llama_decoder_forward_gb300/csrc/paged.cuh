@@ -100,8 +100,8 @@ struct PagedAttnParams {
   int tt, bk_shift;            // query tokens of a unit, log2 of the keys of a tile (paged_sched.cuh)
   int ctas;                    // CTAs that share the work
   unsigned long long wait_ns;  // limit of the bounded waits
-  uint8_t *ws;
-  int *status;
+  uint8_t *ws;                 // notes and parts (paged_sched.cuh)
+  int *status;                 // the status word, and the parts' counters behind it
 };
 size_t paged_attention_ws_bytes(int hd, int H, int KV, int B, int T);
 bool paged_map_q(CUtensorMap *map, const PagedAttnParams &p);

@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
         __syncthreads();
         if (tid == 0) {
           const int c0 = paged_worker_of(u.u0, total, workers), n = paged_worker_of(u.u0 + u.j01 - 1, total, workers) - c0 + 1;
-          int *count = reinterpret_cast<int *>(p.ws + kPagedCountOff) + c0;
+          int *count = paged_counts(p.status) + c0;
           __threadfence();
           const bool mine = atomicAdd(count, 1) == n - 1;
           if (mine) {

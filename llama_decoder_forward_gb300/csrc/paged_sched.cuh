@@ -177,9 +177,15 @@ struct PagedMeta {
 };
 // (The few-rows kernel needs no note: it finds a unit's CTAs by arithmetic.)
 constexpr int kPagedMaxCtas = 160;
-// After the status word: a counter for each CTA, of the parts of the unit that it
-// began (zero between calls); the notes; the parts.
-constexpr size_t kPagedCountOff = 256, kPagedMetaOff = 1024, kPagedPartOff = kPagedMetaOff + kPagedMaxCtas * sizeof(PagedMeta) + 256;
+// Behind the status word, in its block of 1024 bytes: a counter for each CTA, of the
+// parts of the unit that it began.  They are zero between calls, the one thing that a
+// call finds as an earlier one left it, so they lie where no size of a call moves
+// them (the model's forward has its activations between that block and `ws`).
+constexpr size_t kPagedCountOff = 256;
+static_assert(kPagedCountOff + kPagedMaxCtas * sizeof(int) <= 1024, "the counters lie in the status block");
+__device__ __forceinline__ int *paged_counts(int *status) { return status + kPagedCountOff / sizeof(int); }
+// In `ws`, written before they are read in each call: the notes; the parts.
+constexpr size_t kPagedMetaOff = 1024, kPagedPartOff = kPagedMetaOff + kPagedMaxCtas * sizeof(PagedMeta) + 256;
 
 // Place of CTA c: rows of HD sums, then (maximum, sum) of each row.
 __device__ __forceinline__ float *paged_part(uint8_t *ws, int c, int place, int rows, int hd) {

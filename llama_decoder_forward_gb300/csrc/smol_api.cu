@@ -81,7 +81,7 @@ WsLayout ws_layout(const smol_config *c, int B, int T, bool chain = false) {
   const size_t d = c->hidden, hd = c->head_dim, H = c->n_heads, KV = c->n_kv_heads, I = c->intermediate;
   const size_t v_elems = (size_t)B * KV * hd * t_pad(T);
   size_t o = 0;
-  W.status = o; o += 1024;
+  W.status = o; o += 1024;   // and the paged attention's counters, which stay where they are for every B and T
   W.x = o; o = align_up(o + M * d * 2, 1024);
   W.h = o; o = align_up(o + M * d * 2, 1024);
   W.q = o; o = align_up(o + M * H * hd * 2, 1024);
@@ -223,7 +223,7 @@ struct PagedCtx {
   const smol_paged_cache *cache;
   const int32_t *pos;              // [B] device
   int layer;
-  uint8_t *ws;                     // the paged attention's workspace
+  uint8_t *ws;                     // the paged attention's notes and parts
 };
 PagedKv paged_kv(const smol_paged_cache *c, int layer);
 
