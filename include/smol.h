@@ -416,9 +416,10 @@ typedef struct smol_paged_cache {
  *              has n_new[b] rows, 0 to T; NULL: all T.
  * Values outside their range (a negative position or count, more than T rows, a
  * position behind the table's last page, a page number outside [0, n_pages))
- * touch no memory outside the buffers; the rows concerned are not written by
- * smol_paged_append and smol_paged_read, and not defined (but recorded in the
- * status word as SMOL_ERR_INPUT) by smol_paged_attention. */
+ * touch no memory outside the buffers; the rows concerned (of a sequence whose
+ * pos or row_start is negative, all) are not written by smol_paged_append and
+ * smol_paged_read, and not defined (but recorded in the status word as
+ * SMOL_ERR_INPUT) by smol_paged_attention. */
 typedef struct smol_chunk {
   int B, T;
   const int32_t *pos, *row_start, *n_new;
@@ -489,7 +490,8 @@ int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_ch
  *   cache    of cfg's layers, kv heads and head_dim; its pages are written.
  *   pos      device int32 [B]: tokens of sequence b already in its pages, each in
  *            [0, min(max_pages * page_size, max_pos) - T] (SMOL_ERR_INPUT in the
- *            status word otherwise); new token t stands at position pos[b] + t.
+ *            status word otherwise, and no page is written for a negative one);
+ *            new token t stands at position pos[b] + t.
  *   logits   device [B, T, V] bf16.
  *   ws       >= smol_prefill_paged_workspace_bytes(cfg, cache, B, T) bytes, zeroed
  *            once; one of the largest call's size serves prompts, drafts and

@@ -42,6 +42,7 @@ struct PagedSeq {
   int n;                       // rows
   int row0;                    // packed: index of its row 0 (0 otherwise)
   bool bad;                    // a value was out of its range
+  bool moved;                  // its position or start was below 0: its rows are not where L and row0 say
 };
 
 __device__ __forceinline__ PagedSeq paged_seq(const PagedChunk &c, int b, int cap) {
@@ -49,6 +50,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedChunk &c, int b, int ca
   const int L = c.pos[b];
   s.L = min(max(L, 0), cap);
   s.bad = s.L != L;
+  s.moved = L < 0;
   long long n = c.T;
   s.row0 = 0;
   if (c.row_start) {
@@ -56,6 +58,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedChunk &c, int b, int ca
     const long long from = min(max(a, 0ll), c.rows), end = min(max(e, from), c.rows);   // c.rows < 2^31
     s.row0 = static_cast<int>(from);
     s.bad |= from != a || end != e;
+    s.moved |= a < 0;
     n = end - from;
   } else if (c.n_new) {
     n = c.n_new[b];

@@ -32,7 +32,8 @@ namespace {
 constexpr int kPcThreads = 256;
 
 // The sequence and row index of row r of the chunk's row tensors (packed: the
-// sequence that owns row r by a search of row_start; else r = b * T + t).
+// sequence that owns row r by a search of row_start; else r = b * T + t); whether
+// there is such a row, and it stands at a position.
 __device__ __forceinline__ bool chunk_row(const PagedChunk &c, long long r, int cap, int &b, int &t, PagedSeq &s) {
   if (c.row_start) {
     int lo = 0, hi = c.B;                        // row_start[lo] <= r < row_start[hi], if any
@@ -50,7 +51,7 @@ __device__ __forceinline__ bool chunk_row(const PagedChunk &c, long long r, int 
     t = static_cast<int>(r - static_cast<long long>(b) * c.T);
     s = paged_seq(c, b, cap);
   }
-  return t >= 0 && t < s.n;
+  return t >= 0 && t < s.n && !s.moved;
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {

@@ -31,3 +31,77 @@ def test_one_workspace_serves_prompts_drafts_and_single_tokens(S, kind, hd128):
         got, want = forward(B, T, ws), forward(B, T, S.prefill_paged_workspace(cfg, cache, B, T))
         # two runs of one call (the order of the sums of squares may differ): each within the bar of the definition
         assert cosine(got, want) >= LOGITS_COS_MIN and max_abs(got, want) <= 2 * LOGITS_MAX_ABS, (B, T)
+
+
+# ---------------------------------------------------------------- rows out of range
+def bits(cache):
+    return [None if t is None else t.clone().view(torch.uint8) for t in cache.tensors]
+
+
+def unchanged(cache, before, rows):
+    """Nothing in the pools but the rows [(page, slot)] of every layer and kv head has changed."""
+    for now, old in zip(bits(cache), before):
+        if now is None or now.dim() < 4:
+            continue
+        now, old = (t.flatten(4) if t.dim() > 4 else t.view(*t.shape[:3], cache.page_size, -1) for t in (now, old))
+        differs = (now != old).flatten(4).any(-1).any(2).any(0)                # [page, slot]
+        for page, slot in rows:
+            differs[page, slot] = False
+        if bool(differs.any()):
+            return False
+    return True
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 7])
+def test_a_negative_position_moves_no_rows(S, kind, T):
+    """-5 + 6 would be a position again; the whole sequence is left out."""
+    cache = small(S, kind, T, [20, 20, 20])
+    before = bits(cache)
+    k, v = randn(1, 3, T, 2, 64, seed=31), randn(1, 3, T, 2, 64, seed=32)
+    chunk = S.Chunk(3, T, i32([-5, 20, -2 ** 31]))
+    S.paged_append(cache, chunk, k, v)
+    at = [20 + t for t in range(T)]
+    ids = cache.tensors[2][1].tolist()
+    assert unchanged(cache, before, [(ids[x // 16], x % 16) for x in at])
+    for which, new in (("k", k), ("v", v)):
+        want = new[0, 1].transpose(0, 1)                                         # [KV, T, hd]
+        if kind == "e4m3":
+            codes, scale = U.quantised(want)
+            want = codes.double() * scale.double()[..., None]
+        assert torch.equal(U.values(cache, which, 0, 1, 20 + T)[:, 20:], want.double())
+    out = [torch.full((1, 3, T, 2, 64), -7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    S.paged_read(cache, chunk, *out)
+    for o in out:
+        assert bool((o[0, [0, 2]] == -7.0).all()) and not bool((o[0, 1] == -7.0).any())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_a_negative_start_moves_no_rows(S, kind):
+    cache = small(S, kind, 8, [20, 20, 20])
+    before = bits(cache)
+    k, v = randn(1, 12, 2, 64, seed=33), randn(1, 12, 2, 64, seed=34)
+    chunk = S.Chunk(3, 8, i32([4, 20, 9]), row_start=i32([-3, 4, 8, 12]))
+    S.paged_append(cache, chunk, k, v)
+    table = cache.tensors[2].tolist()
+    rows = [(table[b][x // 16], x % 16) for b, at in ((1, 20), (2, 9)) for x in range(at, at + 4)]
+    assert unchanged(cache, before, rows)
+    out = [torch.full((1, 12, 2, 64), -7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    S.paged_read(cache, chunk, *out)
+    for o, new in zip(out, (k, v)):
+        assert bool((o[0, :4] == -7.0).all())
+        if kind == "bf16":
+            assert torch.equal(o[0, 4:], new[0, 4:])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_the_model_leaves_the_pages_of_a_negative_position(S, kind):
+    lengths = [4, 20]
+    wl, _, _, cfg, packed, cache, ids = case(S, 12, lengths, 3, kind=kind)
+    before = bits(cache)
+    logits = torch.zeros(2, 3, wl.vocab, dtype=torch.bfloat16, device="cuda")
+    ws = S.prefill_paged_workspace(cfg, cache, 2, 3)
+    S.prefill_paged(cfg, packed, ids.cuda(), cache, i32([-1, 20]), logits, ws)
+    assert S.workspace_status(ws) == S.ERR_INPUT
+    table = cache.tensors[2].tolist()
+    assert unchanged(cache, before, [(table[1][x // 16], x % 16) for x in range(20, 23)])
