@@ -533,6 +533,8 @@ int smol_prefill_paged(const smol_config *cfg, const void *packed, const int32_t
  *   p_draft     device fp32 [B, T] output or NULL: p_i(draft_i), 0 behind a
  *               sequence's drafts.
  *   ws          >= smol_verify_workspace_bytes(B, T) bytes, zeroed once.
+ * The outputs and ws overlap neither one another nor an input
+ * (SMOL_ERR_INVALID_ARG where one meets drafts, n_draft or uniform).
  * Probabilities are held to about 2^-43 of the row's largest and summed exactly
  * (a token below 2^-45 of the largest counts as impossible), so the choice is
  * the definition's except where u lies within 1e-11 of a border.

@@ -1003,6 +1003,27 @@ SMOL_API size_t smol_verify_workspace_bytes(int B, int T) {
   return 1024 + (sizeof(VerifyRow) + kVerifyList * sizeof(VerifyToken)) * (size_t)B * ((size_t)T + 1);
 }
 
+namespace {
+// One of `outs` overlaps another or one of `ins` (NULL and empty spans overlap nothing).
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+bool overlaps(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span &a, const Span &b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (const Span *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span *q = o + 1; q != outs.end(); ++q)
+      if (meet(*o, *q)) return true;
+    for (const Span &i : ins)
+      if (meet(*o, i)) return true;
+  }
+  return false;
+}
+}  // namespace
+
 SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t *drafts, const int32_t *n_draft,
                                 const float *draft_probs, long long ld_probs, int B, int T, int V,
                                 float temperature, int top_k, float top_p, int do_sample, const float *uniform,
@@ -1021,6 +1042,12 @@ SMOL_API int smol_verify_drafts(const void *logits, long long ld, const int32_t 
     words |= reinterpret_cast<uintptr_t>(q);
   if ((words & 3u) || (reinterpret_cast<uintptr_t>(logits) & 1u) || !aligned16(ws)) return SMOL_ERR_MISALIGNED;
   if (ws_bytes < smol_verify_workspace_bytes(B, T)) return SMOL_ERR_WORKSPACE;
+  // the CTAs of a sequence read its inputs at their own time, some when another has written the outputs: one that
+  // took n_accepted for n_draft would choose another row than the rest, and leave while they read its sums
+  const size_t one = sizeof(int32_t) * (size_t)B, all = one * T;
+  if (overlaps({{n_accepted, one}, {next, one}, {p_draft, all}, {ws, smol_verify_workspace_bytes(B, T)}},
+               {{drafts, all}, {n_draft, one}, {greedy ? nullptr : uniform, all + one}}))
+    return SMOL_ERR_INVALID_ARG;
   int sms;
   const int rc = device_sms(&sms);
   if (rc) return rc;

@@ -610,7 +610,8 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, n_accepted: torch.
                   stream=None) -> None:
     """How many of each sequence's drafts [B, T] (int32) stay, and its next token, from the target's logits
     [B, T + 1, V] (bf16), the drafter's probabilities [B, T, V] (fp32; None: it chooses for certain) and
-    uniform [B, T + 1] (fp32): column i decides draft i, the last one draws the next token."""
+    uniform [B, T + 1] (fp32): column i decides draft i, the last one draws the next token.  No output may share
+    memory with another tensor of the call."""
     B, T = drafts.shape
     V = logits.shape[-1]
     ld = _row_pitch(logits, "logits", torch.bfloat16, B, T + 1, V)

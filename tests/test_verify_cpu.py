@@ -1,5 +1,6 @@
 """Host-side refusals of smol_verify_drafts (no GPU needed)."""
 import pytest
+import torch
 
 from llama_decoder_forward_gb300 import build as B
 
@@ -39,3 +40,23 @@ def test_refusals(S):
 def test_workspace_query(S):
     size = S.raw.smol_verify_workspace_bytes
     assert size(4, 3) >= 1024 + 16 * 8 and size(0, 3) == 0 and size(4, 0) == 0 and size(1 << 24, 1) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a call that is not refused must find no device: the addresses are made up")
+def test_outputs_on_inputs_are_refused(S):
+    """The CTAs of a sequence read its inputs at their own time: none may see another's outputs there."""
+    B, T = 4, 3
+    apart = dict(B=B, T=T, drafts=P, n_draft=P + 0x1000, uniform=P + 0x2000, n_accepted=P + 0x3000, next=P + 0x4000,
+                 p_draft=P + 0x5000, ws=P + 0x6000, logits=P + 0x100000, probs=P + 0x200000)
+    for out in ("n_accepted", "next", "p_draft", "ws"):
+        for other in ("drafts", "n_draft", "uniform", "n_accepted", "next", "p_draft"):
+            if other != out:
+                assert call(S, **dict(apart, **{out: apart[other]})) == -1, (out, other)
+    assert call(S, **dict(apart, next=apart["drafts"] + 4 * (B * T - 1))) == -1            # the last draft
+    assert call(S, **dict(apart, p_draft=apart["uniform"] - 4 * (B * T - 1))) == -1
+    assert call(S, **dict(apart, n_accepted=apart["uniform"] + 4 * (B * (T + 1) - 1))) == -1
+    assert S.last_launch_count() == 0
+    # side by side is apart, and a greedy call reads no random numbers: on to the launch, for which there is no device
+    for kw in (dict(next=apart["drafts"] + 4 * B * T), dict(n_accepted=apart["drafts"] - 4 * B),
+               dict(do_sample=0, p_draft=apart["uniform"])):
+        assert call(S, **dict(apart, **kw)) not in (-1, -3, -5), kw
