@@ -358,12 +358,13 @@ __global__ void __launch_bounds__(512, 1)
       if (!ok) {
         if (lane == 0) set_status(p.status, kPtTimeoutLoad);
         *abort_flag = 1;
-        // what this warp has asked for lands before the block's shared memory goes
-        bool done = units == 0 || mbar_wait_drain(q_full, (units - 1) & 1);
-        for (uint32_t k = n > SD ? n - SD : 0; k < n; ++k)
-          for (int w = 0; w < 2; ++w) done &= mbar_wait_drain(&c_full[(k % SD) * 2 + w], (k / SD) & 1);
-        if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
       }
+      // what this warp has asked for lands before the block's shared memory goes, also where it
+      // came to its end and the warps that would have waited gave up
+      bool done = units == 0 || mbar_wait_drain(q_full, (units - 1) & 1);
+      for (uint32_t k = n > SD ? n - SD : 0; k < n; ++k)
+        for (int w = 0; w < 2; ++w) done &= mbar_wait_drain(&c_full[(k % SD) * 2 + w], (k / SD) & 1);
+      if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
     }
   } else if (warp >= 8) {
     setmaxnreg_dec<C::R_LOAD>();
@@ -423,15 +424,16 @@ __global__ void __launch_bounds__(512, 1)
         if (!ok) {
           if (lane == 0) set_status(p.status, kPtTimeoutLoad);
           *abort_flag = 1;
-          // what this warp has asked for lands before the block's shared memory goes
-          bool done = units == 0 || mbar_wait_drain(q_full, (units - 1) & 1);
-          for (uint32_t n = nk > NST ? nk - NST : 0; n < nk; ++n) done &= mbar_wait_drain(&k_full[n % NST], (n / NST) & 1);
-          for (uint32_t n = nv > NST ? nv - NST : 0; n < nv; ++n) {
-            const uint32_t s = n % NST;
-            done &= (edges >> s) & 1 ? mbar_wait_drain(&v_raw[s], ((raw >> s) & 1) ^ 1) : mbar_wait_drain(&v_full[s], (n / NST) & 1);
-          }
-          if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
         }
+        // what this warp has asked for lands before the block's shared memory goes, also where it
+        // came to its end and the warps that would have waited gave up
+        bool done = units == 0 || mbar_wait_drain(q_full, (units - 1) & 1);
+        for (uint32_t n = nk > NST ? nk - NST : 0; n < nk; ++n) done &= mbar_wait_drain(&k_full[n % NST], (n / NST) & 1);
+        for (uint32_t n = nv > NST ? nv - NST : 0; n < nv; ++n) {
+          const uint32_t s = n % NST;
+          done &= (edges >> s) & 1 ? mbar_wait_drain(&v_raw[s], ((raw >> s) & 1) ^ 1) : mbar_wait_drain(&v_full[s], (n / NST) & 1);
+        }
+        if (!done && lane == 0) set_status(p.status, kPtTimeoutDrain);
       } else if (warp == 9) {
         // V of tiles that reach past what the unit's rows see: zeros there
         uint32_t raw = 0;                         // phase of each stage's v_raw
