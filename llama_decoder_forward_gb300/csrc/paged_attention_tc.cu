@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(512, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
   const uint64_t limit = p.wait_ns;
+  // a role's warp gives up as one: its lanes go on to instructions of the whole warp
+  auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, limit)); };
 
   griddep_launch_dependents();
   if (smem + C::USED > smem_raw + C::SMEM) {      // no room left by the alignment
@@ -234,10 +236,10 @@ __global__ void __launch_bounds__(512, 1)
       };
       // waits for what S of the next tile needs
       auto ready_s = [&]() {
-        if (!mbar_wait_bounded(&k_full[kst], kph, abort_flag, limit)) return false;
+        if (!wait(&k_full[kst], kph)) return false;
         f_next = sInfo[kst].flags;
         if (f_next & kPtNew) {
-          if (!mbar_wait_bounded(q_full, units & 1, abort_flag, limit)) return false;
+          if (!wait(q_full, units & 1)) return false;
           ++units;
         }
         tc_fence_after_sync();
@@ -264,11 +266,11 @@ __global__ void __launch_bounds__(512, 1)
       while (ok) {
         const int f = f_next;
         const bool last = f & kPtLast;
-        if (!mbar_wait_bounded(&v_full[vst], vph, abort_flag, limit)) { ok = false; break; }
+        if (!wait(&v_full[vst], vph)) { ok = false; break; }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (h == 0 || (f & kPtTwo)) {
-            if (!mbar_wait_bounded(&p_full[h], (h ? n1 : n0) & 1, abort_flag, limit)) { ok = false; break; }
+            if (!wait(&p_full[h], (h ? n1 : n0) & 1)) { ok = false; break; }
             tc_fence_after_sync();
             if (elect_one()) {
 #pragma unroll
@@ -332,8 +334,8 @@ __global__ void __launch_bounds__(512, 1)
         const bool last = it.left == 1;
         const int cur = pages;
         if (!last) pages = fetch_pages(nx);       // in use from the next round on
-        if (!mbar_wait_bounded(&c_empty[slot * 2], cph, abort_flag, limit)) { ok = false; break; }
-        if (!mbar_wait_bounded(&c_empty[slot * 2 + 1], cph, abort_flag, limit)) { ok = false; break; }
+        if (!wait(&c_empty[slot * 2], cph)) { ok = false; break; }
+        if (!wait(&c_empty[slot * 2 + 1], cph)) { ok = false; break; }
         if (lane < 8) notes[slot].page[lane] = cur;
         if (lane == 0) notes[slot].info = note_of(it, new_unit, in_unit);
         __syncwarp();                             // before lane 0's arrivals
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(512, 1)
         fetch(1, p.kv.v, cur);
         ++n;
         if (new_unit) {                           // Q behind the unit's first keys
-          if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
+          if (!wait(q_empty, (units & 1) ^ 1)) { ok = false; break; }
           if (lane == 0) load_q(it);
           __syncwarp();
           ++units;
@@ -396,17 +398,17 @@ __global__ void __launch_bounds__(512, 1)
           const bool last = it.left == 1;
           const int cur = pages;
           if (!last) pages = fetch_pages(nx);     // in use from the next round on
-          if (!mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit)) { ok = false; break; }
+          if (!wait(&k_empty[st], ph)) { ok = false; break; }
           if (lane == 0) sInfo[st] = note_of(it, new_unit, in_unit);   // before this lane's arrival in copy()
           copy(sK + st * C::TILE_BYTES, &tmK, &k_full[st], cur);
           ++nk;
           if (new_unit) {                         // Q behind the unit's first keys
-            if (!mbar_wait_bounded(q_empty, (units & 1) ^ 1, abort_flag, limit)) { ok = false; break; }
+            if (!wait(q_empty, (units & 1) ^ 1)) { ok = false; break; }
             if (lane == 0) load_q(it);
             __syncwarp();
             ++units;
           }
-          if (!mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit)) { ok = false; break; }
+          if (!wait(&v_empty[st], ph)) { ok = false; break; }
           const bool edge = it.lo > it.j * kTileK || it.hi < (it.j + 1) * kTileK;
           copy(sV + st * C::TILE_BYTES, &tmV, edge ? &v_raw[st] : &v_full[st], cur);
           ++nv;
@@ -439,12 +441,12 @@ __global__ void __launch_bounds__(512, 1)
         uint32_t raw = 0;                         // phase of each stage's v_raw
         ph = 0;
         while (true) {
-          if (!mbar_wait_bounded(&k_full[st], ph, abort_flag, limit)) { ok = false; break; }
+          if (!wait(&k_full[st], ph)) { ok = false; break; }
           const int f = sInfo[st].flags, valid = sInfo[st].valid;
           __syncwarp();
           if (lane == 0) mbar_arrive(&k_empty[st]);
           if (f & kPtEdge) {
-            if (!mbar_wait_bounded(&v_raw[st], (raw >> st) & 1, abort_flag, limit)) { ok = false; break; }
+            if (!wait(&v_raw[st], (raw >> st) & 1)) { ok = false; break; }
             raw ^= 1u << st;
             const int from = valid & 0xffff, to = valid >> 16, gone = 128 - (to - from);
             for (int i = lane; i < gone * 8 * NSUB; i += 32) {
@@ -497,18 +499,18 @@ __global__ void __launch_bounds__(512, 1)
         if (lane == 0) mbar_arrive(&c_empty[slot * 2 + which]);
       };
       while (true) {
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c_full[slot * 2], cph, abort_flag, limit))) { ok = false; break; }
+        if (!wait(&c_full[slot * 2], cph)) { ok = false; break; }
         const PtCodes &note = reinterpret_cast<const PtCodes *>(smem + C::OFF_NOTE)[slot];
         const int valid = note.info.valid, f = note.info.flags, page = note.page[lt / box];
         const bool edge = f & kPtEdge, in = page >= 0 && page < p.kv.P && lt >= (valid & 0xffff) && lt < valid >> 16;
         const long long at = in ? paged_slot(p.kv, page, note.info.x0 + lt, note.info.kvh) : 0;
         const float ks = in ? __ldg(p.kv.ks + at) : 0.f, vs = in ? __ldg(p.kv.vs + at) : 0.f;   // of key lt, for later
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&k_empty[st], ph, abort_flag, limit))) { ok = false; break; }
+        if (!wait(&k_empty[st], ph)) { ok = false; break; }
         if (lt == 0) sInfo[st] = note.info;
         convert(sK + st * C::TILE_BYTES, 0, valid, edge);
         mbar_arrive(&k_full[st]);
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&c_full[slot * 2 + 1], cph, abort_flag, limit))) { ok = false; break; }
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_empty[st], ph, abort_flag, limit))) { ok = false; break; }
+        if (!wait(&c_full[slot * 2 + 1], cph)) { ok = false; break; }
+        if (!wait(&v_empty[st], ph)) { ok = false; break; }
         // both scales go with V: the softmax reads them until it signals P, and V's
         // stage is free only after P V
         sSc[(st * 2) * 128 + lt] = ks * p.scale_log2;
@@ -544,7 +546,7 @@ __global__ void __launch_bounds__(512, 1)
     PagedMeta meta{};
     float m = -INFINITY, l = 0.f;
     while (true) {
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(&k_full[st], ph, abort_flag, limit))) { ok = false; break; }
+      if (!wait(&k_full[st], ph)) { ok = false; break; }
       const PtInfo &info = sInfo[st];
       const int f = info.flags, x0 = info.x0, first_at = info.first_at, rows = info.rows;
       const long long o_base = info.o_base;
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(512, 1)
           m = -INFINITY;
           l = 0.f;
         }
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_full[h], n & 1, abort_flag, limit))) { ok = false; break; }
+        if (!wait(&s_full[h], n & 1)) { ok = false; break; }
         tc_fence_after_sync();
         if (work) {
           uint32_t sv[128];
@@ -575,7 +577,7 @@ __global__ void __launch_bounds__(512, 1)
           for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sv[32 * c]));
           tmem_ld_wait();
           if constexpr (FP8) {
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&v_full[st], ph, abort_flag, limit))) { ok = false; break; }
+            if (!wait(&v_full[st], ph)) { ok = false; break; }
             // scores times their keys' scales (which hold scale * log2 e already)
             const float4 *sc = reinterpret_cast<const float4 *>(sSc + (st * 2) * 128);
 #pragma unroll
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(512, 1)
         ++n;
         if (f & kPtUnitLast) {
           // ---- the unit (or this CTA's part of it) is done: out, or a partial result
-          if (!__all_sync(0xffffffffu, mbar_wait_bounded(&o_full[h], n_units & 1, abort_flag, limit))) { ok = false; break; }
+          if (!wait(&o_full[h], n_units & 1)) { ok = false; break; }
           ++n_units;
           tc_fence_after_sync();
           if (work) {
