@@ -296,18 +296,19 @@ __global__ void __launch_bounds__(AtCfg<HD, GH>::THREADS, 1)
       }
     }
     if (lane == 0) {
-      // wait (bounded) until every copy this thread issued has landed
-      if (!mbar_wait_drain(q_full, 0)) at_status(p.status, kAtTimeoutDrain);
       if (!ok) {
         at_status(p.status, kAtTimeoutLoad);
         *abort_flag = 1;
-        for (int i = nk > kNST ? nk - kNST : 0; i < nk; ++i)
-          if (!mbar_wait_drain(&k_full[i % kNST], (uint32_t)((i / kNST) & 1)))
-            at_status(p.status, kAtTimeoutDrain);
-        for (int i = nv > kNST ? nv - kNST : 0; i < nv; ++i)
-          if (!mbar_wait_drain(&v_full[i % kNST], (uint32_t)((i / kNST) & 1)))
-            at_status(p.status, kAtTimeoutDrain);
       }
+      // wait (bounded) until every copy this thread issued has landed, also where
+      // it came to its end and the warps that read the last tiles gave up
+      if (!mbar_wait_drain(q_full, 0)) at_status(p.status, kAtTimeoutDrain);
+      for (int i = nk > kNST ? nk - kNST : 0; i < nk; ++i)
+        if (!mbar_wait_drain(&k_full[i % kNST], (uint32_t)((i / kNST) & 1)))
+          at_status(p.status, kAtTimeoutDrain);
+      for (int i = nv > kNST ? nv - kNST : 0; i < nv; ++i)
+        if (!mbar_wait_drain(&v_full[i % kNST], (uint32_t)((i / kNST) & 1)))
+          at_status(p.status, kAtTimeoutDrain);
     }
   } else if (warp == 1) {
     if (lane == 0) {

@@ -200,3 +200,20 @@ def test_model_attention_wait_gives_up(S):
                           inp.ids.numpy().astype(np.int64))
     got = np32(logits)
     assert cosine(got, ref) >= LOGITS_COS_MIN and max_abs(got, ref) <= LOGITS_MAX_ABS
+
+
+@pytest.mark.parametrize("T", [40, 128, 200])
+def test_attention_of_few_tiles_wait_gives_up(S, T):
+    # as test_attention_wait_gives_up, with no more key tiles than stages: the loader has asked for all of them and is at
+    # its end when the warps that read them give up, and waits for its copies all the same
+    wl, inp, dev, cfg, packed, ws = _block(S, T=T)
+    x = dev.x.float().contiguous()
+    out = torch.empty_like(x)
+    try:
+        S.set_wait_limit_ns(1)
+        for _ in range(3):
+            S.block_forward(cfg, packed, 0, x, out, ws)
+            assert S.workspace_status(ws) in (S.OK, S.ERR_TIMEOUT)
+    finally:
+        S.set_wait_limit_ns(0)
+    _normal_block_call(S, wl, inp, dev, cfg, packed, ws)
