@@ -560,10 +560,11 @@ int smol_last_launch_count(void);
 /* For tests of the failure path only (no counterpart on the pages): the limit,
  * in nanoseconds, of the bounded waits of the prefill and paged attention kernels in
  * launches made from now on by any thread (0 restores the default of 1 s).  A
- * limit shorter than the kernel's own latencies makes a wait give up: the
- * kernel drains the copies and MMAs it issued (those drains keep the 1 s
- * limit), records SMOL_ERR_TIMEOUT in the status word and returns, leaving its
- * outputs undefined; the device stays usable. */
+ * limit shorter than the kernel's own latencies makes a wait give up (in the
+ * prefill attention after some 36 us at the earliest): the kernel drains the
+ * copies and MMAs it issued (those drains keep the 1 s limit), records
+ * SMOL_ERR_TIMEOUT in the status word and returns, leaving its outputs
+ * undefined; the device stays usable. */
 void smol_set_wait_limit_ns(unsigned long long ns);
 
 /* ---------------------------------------------------------------------------

@@ -256,7 +256,10 @@ __global__ void __launch_bounds__(512, 1)
           kph ^= 1;
         }
       };
-      ok = ready_s();
+      // the one wait that keeps a short limit, outside the loop; the other roles then see the abort
+      // flag.  (Its code at all twenty waits: 24 packed chunks 332 to 347 us for 288 to 300, 2048
+      // tokens on 32,000 484 for 451, for the instructions to fetch; in the issuer's loop 462.)
+      ok = __all_sync(0xffffffffu, mbar_wait_limit(&k_full[0], 0, abort_flag, limit)) && ready_s();
       if (ok) {
         issue_s(0);
         if (f_next & kPtTwo) issue_s(1);

@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
   constexpr bool PERM = FP8 && HD == 128;
   auto key_of = [](int n) { return PERM ? (n & ~7) | ((n & 7) >> 1) | ((n & 1) << 2) : n; };
   while (true) {
-    if (alive && !__all_sync(0xffffffffu, mbar_wait_bounded(&full[stage], phase, abort_flag, p.wait_ns))) {
+    if (alive && !__all_sync(0xffffffffu, mbar_wait_limit(&full[stage], phase, abort_flag, p.wait_ns))) {
       // give up: what was asked for has a second to land, and the rest is done without
       set_status(p.status, kPdTimeout);
       *abort_flag = 1;
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(PdCfg<HD, FP8, NR>::THREADS, 1)
     const uint32_t q_s = smem_u32(smem + C::OFF_Q + (units & 1) * C::Q_BYTES);
     if (flags & kPdFirst) {
       // ---- a new unit
-      if (alive && !__all_sync(0xffffffffu, mbar_wait_bounded(&q_full[units & 1], (units >> 1) & 1, abort_flag, p.wait_ns))) {
+      if (alive && !__all_sync(0xffffffffu, mbar_wait_limit(&q_full[units & 1], (units >> 1) & 1, abort_flag, p.wait_ns))) {
         set_status(p.status, kPdTimeout);
         *abort_flag = 1;
         alive = false;

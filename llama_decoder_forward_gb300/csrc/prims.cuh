@@ -153,6 +153,22 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
   return done != 0;
 }
 
+// As mbar_wait_bounded, and a short limit is kept: a try suspends its thread for 4 us
+// whatever its hint, so that wait gives up after nine of them, 36 us, at the earliest,
+// longer than any wait of a kernel that does not overlap another.  Below that the
+// barrier is looked at without suspension.
+constexpr uint64_t kShortLimitNs = 40000;
+__device__ __forceinline__ bool mbar_wait_limit(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                                uint64_t limit_ns) {
+  if (limit_ns >= kShortLimitNs) return mbar_wait_bounded(bar, parity, abort_flag, limit_ns);
+  const uint64_t t0 = global_timer_ns();
+  do {
+    if (mbar_test_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+  } while (global_timer_ns() - t0 <= limit_ns);
+  return false;
+}
+
 // ---------------------------------------------------------------- dependent launch
 // Programmatic dependent launch: a kernel launched with the programmatic
 // stream-serialization attribute may start before its predecessor in the

@@ -629,8 +629,8 @@ def verify_drafts(logits: torch.Tensor, drafts: torch.Tensor, n_accepted: torch.
 
 
 def set_wait_limit_ns(ns: int) -> None:
-    """Failure-path tests only: bounded-wait limit of the prefill attention
-    kernel for later launches (0 restores the default of 1 s)."""
+    """Failure-path tests only: bounded-wait limit of the prefill and paged
+    attention kernels for later launches (0 restores the default of 1 s)."""
     _lib.smol_set_wait_limit_ns(int(ns))
 
 

@@ -105,3 +105,69 @@ def test_the_model_leaves_the_pages_of_a_negative_position(S, kind):
     assert S.workspace_status(ws) == S.ERR_INPUT
     table = cache.tensors[2].tolist()
     assert unchanged(cache, before, [(table[1][x // 16], x % 16) for x in range(20, 23)])
+
+
+# ---------------------------------------------------------------- waits that give up
+def gives_up(S, kind, hd, T, lens):
+    """A call under a limit of a nanosecond, three times: its statuses.  What did not give up is right, and the
+    workspace serves the call behind each."""
+    cache = small(S, kind, T, [n + T for n in lens], hd=hd)
+    q = randn(len(lens), T, 6, hd, seed=4, scale=2.0)
+    chunk, ws = S.Chunk(len(lens), T, i32(lens)), S.alloc_paged_workspace(cache, 6, len(lens), T)
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    S.paged_attention(cache, 0, chunk, q, want, ws)
+    assert S.workspace_status(ws) == S.OK
+    flush, reports = torch.empty(256 << 20, dtype=torch.uint8, device="cuda"), []
+    for _ in range(3):
+        flush.fill_(1)                                # the pages come from memory, not from L2
+        try:
+            S.set_wait_limit_ns(1)
+            S.paged_attention(cache, 0, chunk, q, out, ws)
+            reports.append(S.workspace_status(ws))
+        finally:
+            S.set_wait_limit_ns(0)
+        assert reports[-1] == S.ERR_TIMEOUT or (reports[-1] == S.OK and torch.equal(out, want))
+        S.paged_attention(cache, 0, chunk, q, out, ws)
+        assert S.workspace_status(ws) == S.OK and torch.equal(out, want)
+    return reports
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("T", [40, 100])
+@pytest.mark.parametrize("lens", [[900, 6000, 31] + [5000] * 13, [40, 0, 200]])
+def test_many_rows_keep_a_short_wait_limit(S, kind, hd, T, lens):
+    """Pieces of many key tiles, and of one or two, whose copies are all asked for when the first wait gives up."""
+    assert gives_up(S, kind, hd, T, lens) == 3 * [S.ERR_TIMEOUT]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_few_rows_keep_a_short_wait_limit(S, kind, hd):
+    """The first keys of 150 MB, which all the SMs ask for at once.  A kernel whose steps take longer than its copies
+    (32 rows over codes) never waits, and a small call's copies may be there in time: those are right instead."""
+    reports = []
+    for T in (1, 3, 6, 8):
+        reports += gives_up(S, kind, hd, T, [6000] * (48 if kind == "bf16" else 96))
+        gives_up(S, kind, hd, T, [40, 0, 200])
+    assert reports.count(S.ERR_TIMEOUT) >= 3, reports
+
+
+def test_the_model_over_pages_reports_a_wait_that_gave_up(S):
+    lengths = [3, 900, 40]
+    wl, _, _, cfg, packed, cache, ids = case(S, 13, lengths, 30)
+    ws = S.prefill_paged_workspace(cfg, cache, 3, 30)
+    for T in (30, 1):
+        logits, want = (torch.zeros(3, T, wl.vocab, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        call = lambda to: S.prefill_paged(cfg, packed, ids[:, :T].contiguous().cuda(), cache, i32(lengths), to, ws)
+        call(want)
+        assert S.workspace_status(ws) == S.OK
+        try:
+            S.set_wait_limit_ns(1)
+            call(logits)
+            assert S.workspace_status(ws) == S.ERR_TIMEOUT
+        finally:
+            S.set_wait_limit_ns(0)
+        call(logits)
+        assert S.workspace_status(ws) == S.OK
+        assert cosine(np32(logits), np32(want)) >= LOGITS_COS_MIN and max_abs(np32(logits), np32(want)) <= 2 * LOGITS_MAX_ABS
