@@ -574,14 +574,14 @@ enum {
   SMOL_K_EMBED = 0,      /* embedding gather + row statistics            */
   SMOL_K_ROWSTATS = 1,   /* block input row statistics + f16 copy         */
   SMOL_K_QKV = 2,        /* RMSNorm + QKV GEMM + RoPE                     */
-  SMOL_K_ATTN = 3,       /* causal GQA flash attention                    */
+  SMOL_K_ATTN = 3,       /* causal GQA flash attention; paged, many rows  */
   SMOL_K_OPROJ = 4,      /* O GEMM + residual                             */
   SMOL_K_GATEUP = 5,     /* RMSNorm + gate/up GEMM + SwiGLU               */
   SMOL_K_DOWN = 6,       /* down GEMM + residual                          */
   SMOL_K_HEAD = 7,       /* final RMSNorm + tied lm_head GEMM             */
-  SMOL_K_DEC_ATTN = 8,   /* decode attention over the KV cache            */
+  SMOL_K_DEC_ATTN = 8,   /* decode attention over the cache; paged, few rows */
   SMOL_K_OTHER = 9,      /* packing and bookkeeping kernels               */
-  SMOL_K_SAMPLE = 10,    /* next-token choice (smol_sample)               */
+  SMOL_K_SAMPLE = 10,    /* next-token choice (smol_sample), verification */
   SMOL_K_COUNT = 11
 };
 /* From now on (this host thread), every launch whose kind bit is set in

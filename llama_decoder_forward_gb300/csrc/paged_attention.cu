@@ -129,7 +129,8 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64;
   p.bk_shift = rows >= 128 || !(h64 || f8) ? 7 : 8;
   cudaError_t e;
-  prof_before(SMOL_K_DEC_ATTN, st);
+  const int kind = rows >= 128 ? SMOL_K_ATTN : SMOL_K_DEC_ATTN;
+  prof_before(kind, st);
   if (rows >= 128) {
     e = launch_paged_tiles(p, st);
   } else if (h64) {
@@ -137,13 +138,13 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   } else {
     e = f8 ? launch_few<128, true>(rows, p, st) : launch_few<128, false>(rows, p, st);
   }
-  prof_after(SMOL_K_DEC_ATTN, st);
+  prof_after(kind, st);
   if (e != cudaSuccess) return e;
   *launches = 1;
   if (rows < 128) return cudaSuccess;             // that kernel combines its parts itself
-  prof_before(SMOL_K_OTHER, st);
+  prof_before(kind, st);
   e = h64 ? launch_combine<64>(p, rows, st) : launch_combine<128>(p, rows, st);
-  prof_after(SMOL_K_OTHER, st);
+  prof_after(kind, st);
   if (e == cudaSuccess) *launches = 2;
   return e;
 }

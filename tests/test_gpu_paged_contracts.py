@@ -171,3 +171,15 @@ def test_the_model_over_pages_reports_a_wait_that_gave_up(S):
         call(logits)
         assert S.workspace_status(ws) == S.OK
         assert cosine(np32(logits), np32(want)) >= LOGITS_COS_MIN and max_abs(np32(logits), np32(want)) <= 2 * LOGITS_MAX_ABS
+
+
+# ---------------------------------------------------------------- the launch timer
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_the_timer_files_chunks_of_prompts_under_prefill_attention(S, kind):
+    cache = small(S, kind, 100, [300, 40])
+    ws = S.alloc_paged_workspace(cache, 6, 2, 100)
+    for T, want in ((1, [S.K_DEC_ATTN]), (4, [S.K_DEC_ATTN]), (100, [S.K_ATTN, S.K_ATTN])):
+        q = randn(2, T, 6, 64, seed=T)
+        S.profile_begin((1 << len(S.KERNEL_KINDS)) - 1, 8)
+        S.paged_attention(cache, 0, S.Chunk(2, T, i32([20, 30])), q, torch.empty_like(q), ws)
+        assert [k for k, _ in S.profile_end()] == want
