@@ -535,9 +535,12 @@ int smol_prefill_paged(const smol_config *cfg, const void *packed, const int32_t
  *   ws          >= smol_verify_workspace_bytes(B, T) bytes, zeroed once.
  * The outputs and ws overlap neither one another nor an input
  * (SMOL_ERR_INVALID_ARG where one meets drafts, n_draft or uniform).
- * Probabilities are held to about 2^-43 of the row's largest and summed exactly
- * (a token below 2^-45 of the largest counts as impossible), so the choice is
- * the definition's except where u lies within 1e-11 of a border.
+ * A token's weight is a whole number of units of 2^-44 of the row's largest: off
+ * by half a unit (rarely by up to three), and 0 below half a unit.  The sums are
+ * exact, so the choice is the definition's except where u lies within the sum of
+ * the tokens' own errors of a border: some 1e-11 of the whole as a rule; up to
+ * V * 2^-45 (4e-9 at V = 131072) where all tokens share one error, as equal
+ * logits far below the largest do, and six times that in no case exceeded.
  * V <= 2^19, T <= 512.  Two kernel launches on `stream`.
  * ------------------------------------------------------------------------- */
 size_t smol_verify_workspace_bytes(int B, int T);

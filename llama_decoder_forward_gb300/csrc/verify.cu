@@ -13,7 +13,9 @@
 // definition.  Here a token's mass is e = 2^((l - l_max) log2(e) / temperature) as
 // an integer in units of 2^-44, from an exponential good to some 2^-44 (mass_of),
 // and every sum is a 64-bit integer: exact, and the same in any order.  The
-// borders are then off by less than 1e-11 of the whole.
+// borders are then off by the masses' own errors only: some 1e-11 of the whole where
+// those have both signs, up to V 2^-45 (4e-9 at V = 131072) where a long tail of equal
+// values shares one, or falls below half a unit altogether.
 //
 // Two launches.
 //   rows    one CTA for each target row, which it reads one to three times (from L2

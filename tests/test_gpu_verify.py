@@ -294,3 +294,33 @@ def test_tensors_of_another_device_are_refused(S, monkeypatch):
     monkeypatch.undo()
     torch.cuda.synchronize()
     assert int(acc) == -9 and int(nxt) == -9
+
+
+@pytest.mark.parametrize("top", [10.0, 27.75, 31.0, 31.5])
+def test_a_long_tail_of_one_error(S, top):
+    """One likely token behind (V - 1) equal ones, whose masses are rounded alike (31.0: to twice of what they are,
+    nearly) or fall below half a unit (31.5).  Every draw's border is within the header's V * 2^-45 of the definition's."""
+    V, B = 128257, 64
+    logits = torch.zeros(B, 2, V, device="cuda", dtype=torch.bfloat16)
+    logits[:, :, V - 1] = top
+    tail = (V - 1) / (V - 1 + math.exp(top))                # what the equal tokens have of the whole
+    u = torch.rand(B, 2, generator=torch.Generator("cuda").manual_seed(9), device="cuda")
+    u[:32, 1] = (torch.linspace(0.0, 2.0, 32, device="cuda") * tail).clamp_max(1 - 2.0 ** -24)   # among them, and around their end
+    drafts = torch.full((B, 1), V - 1, dtype=torch.int32, device="cuda")
+    acc, nxt = (torch.full((B,), -9, dtype=torch.int32, device="cuda") for _ in range(2))
+    pd, ws = torch.zeros(B, 1, device="cuda"), S.alloc_verify_workspace(B, 1)
+    S.verify_drafts(logits, drafts, acc, nxt, ws, uniform=u, p_draft=pd)
+    assert S.workspace_status(ws) == S.OK
+    bound = V * 2.0 ** -45
+    p = 1.0 - tail
+    assert bool(((pd.double() - p).abs() <= 2.0 ** -24 + bound).all())
+    for b in range(B):
+        u0, u1, x = float(u[b, 0]), float(u[b, 1]), int(nxt[b])
+        if abs(u0 - p) > bound:
+            assert int(acc[b]) == int(u0 < p)
+        if int(acc[b]) == 1:                                # drawn from the row
+            below, upto = tail * x / (V - 1), 1.0 if x == V - 1 else tail * (x + 1) / (V - 1)
+        else:                                               # the draft is gone: drawn from the equal ones
+            assert x < V - 1
+            below, upto = x / (V - 1), (x + 1) / (V - 1)
+        assert below - bound <= u1 < upto + bound, (b, x, u1)
