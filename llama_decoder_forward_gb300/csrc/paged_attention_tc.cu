@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(512, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31, cta = blockIdx.x;
   const uint64_t limit = p.wait_ns;
-  // a role's warp gives up as one: its lanes go on to instructions of the whole warp
+  // the other roles' warps give up as one: their lanes go on to instructions of the whole warp
   auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, limit)); };
 
   griddep_launch_dependents();
@@ -212,8 +212,10 @@ __global__ void __launch_bounds__(512, 1)
 
   if (warp >= 12) {
     setmaxnreg_dec<C::R_MMA>();
-    if (warp == 12) {
-      // ---------------------------------------------------------------- MMA issuer
+    if (warp == 12 && elect_one()) {
+      // ---------------------------------------------------------------- MMA issuer: one thread, which
+      // gives up by itself (as a warp with votes: 2048 tokens on 32,000 449 us, so 426)
+      auto wait = [&](uint64_t *bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, abort_flag, limit); };
       constexpr uint32_t kIdS = idesc_bf16_f32(128, 128, false), kIdO = idesc_bf16_f32(128, HD, true);
       const uint64_t dq = sdesc_kmajor_sw128(smem_u32(sQ)), dk = sdesc_kmajor_sw128(smem_u32(sK));
       const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(sV), 128 * 128);
@@ -223,16 +225,13 @@ __global__ void __launch_bounds__(512, 1)
       uint32_t kph = 0, vph = 0;
       int f_next = 0;                             // flags of the tile whose S is issued next
       auto issue_s = [&](int h) {
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint64_t a = dq + (((k >> 2) * (NQ * 128 * 128) + h * (128 * 128) + (k & 3) * 32) >> 4);
-            const uint64_t b = dk + ((kst * C::TILE_BYTES + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
-            umma_f16(tmem + kColS + h * 128, a, b, kIdS, k > 0);
-          }
-          umma_commit(&s_full[h]);
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint64_t a = dq + (((k >> 2) * (NQ * 128 * 128) + h * (128 * 128) + (k & 3) * 32) >> 4);
+          const uint64_t b = dk + ((kst * C::TILE_BYTES + (k >> 2) * (128 * 128) + (k & 3) * 32) >> 4);
+          umma_f16(tmem + kColS + h * 128, a, b, kIdS, k > 0);
         }
-        __syncwarp();
+        umma_commit(&s_full[h]);
       };
       // waits for what S of the next tile needs
       auto ready_s = [&]() {
@@ -246,11 +245,8 @@ __global__ void __launch_bounds__(512, 1)
         return true;
       };
       auto done_s = [&]() {                       // S of that tile is issued for each query tile
-        if (elect_one()) {
-          umma_commit(&k_empty[kst]);
-          if (f_next & kPtUnitLast) umma_commit(q_empty);
-        }
-        __syncwarp();
+        umma_commit(&k_empty[kst]);
+        if (f_next & kPtUnitLast) umma_commit(q_empty);
         if (++kst == NST) {
           kst = 0;
           kph ^= 1;
@@ -259,7 +255,7 @@ __global__ void __launch_bounds__(512, 1)
       // the one wait that keeps a short limit, outside the loop; the other roles then see the abort
       // flag.  (Its code at all twenty waits: 24 packed chunks 332 to 347 us for 288 to 300, 2048
       // tokens on 32,000 484 for 451, for the instructions to fetch; in the issuer's loop 462.)
-      ok = __all_sync(0xffffffffu, mbar_wait_limit(&k_full[0], 0, abort_flag, limit)) && ready_s();
+      ok = mbar_wait_limit(&k_full[0], 0, abort_flag, limit) && ready_s();
       if (ok) {
         issue_s(0);
         if (f_next & kPtTwo) issue_s(1);
@@ -275,14 +271,11 @@ __global__ void __launch_bounds__(512, 1)
           if (h == 0 || (f & kPtTwo)) {
             if (!wait(&p_full[h], (h ? n1 : n0) & 1)) { ok = false; break; }
             tc_fence_after_sync();
-            if (elect_one()) {
 #pragma unroll
-              for (int k = 0; k < 8; ++k)         // the unit's first tile: O starts at zero
-                umma_f16_tmem_a(tmem + kColO + h * HD, tmem + kColS + h * 128 + k * 8, dv + ((vst * C::TILE_BYTES + k * 2048) >> 4),
-                                kIdO, k > 0 || !(f & kPtNew));
-              if (f & kPtUnitLast) umma_commit(&o_full[h]);
-            }
-            __syncwarp();
+            for (int k = 0; k < 8; ++k)           // the unit's first tile: O starts at zero
+              umma_f16_tmem_a(tmem + kColO + h * HD, tmem + kColS + h * 128 + k * 8, dv + ((vst * C::TILE_BYTES + k * 2048) >> 4),
+                              kIdO, k > 0 || !(f & kPtNew));
+            if (f & kPtUnitLast) umma_commit(&o_full[h]);
             if (h) ++n1;
             else ++n0;
           }
@@ -292,8 +285,7 @@ __global__ void __launch_bounds__(512, 1)
           }
         }
         if (!ok) break;
-        if (elect_one()) umma_commit(&v_empty[vst]);
-        __syncwarp();
+        umma_commit(&v_empty[vst]);
         if (++vst == NST) {
           vst = 0;
           vph ^= 1;
@@ -307,8 +299,7 @@ __global__ void __launch_bounds__(512, 1)
       }
       if (any) {
         // every MMA issued is done before shared and tensor memory go
-        if (elect_one()) umma_commit(drain);
-        __syncwarp();
+        umma_commit(drain);
         if (!mbar_wait_drain(drain, 0)) set_status(p.status, kPtTimeoutDrain);
       }
     }
@@ -708,6 +699,7 @@ __global__ void __launch_bounds__(512, 1)
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 12) {
+    __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
