@@ -464,7 +464,8 @@ int smol_paged_read(const smol_paged_cache *cache, const smol_chunk *chunk, cons
  * drafted continuation, large T a chunk of a prompt; sequences of all three may
  * share a call.  A sequence with no rows costs and writes nothing.
  *   layer    0 .. cache->n_layers - 1.
- *   q, out   bf16 rows of n_heads heads; out must not overlap q or itself.
+ *   q, out   bf16 rows of n_heads heads; out must not overlap q or itself, and
+ *            strides of axes of more than one entry are at least head_dim.
  *   scale    of the scores; 0 means 1 / sqrt(head_dim).
  *   ws       >= smol_paged_workspace_bytes(cache, n_heads, B, T) bytes, zeroed
  *            once; calls that may run at the same time need one each.
@@ -485,7 +486,9 @@ int smol_paged_attention(const smol_paged_cache *cache, int layer, const smol_ch
  * post-RoPE keys and values are written to their pages (smol_paged_append) and
  * the attention reads them there with the earlier ones (smol_paged_attention);
  * NoPE blocks and windows apply as in the other calls.  T = 1 is a decode step, T
- * of a few a drafted continuation for smol_verify_drafts.
+ * of a few a drafted continuation for smol_verify_drafts.  Queries and attention
+ * weights are rounded to bf16, the type of their products with the pages' values
+ * (2^-8 relative; smol_prefill_with_cache holds both in f16).
  *   ids      device int32 [B, T].
  *   cache    of cfg's layers, kv heads and head_dim; its pages are written.
  *   pos      device int32 [B]: tokens of sequence b already in its pages, each in

@@ -57,9 +57,9 @@ cudaError_t launch_few(const PagedAttnParams &p, cudaStream_t st) {
 }
 
 // The most rows that the few-rows kernel takes as one unit (32 sequences of 2000 to 8191
-// cached tokens, by it and by the many-rows kernel): bf16 of hd 64 24 rows 43 and 48 us,
-// 30 rows 50 and 48; of hd 128 16 rows 68 and 71, 20 rows 84 and 71; e4m3 of hd 128 20
-// rows 75 and 157, of hd 64 27 rows 51 and 90.
+// cached tokens, by it and by the many-rows kernel): bf16 of hd 64 24 rows 42 and 48 us,
+// 30 rows 50 and 48; of hd 128 16 rows 70 and 73, 20 rows 84 and 74; e4m3 of hd 128 20
+// rows 75 and 160, of hd 64 27 rows 53 and 90.
 constexpr int few_rows_most(int hd, bool e4m3) { return e4m3 ? 32 : hd == 64 ? 24 : 16; }
 
 template <int HD, bool FP8>
@@ -108,8 +108,8 @@ bool paged_map_pages(CUtensorMap *map, const PagedKv &kv, const void *base, int 
 
 // Rows of a unit: the tile of the kernel that takes the call.  e4m3 chunks of up to 48
 // rows go to the few-rows kernel in two halves, which read the same keys (4 heads, 9
-// tokens: 129 us, by the many-rows kernel 157; 3 heads, 16 tokens 72 and 91; of 64 rows
-// 192 and 162).
+// tokens: 129 us, by the many-rows kernel 163; 3 heads, 16 tokens 73 and 92; of 64 rows
+// 173 and 167).
 static int unit_rows(int G, int T, int hd, bool e4m3) {
   const long long r = (long long)T * G;
   if (r <= few_rows_most(hd, e4m3)) return static_cast<int>((r + 7) / 8 * 8);
@@ -127,7 +127,7 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p0, int sms, cudaStrea
   const int rows = unit_rows(p.G, p.c.T, p.kv.hd, p.kv.e4m3);
   p.tt = rows / p.G;
   const bool f8 = p.kv.e4m3, h64 = p.kv.hd == 64;
-  p.bk_shift = rows >= 128 || !(h64 || f8) ? 7 : 8;
+  p.bk_shift = 7;                                 // the many-rows kernel's tiles; the other one has its own
   cudaError_t e;
   const int kind = rows >= 128 ? SMOL_K_ATTN : SMOL_K_DEC_ATTN;
   prof_before(kind, st);

@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(512, 1)
                 const float4 v4 = vsc[half * 16 + (q >> 1)];
                 x = (q & 1) ? fmul2(x.x, x.y, v4.z, v4.w) : fmul2(x.x, x.y, v4.x, v4.y);
               }
-              pk[q] = pack_bf16x2(x.x, x.y);      // the tensor core's operand type: off by 2^-9 at most
+              pk[q] = pack_bf16x2(x.x, x.y);      // the tensor core's operand type: off by 2^-8 of the value at most
             }
             tmem_st32(tS + half * 32, pk);
           }

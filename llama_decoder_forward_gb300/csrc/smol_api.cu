@@ -885,7 +885,7 @@ SMOL_API int smol_paged_read(const smol_paged_cache *cache, const smol_chunk *ch
 }
 
 namespace {
-constexpr int kPagedMaxSeqs = 4096;   // sequences of one attention call (its schedule is held on chip)
+constexpr int kPagedMaxSeqs = 4096;   // sequences of one attention call (each CTA goes through them all before it begins)
 
 bool paged_heads_ok(const smol_paged_cache *c, int n_heads) {
   return n_heads > 0 && n_heads % c->n_kv_heads == 0 && n_heads / c->n_kv_heads <= 8;
